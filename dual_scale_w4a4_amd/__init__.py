@@ -19,6 +19,8 @@ LIB_PATH = os.path.join(_HERE, "libdq.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "dq.h")
 
 FMT = {"int4_bf16": 0, "mxint4": 1, "mxfp4": 2, "nvfp4": 3}
+ACT_FMT = {**FMT, "mxfp8": 4}  # formats of the MLP operators (include/dq_mlp.h)
+ACTIVATION = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 DTYPE = {"f32": 0, "bf16": 1}
 STATUS = {0: "DQ_OK", 1: "DQ_ERR_ARG", 2: "DQ_ERR_UNSUPPORTED", 3: "DQ_ERR_NONFINITE",
           4: "DQ_ERR_RANGE", 5: "DQ_ERR_WORKSPACE", 6: "DQ_ERR_HIP", 7: "DQ_ERR_INTERNAL"}
@@ -102,6 +104,20 @@ def lib() -> ctypes.CDLL:
         L.dq_gemm_pack_weights.restype = I
         L.dq_gemm_mx_packed.argtypes = [P, P, I64, I64, P, P, P, I64, I, P, P]
         L.dq_gemm_mx_packed.restype = I
+        D, F = ctypes.c_double, ctypes.c_float
+        L.dq_norm_quantize_act_async.argtypes = [P, I, P, P, I64, I64, P, I, D, P, I, I, F, P, P,
+                                                 P, P]
+        L.dq_norm_quantize_act_async.restype = I
+        L.dq_norm_quantize_act.argtypes = [P, I, P, P, I64, I64, P, I, D, P, I, I, F, P, P, P, SZ,
+                                           P]
+        L.dq_norm_quantize_act.restype = I
+        L.dq_gemm_mx_epilogue.argtypes = [P, P, I, I64, I64, P, P, P, P, I, P, I64, I, P, P]
+        L.dq_gemm_mx_epilogue.restype = I
+        L.dq_gated_mx.argtypes = [P, P, I, I64, I64, P, P, P, P, P, P, I, I64, I, P, P]
+        L.dq_gated_mx.restype = I
+        L.dq_gated_mx_quantized.argtypes = [P, P, I, I64, I64, P, P, P, P, P, P, I, I64, P, I, P, P,
+                                            P]
+        L.dq_gated_mx_quantized.restype = I
         L.dq_status_str.argtypes = [I]
         L.dq_status_str.restype = ctypes.c_char_p
         _lib = L
@@ -427,6 +443,227 @@ def gemm_mx_packed(act_codes, act_scales, packed, a=None, out_dtype: str = "bf16
     if st != 0:
         raise DQError(st, "dq_gemm_mx_packed")
     return y
+
+
+# ------------------------------------------------------------------ the MLP operators
+# (include/dq_mlp.h) Every tensor lies on one device; the call runs on `stream`, or on that
+# device's current stream, whichever device is current.
+
+
+def _call(dev, stream, f, *args):
+    """f(*args, stream) with ``dev`` current."""
+    torch = _torch()
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    if s.device != dev:
+        raise ValueError("stream belongs to another device than the tensors")
+    if torch.cuda.current_device() == dev.index:
+        return f(*args, s.cuda_stream)
+    with torch.cuda.device(dev):
+        return f(*args, s.cuda_stream)
+
+
+def _empty(shape, dtype, dev, stream):
+    """An uninitialized tensor that belongs to the stream it will be written on."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _arr(name, t, dev, dtype, shape, optional=False):
+    """The address of a dense tensor after its checks (None for a missing optional one)."""
+    if t is None and optional:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"on {dev}")
+    return t.data_ptr()
+
+
+def _out_dtype(out_dtype):
+    torch = _torch()
+    if out_dtype not in DTYPE:
+        raise ValueError("out_dtype is 'bf16' or 'f32'")
+    return torch.bfloat16 if out_dtype == "bf16" else torch.float32
+
+
+def act_outputs(X, fmt: str, group: int):
+    """The (codes, scales) tensors that quantizing X (tokens x cols) writes: codes tokens x
+    cols/2 uint8 (MXFP8: tokens x cols), scales tokens x cols/group (int16 holding bf16 bits for
+    int4_bf16, else uint8)."""
+    torch = _torch()
+    if fmt not in ACT_FMT:
+        raise ValueError(f"unknown format {fmt!r}")
+    tokens, cols = X.shape
+    codes = torch.empty((tokens, cols if fmt == "mxfp8" else cols // 2), dtype=torch.uint8,
+                        device=X.device)
+    sdt = torch.int16 if fmt == "int4_bf16" else torch.uint8
+    return codes, torch.empty((tokens, cols // group), dtype=sdt, device=X.device)
+
+
+def _norm_args(X, fmt, group, codes, scales, weight, residual, residual_out, b, eps, g):
+    torch = _torch()
+    dt = _check_w(X)
+    dev, (tokens, cols) = X.device, X.shape
+    if fmt not in ACT_FMT:
+        raise ValueError(f"unknown format {fmt!r}")
+    if group not in (16, 32, 64) or cols % group:
+        raise ValueError("group must be 16, 32 or 64 and divide the channels")
+    wt = 0
+    if weight is not None:
+        if weight.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("weight must be float32 or bfloat16")
+        wt = 1 if weight.dtype == torch.bfloat16 else 0
+    one = (cols,)
+    sdt = torch.int16 if fmt == "int4_bf16" else torch.uint8
+    return (X.data_ptr(), DTYPE[dt], _arr("residual", residual, dev, X.dtype, X.shape, True),
+            _arr("residual_out", residual_out, dev, X.dtype, X.shape, True), tokens, cols,
+            None if weight is None else _arr("weight", weight, dev, weight.dtype, one), wt,
+            float(eps), _arr("b", b, dev, torch.float32, one, True), ACT_FMT[fmt], group, float(g),
+            _arr("codes", codes, dev, torch.uint8,
+                 (tokens, cols if fmt == "mxfp8" else cols // 2)),
+            _arr("scales", scales, dev, sdt, (tokens, cols // group)))
+
+
+def norm_quantize_act(X, fmt: str, group: int, weight=None, residual=None, residual_out=None,
+                      b=None, eps: float = 1e-5, g: float = 0.0, workspace=None,
+                      stream=None) -> Dict[str, object]:
+    """dq_norm_quantize_act: h = X + residual, its root-mean-square norm times ``weight`` and the
+    column inverse scales ``b``, quantized as quantize_act does (any of its formats; NVFP4 takes
+    a fixed ``g`` > 0) or to "mxfp8". Returns codes, scales and, with a residual, "residual": h
+    in ``residual_out`` (``residual`` itself updates it in place) or a new tensor."""
+    torch = _torch()
+    if fmt in ACT_FMT and X.dim() == 2 and group in (16, 32, 64):
+        tokens, cols = X.shape
+        codes = _empty((tokens, cols if fmt == "mxfp8" else cols // 2), torch.uint8, X.device,
+                       stream)
+        scales = _empty((tokens, cols // group),
+                        torch.int16 if fmt == "int4_bf16" else torch.uint8, X.device, stream)
+    else:
+        codes = scales = None  # refused below
+    if residual is not None and residual_out is None:
+        residual_out = _empty(X.shape, X.dtype, X.device, stream)
+    args = _norm_args(X, fmt, group, codes, scales, weight, residual, residual_out, b, eps, g)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                            workspace.numel() * workspace.element_size())
+    st = _call(X.device, stream, lib().dq_norm_quantize_act, *args, ws_ptr, ws_bytes)
+    if st != 0:
+        raise DQError(st, "dq_norm_quantize_act")
+    out = {"codes": codes, "scales": scales}
+    if residual is not None:
+        out["residual"] = residual_out
+    return out
+
+
+def norm_quantize_act_async(X, fmt: str, group: int, codes, scales, status, weight=None,
+                            residual=None, residual_out=None, b=None, eps: float = 1e-5,
+                            g: float = 0.0, stream=None) -> None:
+    """dq_norm_quantize_act_async into caller-allocated outputs (codes, scales from act_outputs;
+    ``residual_out`` wherever ``residual`` is given): enqueued on the stream, no wait; device
+    errors are OR-ed into ``status`` (an int32 CUDA tensor the caller clears)."""
+    args = _norm_args(X, fmt, group, codes, scales, weight, residual, residual_out, b, eps, g)
+    if status.dtype != _torch().int32 or status.device != X.device:
+        raise ValueError("status must be an int32 tensor on X's device")
+    st = _call(X.device, stream, lib().dq_norm_quantize_act_async, *args, status.data_ptr())
+    if st != 0:
+        raise DQError(st, "dq_norm_quantize_act_async")
+
+
+def _product_args(act_codes, act_scales, act_fmt, packed, a, name):
+    """Checks of one product: the arguments it shares with every other, its packed weights' and
+    its a."""
+    torch = _torch()
+    if act_fmt not in ("mxfp4", "mxfp8"):
+        raise ValueError("act_fmt is 'mxfp4' or 'mxfp8'")
+    if not act_codes.is_cuda or act_codes.dim() != 2:
+        raise ValueError("act_codes must be a 2-D CUDA (HIP) tensor")
+    dev, tokens = act_codes.device, act_codes.shape[0]
+    K, out = packed["K"], packed["out"]
+    xc = _arr("act_codes", act_codes, dev, torch.uint8,
+              (tokens, K if act_fmt == "mxfp8" else K // 2))
+    xs = _arr("act_scales", act_scales, dev, torch.uint8, (tokens, K // 32))
+    pc, ps = packed["codes"], packed["scales"]
+    nrb = -(-out // 32)
+    return ((xc, xs, ACT_FMT[act_fmt], tokens, K),
+            (_arr(name + " codes", pc, dev, torch.uint8, (nrb * 16 * K,)),
+             _arr(name + " scales", ps, dev, torch.uint8, (nrb * K,))),
+            _arr(name + " a", a, dev, torch.float32, (out,), True))
+
+
+def gemm_mx_epilogue(act_codes, act_scales, packed, a=None, bias=None, activation: str = "none",
+                     residual=None, act_fmt: str = "mxfp4", out_dtype: str = "bf16", y=None,
+                     stream=None):
+    """dq_gemm_mx_epilogue: Y = residual + act((xhat Qhat^T) D_a + bias) with weights from
+    gemm_pack_weights and MXFP4 or MXFP8 activations. ``residual`` (tokens x out, of the output
+    type) may be ``y`` itself. Returns Y (tokens x out, bfloat16 or float32; MXFP8 activations
+    give bfloat16), into ``y`` when given."""
+    torch = _torch()
+    head, w, ap = _product_args(act_codes, act_scales, act_fmt, packed, a, "packed")
+    dev, out, dt = act_codes.device, packed["out"], _out_dtype(out_dtype)
+    if activation not in ACTIVATION:
+        raise ValueError(f"unknown activation {activation!r}")
+    shape = (head[3], out)
+    if y is None:
+        y = _empty(shape, dt, dev, stream)
+    st = _call(dev, stream, lib().dq_gemm_mx_epilogue, *head, *w, ap,
+               _arr("bias", bias, dev, torch.float32, (out,), True), ACTIVATION[activation],
+               _arr("residual", residual, dev, dt, shape, True), out, DTYPE[out_dtype],
+               _arr("y", y, dev, dt, shape))
+    if st != 0:
+        raise DQError(st, "dq_gemm_mx_epilogue")
+    return y
+
+
+def _gated_args(act_codes, act_scales, act_fmt, gate, up, a_gate, a_up, activation):
+    head, g, ag = _product_args(act_codes, act_scales, act_fmt, gate, a_gate, "gate")
+    _, u, au = _product_args(act_codes, act_scales, act_fmt, up, a_up, "up")
+    if gate["out"] != up["out"]:
+        raise ValueError("gate and up weights disagree on their output channels")
+    if activation not in ACTIVATION:
+        raise ValueError(f"unknown activation {activation!r}")
+    return (*head, *g, ag, *u, au, ACTIVATION[activation], gate["out"])
+
+
+def gated_mx(act_codes, act_scales, gate, up, a_gate=None, a_up=None, activation: str = "silu",
+             act_fmt: str = "mxfp4", out_dtype: str = "bf16", y=None, stream=None):
+    """dq_gated_mx: H = act((xhat Qgate^T) D_a_gate) * ((xhat Qup^T) D_a_up) in one kernel, gate
+    and up weights each from gemm_pack_weights. Returns H (tokens x inner, bfloat16 or float32;
+    MXFP8 activations give bfloat16), into ``y`` when given."""
+    args = _gated_args(act_codes, act_scales, act_fmt, gate, up, a_gate, a_up, activation)
+    dev, dt, shape = act_codes.device, _out_dtype(out_dtype), (act_codes.shape[0], gate["out"])
+    if y is None:
+        y = _empty(shape, dt, dev, stream)
+    st = _call(dev, stream, lib().dq_gated_mx, *args, DTYPE[out_dtype],
+               _arr("y", y, dev, dt, shape))
+    if st != 0:
+        raise DQError(st, "dq_gated_mx")
+    return y
+
+
+def gated_mx_quantized(act_codes, act_scales, gate, up, fmt: str, a_gate=None, a_up=None,
+                       activation: str = "silu", b=None, act_fmt: str = "mxfp4", codes=None,
+                       scales=None, stream=None) -> Dict[str, object]:
+    """dq_gated_mx_quantized: gated_mx's H times ``b`` (the next product's column inverse scales),
+    quantized to ``fmt`` ("mxfp4" or "mxfp8") in groups of 32 channels. Returns codes and scales
+    (into the given tensors), as the next product takes them."""
+    torch = _torch()
+    args = _gated_args(act_codes, act_scales, act_fmt, gate, up, a_gate, a_up, activation)
+    dev, tokens, inner = act_codes.device, act_codes.shape[0], gate["out"]
+    if fmt not in ("mxfp4", "mxfp8") or inner % 32:
+        raise ValueError("fmt is 'mxfp4' or 'mxfp8', and the channels a multiple of 32")
+    cs, ss = (tokens, inner if fmt == "mxfp8" else inner // 2), (tokens, inner // 32)
+    if codes is None:
+        codes = _empty(cs, torch.uint8, dev, stream)
+    if scales is None:
+        scales = _empty(ss, torch.uint8, dev, stream)
+    st = _call(dev, stream, lib().dq_gated_mx_quantized, *args,
+               _arr("b", b, dev, torch.float32, (inner,), True), ACT_FMT[fmt],
+               _arr("codes", codes, dev, torch.uint8, cs),
+               _arr("scales", scales, dev, torch.uint8, ss))
+    if st != 0:
+        raise DQError(st, "dq_gated_mx_quantized")
+    return {"codes": codes, "scales": scales}
 
 
 class _BatchItem(ctypes.Structure):

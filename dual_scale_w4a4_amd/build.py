@@ -16,6 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libdq.so")
 SOURCES = ["dq_kernels.hip", "dq_pass.hip", "dq_rowres.hip", "dq_act.hip", "dq_gemm.hip",
+           "dq_norm.hip", "dq_mlp.hip",
            "dq_api.hip"]
 ARCH = os.environ.get("DQ_OFFLOAD_ARCH", "gfx950")
 
