@@ -22,6 +22,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/dq_mlp.h"
 #include "dq_outq.h"
@@ -70,14 +71,25 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }
 
-__device__ __forceinline__ float activate(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ float activation(float z) {
+  if (ACT == DQ_ACTIVATION_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
+  if (ACT == DQ_ACTIVATION_SILU) return z * sigmoid(z);
+  if (ACT == DQ_ACTIVATION_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if (ACT == DQ_ACTIVATION_GELU_TANH)  // (1 + tanh u) / 2 = sigmoid(2 u)
+    return z * sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
+  return z;
+}
+
+// f(integral_constant<ACT>) for the call's activation (a uniform branch)
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F f) {
   switch (act) {
-    case DQ_ACTIVATION_RELU: return z < 0.0f ? 0.0f : z;  // a NaN stays one
-    case DQ_ACTIVATION_SILU: return z * sigmoid(z);
-    case DQ_ACTIVATION_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    case DQ_ACTIVATION_GELU_TANH:  // (1 + tanh u) / 2 = sigmoid(2 u)
-      return z * sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
-    default: return z;
+    case DQ_ACTIVATION_RELU: f(std::integral_constant<int, DQ_ACTIVATION_RELU>{}); break;
+    case DQ_ACTIVATION_SILU: f(std::integral_constant<int, DQ_ACTIVATION_SILU>{}); break;
+    case DQ_ACTIVATION_GELU: f(std::integral_constant<int, DQ_ACTIVATION_GELU>{}); break;
+    case DQ_ACTIVATION_GELU_TANH: f(std::integral_constant<int, DQ_ACTIVATION_GELU_TANH>{}); break;
+    default: f(std::integral_constant<int, DQ_ACTIVATION_NONE>{}); break;
   }
 }
 
@@ -98,108 +110,88 @@ __device__ __forceinline__ f32x4 load_channels(const float* p, int ich, int out,
   return v;
 }
 
-// The factors of 4 channels, kept for every token a lane finishes.
-struct Chan {
-  f32x4 a0, a1, c;  // row scales; bias (single), column scales (quantized)
-};
-
-template <bool GATED, int OUT>
-__device__ __forceinline__ Chan load_chan(const MlpArgs& p, int ich) {
-  Chan c;
-  c.a0 = load_channels(p.a[0], ich, p.out, 1.0f);
-  if (GATED) c.a1 = load_channels(p.a[1], ich, p.out, 1.0f);
-  if (!GATED) c.c = load_channels(p.bias, ich, p.out, 0.0f);
-  if (OUT >= kOutFp4) c.c = load_channels(p.b, ich, p.out, 1.0f);
-  return c;
-}
-
-// Finish channels ich .. ich + 3 of token t from the raw sums s0 (and s1) and store them. For a
-// quantized output the 8 lanes of an aligned group of 8 hold the 32 channels of one scale
-// group of one token, and all are here with the same t.
-template <bool GATED, int OUT>
-__device__ __forceinline__ void finish(const MlpArgs& p, int64_t t, int ich, const Chan& c,
-                                       f32x4 s0, f32x4 s1) {
+// The epilogue's value of 4 channels from the raw sums s0 (and s1)
+template <bool GATED>
+__device__ __forceinline__ f32x4 combine(int act, const f32x4& a0, const f32x4& a1,
+                                         const f32x4& bias, const f32x4& s0, const f32x4& s1) {
   f32x4 y;
-#pragma unroll
-  for (int e = 0; e < 4; e++) {
-    const float z = s0[e] * c.a0[e];
-    if (GATED)
-      y[e] = activate(z, p.act) * (s1[e] * c.a1[e]);
-    else
-      y[e] = activate(z + c.c[e], p.act);
-  }
-  const int64_t off = t * p.out + ich;
-  if (OUT >= kOutFp4) {
-    float x[4];
-    uint32_t mb = 0u;
+  with_activation(act, [&](auto k) {
 #pragma unroll
     for (int e = 0; e < 4; e++) {
-      x[e] = y[e] * c.c[e];
-      mb = max(mb, dq::f2u(x[e]) & 0x7FFFFFFFu);
+      const float z = GATED ? s0[e] * a0[e] : s0[e] * a0[e] + bias[e];
+      y[e] = activation<decltype(k)::value>(z);
+      if (GATED) y[e] *= s1[e] * a1[e];
     }
-    mb = dq::group_max_bits<8>(mb);
-    const bool bad = mb >= 0x7F800000u;  // a NaN or an infinity in the group
-    if (bad) {
-      mb = 0u;
-#pragma unroll
-      for (int e = 0; e < 4; e++) x[e] = 0.0f;
-    }
-    const uint32_t sc = dq::mx_scale_code<OUT == kOutFp8 ? 8 : 2>(mb);
-    if (ich < p.out) {
-      if (OUT == kOutFp8) {
-        *reinterpret_cast<uint32_t*>(p.codes + off) =
-            dq::fp8_pack4(x, dq::u2f((254u - sc) << 23));
-      } else {
-        *reinterpret_cast<uint16_t*>(p.codes + (off >> 1)) =
-            (uint16_t)dq::fp4_pack<4>(x, dq::mx_group(sc));
-      }
-      if ((threadIdx.x & 7) == 0) p.scales[off >> 5] = bad ? 0xFFu : (uint8_t)sc;
-    }
-    return;
-  }
-  const bool vec = p.vec && ich < p.out;  // then all 4 channels exist
+  });
+  return y;
+}
+
+// Store channels ich .. ich + 3 of token t, after adding the residual. VEC: whole 4-channel
+// accesses (then ich < out means that all four exist).
+template <int OUT, bool VEC>
+__device__ __forceinline__ void store_row(const MlpArgs& p, int64_t t, int ich, f32x4 y) {
+  if (VEC && ich >= p.out) return;
+  const int64_t off = t * p.out + ich;
   if (OUT == kOutBf16) {
     __bf16* yp = static_cast<__bf16*>(p.y) + off;
-    if (!GATED && p.res) {
-      const __bf16* rp = static_cast<const __bf16*>(p.res) + off;
-      if (vec) {
+    const __bf16* rp = static_cast<const __bf16*>(p.res) + off;
+    if (VEC) {
+      if (p.res) {
         const bf16x4 r = *reinterpret_cast<const bf16x4*>(rp);
 #pragma unroll
         for (int e = 0; e < 4; e++) y[e] = (float)r[e] + y[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-          if (ich + e < p.out) y[e] = (float)rp[e] + y[e];
       }
-    }
-    const bf16x4 hv = {(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
-    if (vec) {
-      *reinterpret_cast<bf16x4*>(yp) = hv;
+      *reinterpret_cast<bf16x4*>(yp) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
     } else {
 #pragma unroll
       for (int e = 0; e < 4; e++)
-        if (ich + e < p.out) yp[e] = hv[e];
+        if (ich + e < p.out) yp[e] = (__bf16)(p.res ? (float)rp[e] + y[e] : y[e]);
     }
   } else {
     float* yp = static_cast<float*>(p.y) + off;
-    if (!GATED && p.res) {
-      const float* rp = static_cast<const float*>(p.res) + off;
-      if (vec) {
-        y = *reinterpret_cast<const f32x4*>(rp) + y;
-      } else {
+    const float* rp = static_cast<const float*>(p.res) + off;
+    if (VEC) {
+      if (p.res) {
+        const f32x4 r = *reinterpret_cast<const f32x4*>(rp);
 #pragma unroll
-        for (int e = 0; e < 4; e++)
-          if (ich + e < p.out) y[e] = rp[e] + y[e];
+        for (int e = 0; e < 4; e++) y[e] = r[e] + y[e];
       }
-    }
-    if (vec) {
       *reinterpret_cast<f32x4*>(yp) = y;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; e++)
-        if (ich + e < p.out) yp[e] = y[e];
+        if (ich + e < p.out) yp[e] = p.res ? rp[e] + y[e] : y[e];
     }
   }
+}
+
+// Quantize channels ich .. ich + 3 of token t and store codes and scale: the 8 lanes of an
+// aligned group of 8 hold the 32 channels of one scale group of one token, and all are here.
+template <int OUT>
+__device__ __forceinline__ void store_quantized(const MlpArgs& p, int64_t t, int ich,
+                                                const f32x4& b, const f32x4& y) {
+  const int64_t off = t * p.out + ich;
+  float x[4];
+  uint32_t mb = 0u;
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    x[e] = y[e] * b[e];
+    mb = max(mb, dq::f2u(x[e]) & 0x7FFFFFFFu);
+  }
+  mb = dq::group_max_bits<8>(mb);
+  const bool bad = mb >= 0x7F800000u;  // a NaN or an infinity in the group
+  if (bad) {
+    mb = 0u;
+#pragma unroll
+    for (int e = 0; e < 4; e++) x[e] = 0.0f;
+  }
+  const uint32_t sc = dq::mx_scale_code<OUT == kOutFp8 ? 8 : 2>(mb);
+  if (OUT == kOutFp8)
+    *reinterpret_cast<uint32_t*>(p.codes + off) = dq::fp8_pack4(x, dq::u2f((254u - sc) << 23));
+  else
+    *reinterpret_cast<uint16_t*>(p.codes + (off >> 1)) =
+        (uint16_t)dq::fp4_pack<4>(x, dq::mx_group(sc));
+  if ((threadIdx.x & 7) == 0) p.scales[off >> 5] = bad ? 0xFFu : (uint8_t)sc;
 }
 
 // ------------------------------------------------------------------- split-k kernel
@@ -324,16 +316,458 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
         for (int w = 0; w < W; w++)
           s[m] += *reinterpret_cast<const f32x4*>(part + (w * MB + m) * kPartBlock + tr * kPartRow + ch);
       const int t = t0 + n * 32 + tr, ich = rb * 32 + ch;
-      if (t < p.tokens)
-        finish<GATED, OUT>(p, t, ich, load_chan<GATED, OUT>(p, ich), s[0], s[1]);
+      if (t >= p.tokens) continue;  // the same for the 8 lanes of a group of channels
+      const f32x4 a0 = load_channels(p.a[0], ich, p.out, 1.0f);
+      const f32x4 a1 = load_channels(GATED ? p.a[1] : nullptr, ich, p.out, 1.0f);
+      const f32x4 c = load_channels(GATED ? p.b : p.bias, ich, p.out, GATED ? 1.0f : 0.0f);
+      const f32x4 y = combine<GATED>(p.act, a0, a1, c, s[0], s[1]);
+      if constexpr (OUT >= kOutFp4) store_quantized<OUT>(p, t, ich, c, y);
+      else if (p.vec) store_row<OUT, true>(p, t, ich, y);
+      else store_row<OUT, false>(p, t, ich, y);
     }
   }
+}
+
+// --------------------------------------------------------------------- tile kernel
+// Four waves, each with two 32-row weight blocks m (single product: blocks 2 w, 2 w + 1 of the
+// tile's 256 rows; gated: the gate's and the up weights' block of the tile's channels 32 w ..)
+// times all the tile's 32 NB tokens. Weight fragments go from memory straight into registers,
+// each entering the CU once; the tokens go through LDS.
+//
+// k runs in stages of 128 bytes of a token row: 256 k in four steps (FP4), 128 k in two (FP8:
+// half a packed stage, steps 2 hs and 2 hs + 1 of it, hs = stage % 2; of each token row the bytes
+// of k chunks 2 hs, 2 hs + 1, 4 + 2 hs and 5 + 2 hs). Loads run two stages ahead: the
+// fragments of two stages are a ring of registers, each reloaded right after the last product
+// that reads it, and the tokens use a ring of three LDS buffers. A row's eight 16-byte pieces
+// are XOR-swizzled in LDS so that neither the loads nor the reads conflict.
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+// s_waitcnt operand: at most n vector-memory operations outstanding, the other counters free
+constexpr int vmcnt_imm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+
+constexpr int kRowB = 128;         // bytes of a token row in a stage
+constexpr int kScaleRowB = 16;     // token scale bytes per row and period (512 k)
+constexpr int kGroupM = 4;         // weight tiles per tile group (L2 reuse)
+
+template <int NB>
+struct TileLds {
+  uint8_t x[3][NB * 32 * kRowB];   // [stage % 3]: token stages
+  uint8_t xs[2][256 * kScaleRowB]; // [period parity]: token scales
+};
+
+template <bool ACT8, int NB>
+struct TileCtx {
+  __amdgpu_buffer_rsrc_t rw[2], rs[2], rx, rxs, rnone;
+  int wave, nst;
+  uint32_t vw[2], vs[2];  // this lane's offsets in the wave's weight blocks' codes and scales
+  uint32_t vx[NB];        // token-stage offsets of this lane's rows, or kOob
+  uint32_t vxs;           // token-scale offset of this lane's row, or kOob
+};
+
+constexpr int steps(bool act8) { return act8 ? 2 : 4; }
+
+// 16 bytes per lane from memory to LDS: lane l's at dst + 16 l
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rs, uint8_t* dst, uint32_t voff,
+                                         int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)dst, 16, (int)voff, soff, 0, 0);
+}
+
+// Token-stage load j of this wave: LDS rows 8 (NB wave + j) .. + 7, lane l writing row
+// l / 8 of them at piece position l % 8.
+template <bool ACT8, int NB>
+__device__ __forceinline__ void load_x(const TileCtx<ACT8, NB>& c, uint8_t* xb, int j, int s,
+                                       bool on) {
+  const int o = ACT8 ? (s >> 1) * 256 + (s & 1) * 64 : s * kRowB;
+  load_lds(on ? c.rx : c.rnone, xb + (c.wave * NB + j) * 1024, c.vx[j], o);
+}
+
+template <bool ACT8, int NB>
+__device__ __forceinline__ void load_xs(const TileCtx<ACT8, NB>& c, uint8_t* xs, int q, bool on) {
+  load_lds(on ? c.rxs : c.rnone, xs + c.wave * 1024, c.vxs, q * 16);
+}
+
+template <bool ACT8, int NB>
+__device__ __forceinline__ u32x4 load_w(const TileCtx<ACT8, NB>& c, int m, int s, int ks, bool on) {
+  return __builtin_amdgcn_raw_buffer_load_b128(
+      on ? c.rw[m] : c.rnone, c.vw[m], (uint32_t)((s * steps(ACT8) + ks) * kPackStepB), 0);
+}
+
+template <bool ACT8, int NB>
+__device__ __forceinline__ uint32_t load_ws(const TileCtx<ACT8, NB>& c, int m, int s, bool on) {
+  return __builtin_amdgcn_raw_buffer_load_b32(on ? c.rs[m] : c.rnone, c.vs[m],
+                                              (uint32_t)((ACT8 ? s >> 1 : s) * kPackScaleB), 0);
+}
+
+// The 16-byte piece(s) of one token row that step ks takes: xt = the row's swizzle term with the
+// lane half folded in (FP4: piece 4 h + ks; FP8: pieces 2 ks + h and 4 + 2 ks + h).
+template <bool ACT8>
+__device__ __forceinline__ u32x4 read_x(const uint8_t* row, int ks, int part, int xt) {
+  return *reinterpret_cast<const u32x4*>(row + (((ACT8 ? 2 * ks + 4 * part : ks) ^ xt) * 16));
+}
+
+// Step KS of a stage (HS: FP8's half of the packed stage): 2 NB products in the order (m, n), and
+// between them the next step's token fragments from LDS (after the last step the next stage's
+// first ones, and its token scales), the reload of block m's fragment with stage s + 2's
+// after its last product, and this step's share of stage s + 2's token loads (XS: also the
+// next period's token scales). Loads past the last stage read nothing (they still write
+// zeros to LDS, into buffers no longer read), so every stage issues the same number.
+template <bool ACT8, int NB, int KS, int HS, bool XS>
+__device__ __forceinline__ void tile_step(v16f (&acc)[2][NB], u32x4 (&fa)[2][steps(ACT8)],
+                                          const u32x4 (&fb)[NB][ACT8 ? 2 : 1],
+                                          u32x4 (&fn)[NB][ACT8 ? 2 : 1], uint32_t (&sw)[2],
+                                          const uint32_t (&sx)[NB], uint32_t (&sn)[NB],
+                                          const uint8_t* lx, const uint8_t* lxn,
+                                          const uint8_t* xsn, int xt, const TileCtx<ACT8, NB>& c,
+                                          uint8_t* xb, uint8_t* xsb, int s, int q, bool xs_on) {
+  constexpr int NK = steps(ACT8), TL = NB / NK;
+  constexpr bool kLast = KS == NK - 1;
+  const int s2 = s + 2;
+  const bool on = s2 < c.nst;
+#pragma unroll
+  for (int t = 0; t < 2 * NB; t++) {
+    const int m = t / NB, n = t % NB;
+    acc[m][n] = mfma<ACT8>(fa[m][KS], fb[n], acc[m][n], sw[m], sx[n], ACT8 ? 2 * HS + KS : KS);
+    const uint8_t* row = (kLast ? lxn : lx) + (t / 2) * 32 * kRowB;
+    if (ACT8 || t % 2 == 0)
+      fn[t / 2][ACT8 ? t % 2 : 0] = read_x<ACT8>(row, kLast ? 0 : KS + 1, t % 2, xt);
+    if (kLast && t % 2 == 1)
+      sn[t / 2] = *reinterpret_cast<const uint32_t*>(xsn + (t / 2) * 32 * kScaleRowB);
+    if (n == NB - 1) {
+      fa[m][KS] = load_w(c, m, s2, KS, on);
+      if (kLast) sw[m] = load_ws(c, m, s2, on);
+    }
+    if (t % (2 * NB / TL) == 1) load_x(c, xb, KS * TL + t / (2 * NB / TL), s2, on);
+    if (XS && KS == 0 && t == 2) load_xs(c, xsb, q, xs_on);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// The epilogue. Result v of block (m, n) is channel 32 rb + 8 (v / 4) + 4 h + v % 4 of the
+// block's 32 and token 32 n + lane % 32: scales, bias, activation and the gate's product are
+// applied there, 32 tokens at a time, with each lane's channel factors in registers.
+// Quantized outputs then need one exchange between the lane halves per token group (its 32
+// channels lie in lanes l and l + 32) and are stored from there. bf16 and fp32 outputs go through
+// LDS, so that the stores (and the residual's loads, one chunk ahead) cover whole rows of the
+// wave's channels instead of 8 or 16 bytes of 32 rows. FULL: the tile lies inside the tokens and
+// channels and takes 4-channel accesses.
+// order LDS accesses of one wave (its LDS instructions execute in order; this keeps the compiler
+// from moving them)
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <bool GATED, int OUT>
+__device__ __forceinline__ void quantize_chunk(const MlpArgs& p, f32x4 (&y)[4], int t, int rb,
+                                               int h, bool in) {
+  uint32_t mb = 0u;
+#pragma unroll
+  for (int g = 0; g < 4; g++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) mb = max(mb, dq::f2u(y[g][e]) & 0x7FFFFFFFu);
+  mb = max(mb, (uint32_t)__shfl_xor((int)mb, 32, 64));
+  const bool bad = mb >= 0x7F800000u;  // a NaN or an infinity in the group
+  if (bad) {
+    mb = 0u;
+#pragma unroll
+    for (int g = 0; g < 4; g++) y[g] = f32x4{};
+  }
+  const uint32_t sc = dq::mx_scale_code<OUT == kOutFp8 ? 8 : 2>(mb);
+  uint32_t c[4];  // the codes of channels 8 g + 4 h .. + 3
+  if (OUT == kOutFp8) {
+    const float rd = dq::u2f((254u - sc) << 23);
+#pragma unroll
+    for (int g = 0; g < 4; g++) c[g] = dq::fp8_pack4(reinterpret_cast<const float*>(&y[g]), rd);
+  } else {
+    const dq::GroupQ gq = dq::mx_group(sc);
+#pragma unroll
+    for (int g = 0; g < 4; g++) c[g] = dq::fp4_pack<4>(reinterpret_cast<const float*>(&y[g]), gq);
+  }
+  // after the swaps lane half 0 holds groups 0, 1 of both halves and lane half 1 groups 2, 3
+  const auto s0 = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
+  const auto s1 = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
+  if (!in) return;
+  const int64_t off = (int64_t)t * p.out + rb * 32 + 16 * h;
+  if (OUT == kOutFp8) {
+    *reinterpret_cast<u32x4*>(p.codes + off) =
+        u32x4{(uint32_t)s0[0], (uint32_t)s0[1], (uint32_t)s1[0], (uint32_t)s1[1]};
+  } else {
+    const uint64_t lo = (uint32_t)s0[0] | ((uint32_t)s0[1] << 16);
+    const uint64_t hi = (uint32_t)s1[0] | ((uint32_t)s1[1] << 16);
+    *reinterpret_cast<uint64_t*>(p.codes + (off >> 1)) = lo | (hi << 32);
+  }
+  if (h == 0) p.scales[off >> 5] = bad ? 0xFFu : (uint8_t)sc;
+}
+
+template <bool GATED, int NB, int OUT, bool FULL>
+__device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2][NB], int rb0,
+                                           int t0, uint8_t* stage) {
+  constexpr int ME = GATED ? 1 : 2;       // row blocks of results
+  constexpr int LPR = 8 * ME;             // lanes per token row in the read-back
+  constexpr int NR = 32 * LPR / 64;       // row accesses of a chunk per lane
+  constexpr int kRow = 128 * ME + 16;     // bytes of a staged token row, padded
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rl = lane & 31, h = lane >> 5;
+  f32x4 a0[ME][4], a1[4], cc[ME][4];
+#pragma unroll
+  for (int m = 0; m < ME; m++)
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const int ich = (rb0 + m) * 32 + 8 * g + 4 * h;
+      a0[m][g] = load_channels(p.a[0], ich, p.out, 1.0f);
+      if (GATED) a1[g] = load_channels(p.a[1], ich, p.out, 1.0f);
+      cc[m][g] = load_channels(GATED ? p.b : p.bias, ich, p.out, GATED ? 1.0f : 0.0f);
+    }
+  __syncthreads();  // every wave is done with the main loop's LDS
+  uint8_t* region = stage + wave * 2 * (32 * kRow);  // two chunks, taken in turn
+  const int cl = lane % LPR, rr = lane / LPR;
+  const int ich = rb0 * 32 + cl * 4;      // the 4 channels this lane stores
+  typedef typename std::conditional<OUT == kOutF32, f32x4, bf16x4>::type row4;
+  row4 res[2][NR];
+  const bool has_res = FULL && !GATED && p.res;
+  auto fetch = [&](int n) {
+    if (OUT < kOutFp4 && has_res) {
+#pragma unroll
+      for (int r = 0; r < NR; r++) {
+        const int64_t t = t0 + n * 32 + r * (64 / LPR) + rr;
+        res[n & 1][r] = *reinterpret_cast<const row4*>(
+            static_cast<const char*>(p.res) + (t * p.out + ich) * (OUT == kOutF32 ? 4 : 2));
+      }
+    }
+  };
+  fetch(0);
+#pragma unroll
+  for (int n = 0; n < NB; n++) {
+    __builtin_amdgcn_sched_barrier(0);  // one chunk's registers at a time
+    f32x4 y[ME][4];
+    with_activation(p.act, [&](auto k) {
+#pragma unroll
+      for (int m = 0; m < ME; m++)
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const float z = acc[m][n][4 * g + e] * a0[m][g][e];
+            float v = activation<decltype(k)::value>(GATED ? z : z + cc[m][g][e]);
+            if (GATED) v *= acc[1][n][4 * g + e] * a1[g][e];
+            y[m][g][e] = v;
+          }
+    });
+    if constexpr (OUT >= kOutFp4) {
+#pragma unroll
+      for (int g = 0; g < 4; g++) y[0][g] *= cc[0][g];
+      const int t = t0 + n * 32 + rl;
+      quantize_chunk<GATED, OUT>(p, y[0], t, rb0, h, FULL || (t < p.tokens && rb0 * 32 < p.out));
+    } else {
+      uint8_t* reg = region + (n & 1) * (32 * kRow);
+#pragma unroll
+      for (int m = 0; m < ME; m++)
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+          *reinterpret_cast<f32x4*>(reg + rl * kRow + (m * 32 + g * 8 + h * 4) * 4) = y[m][g];
+      wave_lds_order();
+      if (FULL) {
+        if (n + 1 < NB) fetch(n + 1);
+#pragma unroll
+        for (int r = 0; r < NR; r++) {
+          const int row = r * (64 / LPR) + rr;
+          f32x4 v = *reinterpret_cast<const f32x4*>(reg + row * kRow + cl * 16);
+          const int64_t off = (int64_t)(t0 + n * 32 + row) * p.out + ich;
+          if (has_res) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] = (float)res[n & 1][r][e] + v[e];
+          }
+          if constexpr (OUT == kOutBf16) {
+            const bf16x4 o = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+            __builtin_nontemporal_store(o, reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.y) + off));
+          } else {
+            __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + off));
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int r = 0; r < NR; r++) {
+          const int row = r * (64 / LPR) + rr;
+          const f32x4 v = *reinterpret_cast<const f32x4*>(reg + row * kRow + cl * 16);
+          const int t = t0 + n * 32 + row;
+          if (t < p.tokens) {
+            if (p.vec) store_row<OUT, true>(p, t, ich, v);
+            else store_row<OUT, false>(p, t, ich, v);
+          }
+        }
+      }
+      wave_lds_order();
+    }
+  }
+}
+
+// Workgroups are dealt round-robin to the eight XCDs, so consecutive ids are spread: each XCD
+// gets a contiguous range of tiles, ordered in groups of kGroupM weight tiles by every token
+// tile, so that the workgroups running together on one XCD share weights and tokens in its L2.
+__device__ __forceinline__ void tile_origin(int nti, int ntt, int& ti, int& tt) {
+  const int ntiles = nti * ntt, bid = blockIdx.x;
+  const int full = (ntiles / 8) * 8;
+  const int L = bid < full ? (bid % 8) * (ntiles / 8) + bid / 8 : bid;
+  const int gsz = kGroupM * ntt;
+  const int first = (L / gsz) * kGroupM;
+  const int gm = min(nti - first, kGroupM);
+  ti = first + (L % gsz) % gm;
+  tt = (L % gsz) / gm;
+}
+
+template <bool ACT8, bool GATED, int NB, int OUT>
+__global__ __launch_bounds__(256, 1) void k_mlp_tile(MlpArgs p, int nti, int ntt) {
+  __shared__ __attribute__((aligned(1024))) TileLds<NB> L;
+  static_assert(sizeof(L) >= 4 * 2 * 32 * (256 + 16) || (GATED && sizeof(L) >= 4 * 2 * 32 * (128 + 16)),
+                "epilogue staging does not fit");
+  constexpr int NK = steps(ACT8);
+  constexpr int PER = ACT8 ? 4 : 2;  // stages per token-scale period (512 k)
+  int ti, tt;
+  tile_origin(nti, ntt, ti, tt);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rl = lane & 31, h = lane >> 5;
+  const int t0 = tt * 32 * NB;
+  const int rows = min(p.tokens - t0, 32 * NB);
+  const int ldb = ACT8 ? p.K : p.K / 2, nkb = p.K / 32, npk = p.K / kStage;
+  const int nrb = (p.out + 31) / 32;
+  const int rb0 = ti * (GATED ? 4 : 8) + wave * (GATED ? 1 : 2);  // this wave's first row block
+
+  TileCtx<ACT8, NB> c;
+  c.wave = wave;
+  c.nst = p.K / (ACT8 ? 128 : 256);
+#pragma unroll
+  for (int m = 0; m < 2; m++) {
+    // a block past the last weight row reads nothing: a descriptor without records
+    const int rb = GATED ? rb0 : rb0 + m;
+    const bool in = rb < nrb;
+    const int64_t at = in ? rb : 0;
+    c.rw[m] = rsrc(p.wc[GATED ? m : 0] + at * npk * kPackStageB, in ? (uint32_t)npk * kPackStageB : 0u);
+    c.rs[m] = rsrc(p.ws[GATED ? m : 0] + at * npk * kPackScaleB, in ? (uint32_t)npk * kPackScaleB : 0u);
+    c.vw[m] = (uint32_t)lane * 16u;
+    c.vs[m] = (uint32_t)lane * 4u;
+  }
+  c.rx = rsrc(p.xc + (int64_t)t0 * ldb, (uint32_t)rows * (uint32_t)ldb);
+  c.rxs = rsrc(p.xs + (int64_t)t0 * nkb, (uint32_t)rows * (uint32_t)nkb);
+  c.rnone = rsrc(p.xc, 0u);
+#pragma unroll
+  for (int j = 0; j < NB; j++) {
+    // lane l writes piece position l % 8 of row r, which holds the row's piece (l % 8) ^ term
+    const int r = 8 * (wave * NB + j) + (lane >> 3);
+    const int pc = (lane & 7) ^ (r & 7) ^ ((r >> 3) & 1);
+    const uint32_t o = (uint32_t)pc * 16u + (ACT8 && pc >= 4 ? 64u : 0u);
+    c.vx[j] = r < rows ? (uint32_t)r * (uint32_t)ldb + o : kOob;
+  }
+  {
+    const int r = wave * 64 + lane;
+    c.vxs = r < rows ? (uint32_t)r * (uint32_t)nkb : kOob;
+  }
+
+  v16f acc[2][NB];
+#pragma unroll
+  for (int m = 0; m < 2; m++)
+#pragma unroll
+    for (int n = 0; n < NB; n++) acc[m][n] = v16f{};
+
+  const int xt = (rl & 7) ^ ((rl >> 3) & 1) ^ (ACT8 ? h : 4 * h);
+  const int xrow = rl * kRowB;
+  const int xsrow = rl * kScaleRowB + 4 * h;
+
+  u32x4 fa[2][2][NK];              // [stage parity][m][step]: weight fragments
+  uint32_t sw[2][2];               // [stage parity][m]: their scale dwords
+  u32x4 fb[2][NB][ACT8 ? 2 : 1];   // this step's and the next step's token fragments
+  uint32_t sx[2][NB];              // [stage parity]: token scale dwords
+
+  // stages 0 and 1 and the first period's token scales; only stage 0 has to land before the loop
+#pragma unroll
+  for (int st = 0; st < 2; st++) {
+#pragma unroll
+    for (int m = 0; m < 2; m++) {
+#pragma unroll
+      for (int i = 0; i < NK; i++) fa[st][m][i] = load_w(c, m, st, i, true);
+      sw[st][m] = load_ws(c, m, st, true);
+    }
+#pragma unroll
+    for (int j = 0; j < NB; j++) load_x(c, L.x[st], j, st, true);
+    if (st == 0) load_xs(c, L.xs[0], 0, true);
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * NK + 2 + NB));  // stage 1's loads may be in flight
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+  for (int n = 0; n < NB; n++) {
+    sx[0][n] = *reinterpret_cast<const uint32_t*>(L.xs[0] + xsrow + n * 32 * kScaleRowB);
+#pragma unroll
+    for (int e = 0; e < (ACT8 ? 2 : 1); e++)
+      fb[0][n][e] = read_x<ACT8>(L.x[0] + xrow + n * 32 * kRowB, 0, e, xt);
+  }
+
+  // Stage s of period position J (fragments fa[J % 2], token buffer s % 3) while stage s + 2
+  // loads into the registers it frees and buffer (s + 2) % 3. Before the last step every load
+  // issued before this stage is complete in this wave (the loads of the steps so far may be in
+  // flight: a fixed count) and its LDS reads are done; after the barrier that holds in every
+  // wave, so the last step may read stage s + 1's first fragments and scales under its own
+  // products, and stage s + 1 may load into the buffer that stage s - 1 read.
+  auto stage = [&](auto jc, int s, int q, bool more) {
+    constexpr int J = decltype(jc)::value, P = J & 1;
+    constexpr bool XS = J == 0;
+    const uint8_t* lx = L.x[s % 3] + xrow;
+    const uint8_t* lxn = L.x[(s + 1) % 3] + xrow;
+    uint8_t* xb = L.x[(s + 2) % 3];
+    // stage s + 1's token scales: its period, and the half (256 k) of it
+    const uint8_t* xsn = L.xs[((s + 1) / PER) & 1] + xsrow + (((J + 1) % PER) / (PER / 2)) * 8;
+    uint8_t* xsb = L.xs[(q + 1) & 1];
+    auto step = [&](auto kc) {
+      constexpr int KS = decltype(kc)::value;
+      tile_step<ACT8, NB, KS, P, XS>(acc, fa[P], fb[KS & 1], fb[(KS & 1) ^ 1], sw[P], sx[P],
+                                     sx[P ^ 1], lx, lxn, xsn, xt, c, xb, xsb, s, q + 1, more);
+    };
+    __builtin_amdgcn_sched_barrier(0);
+    step(std::integral_constant<int, 0>{});
+    if constexpr (NK == 4) {
+      step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{});
+    }
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm((NK - 1) * (2 + NB / NK) + (XS ? 1 : 0)) & ~(15 << 8));
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+    step(std::integral_constant<int, NK - 1>{});
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  for (int q = 0; q < p.K / 512; q++) {
+    const bool more = q + 1 < p.K / 512;
+    stage(std::integral_constant<int, 0>{}, PER * q, q, more);
+    stage(std::integral_constant<int, 1>{}, PER * q + 1, q, more);
+    if constexpr (PER == 4) {
+      stage(std::integral_constant<int, 2>{}, PER * q + 2, q, more);
+      stage(std::integral_constant<int, 3>{}, PER * q + 3, q, more);
+    }
+  }
+  // the last stages' loads read nothing but still write zeros into LDS: drain them before the
+  // epilogue reuses that memory
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  uint8_t* stage_mem = reinterpret_cast<uint8_t*>(&L);
+  if (rows == 32 * NB && (rb0 + (GATED ? 1 : 2)) * 32 <= p.out && (OUT >= kOutFp4 || p.vec))
+    tile_store<GATED, NB, OUT, true>(p, acc, rb0, t0, stage_mem);
+  else
+    tile_store<GATED, NB, OUT, false>(p, acc, rb0, t0, stage_mem);
 }
 
 // ---------------------------------------------------------------------------------- host
 
 template <bool ACT8, bool GATED, int OUT>
 hipError_t launch_t(const MlpArgs& p, hipStream_t s) {
+  if (p.tokens >= 256) {
+    constexpr int NB = 8;
+    const int nti = (p.out + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
+    const int ntt = (p.tokens + 32 * NB - 1) / (32 * NB);
+    hipLaunchKernelGGL((k_mlp_tile<ACT8, GATED, NB, OUT>), dim3((unsigned)(nti * ntt)), dim3(256),
+                       0, s, p, nti, ntt);
+    return hipGetLastError();
+  }
   constexpr int NB = 1, W = 8;
   const int64_t nrb = (p.out + 31) / 32, ntt = (p.tokens + 32 * NB - 1) / (32 * NB);
   hipLaunchKernelGGL((k_mlp_split<ACT8, GATED, NB, OUT, W>), dim3((unsigned)(nrb * ntt)),
