@@ -194,20 +194,40 @@ __device__ __forceinline__ void store_quantized(const MlpArgs& p, int64_t t, int
   if ((threadIdx.x & 7) == 0) p.scales[off >> 5] = bad ? 0xFFu : (uint8_t)sc;
 }
 
-// ------------------------------------------------------------------- split-k kernel
-// A workgroup owns MB row blocks (the product's, or the gate's and the up weights' block of the
-// same 32 channels) and NB blocks of 32 tokens; its W waves share the stages of k between
-// them (wave w takes stages w, w + W, ..), every operand going from memory straight to
-// registers, and their partial sums are joined in LDS in wave order.
+// ------------------------------------------------------------------- operands
+// k runs in stages of 128 bytes of a token row: 256 k in four steps (FP4), 128 k in two (FP8:
+// half a packed stage, steps 2 hs and 2 hs + 1 of it, hs = stage % 2; of each token row the bytes
+// of k chunks 2 hs, 2 hs + 1, 4 + 2 hs and 5 + 2 hs). In LDS a row's eight 16-byte pieces are
+// XOR-swizzled so that neither the loads to LDS (whole rows) nor the reads (one piece of 32 rows
+// and both lane halves) conflict.
 
-// One stage's operands of a wave.
-template <bool ACT8, int MB, int NB>
-struct Frags {
-  u32x4 a[MB][4];
-  uint32_t sa[MB];
-  u32x4 b[NB][ACT8 ? 8 : 4];
-  uint32_t sb[NB];
-};
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+// s_waitcnt operand: at most n vector-memory operations outstanding, the other counters free
+constexpr int vmcnt_imm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+
+constexpr int kRowB = 128;         // bytes of a token row in a stage
+constexpr int steps(bool act8) { return act8 ? 2 : 4; }
+
+// 16 bytes per lane from memory to LDS: lane l's at dst + 16 l
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rs, uint8_t* dst, uint32_t voff,
+                                         int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)dst, 16, (int)voff, soff, 0, 0);
+}
+
+// The 16-byte piece(s) of one token row that step ks takes: xt = the row's swizzle term with the
+// lane half folded in (FP4: piece 4 h + ks; FP8: pieces 2 ks + h and 4 + 2 ks + h).
+template <bool ACT8>
+__device__ __forceinline__ u32x4 read_x(const uint8_t* row, int ks, int part, int xt) {
+  return *reinterpret_cast<const u32x4*>(row + (((ACT8 ? 2 * ks + 4 * part : ks) ^ xt) * 16));
+}
+
+// order LDS accesses of one wave (its LDS instructions execute in order; this keeps the compiler
+// from moving them)
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 template <bool ACT8>
 __device__ __forceinline__ v16f mfma(const u32x4& a, const u32x4* b, v16f c, uint32_t sa,
@@ -225,97 +245,160 @@ __device__ __forceinline__ v16f mfma(const u32x4& a, const u32x4* b, v16f c, uin
   }
 }
 
+// ------------------------------------------------------------------- split-k kernel
+// A workgroup owns M row blocks of 32 (the product's M neighbouring ones; gated: the gate's and
+// the up weights' block of the same 32 channels) and 32 NB tokens; its W waves share k between
+// them, wave w taking stages w, w + W, .., and their partial sums are joined in LDS in wave
+// order. Every wave runs by itself: its weights go from memory straight to registers, its tokens
+// through a ring of two LDS stages of its own, both loaded two of its stages ahead.
+
 // LDS row of one token's 32 partial sums, padded so that 8 rows cover distinct banks
 constexpr int kPartRow = 36;
 constexpr int kPartBlock = 32 * kPartRow;  // floats of one 32 x 32 block
 
-template <bool ACT8, bool GATED, int NB, int OUT, int W>
+// One stage's operands of a wave, but for the tokens in LDS.
+template <bool ACT8, int M, int NB>
+struct Frags {
+  u32x4 a[M][steps(ACT8)];
+  uint32_t sa[M];
+  uint32_t sb[NB];
+};
+
+template <bool ACT8, bool GATED, int M, int NB, int OUT, int W>
 __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
-  constexpr int MB = GATED ? 2 : 1;
-  __shared__ __attribute__((aligned(16))) float part[W * MB * kPartBlock];
+  static_assert(!GATED || M == 2, "gate and up");
+  constexpr int NK = steps(ACT8);
+  constexpr int kRing = NB * 32 * kRowB;  // one stage of a wave's tokens
+  constexpr int kPart = W * M * kPartBlock * 4;
+  constexpr int kLds = 2 * W * kRing > kPart ? 2 * W * kRing : kPart;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rl = lane & 31, h = lane >> 5;
   const int nrb = (p.out + 31) / 32;
-  const int rb = blockIdx.x % nrb;                // row block
-  const int t0 = (blockIdx.x / nrb) * (32 * NB);
-  const int ldb = ACT8 ? p.K : p.K / 2, nkb = p.K / 32, nst = p.K / kStage;
+  const int ntr = GATED ? nrb : (nrb + M - 1) / M;   // row tiles
+  const int rb0 = (blockIdx.x % ntr) * (GATED ? 1 : M);
+  const int t0 = (blockIdx.x / ntr) * (32 * NB);
   const int rows = min(p.tokens - t0, 32 * NB);
+  const int ldb = ACT8 ? p.K : p.K / 2, nkb = p.K / 32, npk = p.K / kStage;
+  const int nst = p.K / (ACT8 ? 128 : 256);
 
-  __amdgpu_buffer_rsrc_t rw[MB], rs[MB];
+  __amdgpu_buffer_rsrc_t rw[M], rs[M];
 #pragma unroll
-  for (int m = 0; m < MB; m++) {
-    rw[m] = rsrc(p.wc[m] + (int64_t)rb * nst * kPackStageB, (uint32_t)nst * kPackStageB);
-    rs[m] = rsrc(p.ws[m] + (int64_t)rb * nst * kPackScaleB, (uint32_t)nst * kPackScaleB);
+  for (int m = 0; m < M; m++) {
+    const int rb = GATED ? rb0 : rb0 + m;
+    const bool in = rb < nrb;  // a block past the last weight row reads nothing
+    const int64_t at = in ? rb : 0;
+    rw[m] = rsrc(p.wc[GATED ? m : 0] + at * npk * kPackStageB, in ? (uint32_t)npk * kPackStageB : 0u);
+    rs[m] = rsrc(p.ws[GATED ? m : 0] + at * npk * kPackScaleB, in ? (uint32_t)npk * kPackScaleB : 0u);
   }
   const __amdgpu_buffer_rsrc_t rx = rsrc(p.xc + (int64_t)t0 * ldb, (uint32_t)rows * (uint32_t)ldb);
   const __amdgpu_buffer_rsrc_t rxs = rsrc(p.xs + (int64_t)t0 * nkb, (uint32_t)rows * (uint32_t)nkb);
-  uint32_t vx[NB], vs[NB];
+  uint32_t vx[4 * NB], vs[NB];
+#pragma unroll
+  for (int j = 0; j < 4 * NB; j++) {
+    // lane l writes piece position l % 8 of row r, which holds the row's piece (l % 8) ^ term
+    const int r = 8 * j + (lane >> 3);
+    const int pc = (lane & 7) ^ (r & 7) ^ ((r >> 3) & 1);
+    vx[j] = r < rows ? (uint32_t)r * (uint32_t)ldb + (uint32_t)pc * 16u + (ACT8 && pc >= 4 ? 64u : 0u)
+                     : kOob;
+  }
 #pragma unroll
   for (int n = 0; n < NB; n++) {
     const int r = n * 32 + rl;
-    vx[n] = r < rows ? (uint32_t)r * (uint32_t)ldb + (ACT8 ? 16u : 64u) * (uint32_t)h : kOob;
     vs[n] = r < rows ? (uint32_t)r * (uint32_t)nkb + 4u * (uint32_t)h : kOob;
   }
+  uint8_t* ring = lds + wave * 2 * kRing;
+  const int xt = (rl & 7) ^ ((rl >> 3) & 1) ^ (ACT8 ? h : 4 * h);
 
-  v16f acc[MB][NB];
+  v16f acc[M][NB];
 #pragma unroll
-  for (int m = 0; m < MB; m++)
+  for (int m = 0; m < M; m++)
 #pragma unroll
     for (int n = 0; n < NB; n++) acc[m][n] = v16f{};
 
-  for (int s = wave; s < nst; s += W) {
-    Frags<ACT8, MB, NB> f;
+  auto load = [&](int s, uint8_t* xb, Frags<ACT8, M, NB>& f) {
 #pragma unroll
-    for (int m = 0; m < MB; m++) {
+    for (int j = 0; j < 4 * NB; j++)
+      load_lds(rx, xb + j * 1024, vx[j], ACT8 ? (s >> 1) * 256 + (s & 1) * 64 : s * kRowB);
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        f.a[m][i] = __builtin_amdgcn_raw_buffer_load_b128(
-            rw[m], (uint32_t)lane * 16u, (uint32_t)(s * kPackStageB + i * kPackStepB), 0);
+    for (int m = 0; m < M; m++) {
+#pragma unroll
+      for (int i = 0; i < NK; i++)
+        f.a[m][i] = __builtin_amdgcn_raw_buffer_load_b128(rw[m], (uint32_t)lane * 16u,
+                                                          (uint32_t)((s * NK + i) * kPackStepB), 0);
       f.sa[m] = __builtin_amdgcn_raw_buffer_load_b32(rs[m], (uint32_t)lane * 4u,
-                                                     (uint32_t)(s * kPackScaleB), 0);
+                                                     (uint32_t)((ACT8 ? s >> 1 : s) * kPackScaleB), 0);
     }
 #pragma unroll
-    for (int n = 0; n < NB; n++) {
+    for (int n = 0; n < NB; n++)
+      f.sb[n] = __builtin_amdgcn_raw_buffer_load_b32(rxs, vs[n], (uint32_t)((ACT8 ? s >> 1 : s) * 8), 0);
+  };
+  constexpr int kLoads = 4 * NB + M * (NK + 1) + NB;  // of one stage
+  static_assert(kLoads < 64, "the wait counts to 63");
+  // the products of stage s (its loads are done)
+  auto products = [&](int s, const uint8_t* xb, const Frags<ACT8, M, NB>& f) {
+    // FP8: the stage's half of the packed stage picks its scale bytes
+    uint32_t sa[M], sb[NB];
 #pragma unroll
-      for (int i = 0; i < (ACT8 ? 8 : 4); i++) {
-        // FP4: the lane's four chunks; FP8: 16 bytes of chunk i / 2 of either half
-        const uint32_t o = ACT8 ? (uint32_t)(s * 256 + (i / 2) * 32 + (i % 2) * 128)
-                                : (uint32_t)(s * 128 + i * 16);
-        f.b[n][i] = __builtin_amdgcn_raw_buffer_load_b128(rx, vx[n], o, 0);
+    for (int m = 0; m < M; m++) sa[m] = ACT8 ? f.sa[m] >> (16 * (s & 1)) : f.sa[m];
+#pragma unroll
+    for (int n = 0; n < NB; n++) sb[n] = ACT8 ? f.sb[n] >> (16 * (s & 1)) : f.sb[n];
+#pragma unroll
+    for (int i = 0; i < NK; i++)
+#pragma unroll
+      for (int n = 0; n < NB; n++) {
+        u32x4 b[ACT8 ? 2 : 1];
+#pragma unroll
+        for (int e = 0; e < (ACT8 ? 2 : 1); e++)
+          b[e] = read_x<ACT8>(xb + (n * 32 + rl) * kRowB, i, e, xt);
+#pragma unroll
+        for (int m = 0; m < M; m++) acc[m][n] = mfma<ACT8>(f.a[m][i], b, acc[m][n], sa[m], sb[n], i);
       }
-      f.sb[n] = __builtin_amdgcn_raw_buffer_load_b32(rxs, vs[n], (uint32_t)(s * 8), 0);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-      for (int m = 0; m < MB; m++)
-#pragma unroll
-        for (int n = 0; n < NB; n++)
-          acc[m][n] = mfma<ACT8>(f.a[m][i], &f.b[n][ACT8 ? 2 * i : i], acc[m][n], f.sa[m], f.sb[n], i);
+  };
+  // a stage's token reads are done before its buffer is loaded again, and its loads are done
+  // before it is read: no other wave touches the ring
+  auto stage = [&](int s, uint8_t* xb, Frags<ACT8, M, NB>& f) {
+    if (s + W < nst) __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLoads));
+    else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    wave_lds_order();
+    products(s, xb, f);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    wave_lds_order();
+    if (s + 2 * W < nst) load(s + 2 * W, xb, f);
+  };
+  Frags<ACT8, M, NB> f0, f1;
+  if (wave < nst) load(wave, ring, f0);
+  if (wave + W < nst) load(wave + W, ring + kRing, f1);
+  for (int s = wave; s < nst; s += 2 * W) {
+    stage(s, ring, f0);
+    if (s + W < nst) stage(s + W, ring + kRing, f1);
   }
 
   // join: block (m, n) of every wave as rows of tokens, then thread x adds the W partial sums
   // of 4 channels of one token in wave order
+  float* part = reinterpret_cast<float*>(lds);
 #pragma unroll
   for (int n = 0; n < NB; n++) {
-    if (n > 0) __syncthreads();
+    __syncthreads();  // every wave is done with its ring, or with the block before
 #pragma unroll
-    for (int m = 0; m < MB; m++)
+    for (int m = 0; m < M; m++)
 #pragma unroll
       for (int g = 0; g < 4; g++)
-        *reinterpret_cast<f32x4*>(part + (wave * MB + m) * kPartBlock + rl * kPartRow + g * 8 + h * 4) =
+        *reinterpret_cast<f32x4*>(part + (wave * M + m) * kPartBlock + rl * kPartRow + g * 8 + h * 4) =
             f32x4{acc[m][n][g * 4], acc[m][n][g * 4 + 1], acc[m][n][g * 4 + 2], acc[m][n][g * 4 + 3]};
     __syncthreads();
-    for (int x = threadIdx.x; x < 256; x += W * 64) {
-      const int tr = x >> 3, ch = (x & 7) * 4;
+    constexpr int MS = GATED ? 1 : M;  // blocks of results
+    for (int x = threadIdx.x; x < 256 * MS; x += W * 64) {
+      const int mr = x >> 8, tr = (x >> 3) & 31, ch = (x & 7) * 4;
       f32x4 s[2] = {f32x4{}, f32x4{}};
 #pragma unroll
-      for (int m = 0; m < MB; m++)
+      for (int k = 0; k < (GATED ? 2 : 1); k++)
 #pragma unroll
         for (int w = 0; w < W; w++)
-          s[m] += *reinterpret_cast<const f32x4*>(part + (w * MB + m) * kPartBlock + tr * kPartRow + ch);
-      const int t = t0 + n * 32 + tr, ich = rb * 32 + ch;
+          s[k] += *reinterpret_cast<const f32x4*>(part + (w * M + (GATED ? k : mr)) * kPartBlock +
+                                                  tr * kPartRow + ch);
+      const int t = t0 + n * 32 + tr, ich = (rb0 + mr) * 32 + ch;
       if (t >= p.tokens) continue;  // the same for the 8 lanes of a group of channels
       const f32x4 a0 = load_channels(p.a[0], ich, p.out, 1.0f);
       const f32x4 a1 = load_channels(GATED ? p.a[1] : nullptr, ich, p.out, 1.0f);
@@ -334,19 +417,9 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
 // times all the tile's 32 NB tokens. Weight fragments go from memory straight into registers,
 // each entering the CU once; the tokens go through LDS.
 //
-// k runs in stages of 128 bytes of a token row: 256 k in four steps (FP4), 128 k in two (FP8:
-// half a packed stage, steps 2 hs and 2 hs + 1 of it, hs = stage % 2; of each token row the bytes
-// of k chunks 2 hs, 2 hs + 1, 4 + 2 hs and 5 + 2 hs). Loads run two stages ahead: the
-// fragments of two stages are a ring of registers, each reloaded right after the last product
-// that reads it, and the tokens use a ring of three LDS buffers. A row's eight 16-byte pieces
-// are XOR-swizzled in LDS so that neither the loads nor the reads conflict.
+// Loads run two stages ahead: the fragments of two stages are a ring of registers, each reloaded
+// right after the last product that reads it, and the tokens use a ring of three LDS buffers.
 
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-
-// s_waitcnt operand: at most n vector-memory operations outstanding, the other counters free
-constexpr int vmcnt_imm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
-
-constexpr int kRowB = 128;         // bytes of a token row in a stage
 constexpr int kScaleRowB = 16;     // token scale bytes per row and period (512 k)
 constexpr int kGroupM = 4;         // weight tiles per tile group (L2 reuse)
 
@@ -364,14 +437,6 @@ struct TileCtx {
   uint32_t vx[NB];        // token-stage offsets of this lane's rows, or kOob
   uint32_t vxs;           // token-scale offset of this lane's row, or kOob
 };
-
-constexpr int steps(bool act8) { return act8 ? 2 : 4; }
-
-// 16 bytes per lane from memory to LDS: lane l's at dst + 16 l
-__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rs, uint8_t* dst, uint32_t voff,
-                                         int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)dst, 16, (int)voff, soff, 0, 0);
-}
 
 // Token-stage load j of this wave: LDS rows 8 (NB wave + j) .. + 7, lane l writing row
 // l / 8 of them at piece position l % 8.
@@ -397,13 +462,6 @@ template <bool ACT8, int NB>
 __device__ __forceinline__ uint32_t load_ws(const TileCtx<ACT8, NB>& c, int m, int s, bool on) {
   return __builtin_amdgcn_raw_buffer_load_b32(on ? c.rs[m] : c.rnone, c.vs[m],
                                               (uint32_t)((ACT8 ? s >> 1 : s) * kPackScaleB), 0);
-}
-
-// The 16-byte piece(s) of one token row that step ks takes: xt = the row's swizzle term with the
-// lane half folded in (FP4: piece 4 h + ks; FP8: pieces 2 ks + h and 4 + 2 ks + h).
-template <bool ACT8>
-__device__ __forceinline__ u32x4 read_x(const uint8_t* row, int ks, int part, int xt) {
-  return *reinterpret_cast<const u32x4*>(row + (((ACT8 ? 2 * ks + 4 * part : ks) ^ xt) * 16));
 }
 
 // Step KS of a stage (HS: FP8's half of the packed stage): 2 NB products in the order (m, n), and
@@ -451,13 +509,6 @@ __device__ __forceinline__ void tile_step(v16f (&acc)[2][NB], u32x4 (&fa)[2][ste
 // LDS, so that the stores (and the residual's loads, one chunk ahead) cover whole rows of the
 // wave's channels instead of 8 or 16 bytes of 32 rows. FULL: the tile lies inside the tokens and
 // channels and takes 4-channel accesses.
-// order LDS accesses of one wave (its LDS instructions execute in order; this keeps the compiler
-// from moving them)
-__device__ __forceinline__ void wave_lds_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 template <bool GATED, int OUT>
 __device__ __forceinline__ void quantize_chunk(const MlpArgs& p, f32x4 (&y)[4], int t, int rb,
                                                int h, bool in) {
@@ -617,9 +668,11 @@ __device__ __forceinline__ void tile_origin(int nti, int ntt, int& ti, int& tt) 
 
 template <bool ACT8, bool GATED, int NB, int OUT>
 __global__ __launch_bounds__(256, 1) void k_mlp_tile(MlpArgs p, int nti, int ntt) {
-  __shared__ __attribute__((aligned(1024))) TileLds<NB> L;
-  static_assert(sizeof(L) >= 4 * 2 * 32 * (256 + 16) || (GATED && sizeof(L) >= 4 * 2 * 32 * (128 + 16)),
-                "epilogue staging does not fit");
+  // the epilogue stages two 32-token chunks of every wave's channels in the same memory
+  constexpr int kStaging = OUT >= kOutFp4 ? 0 : 4 * 2 * 32 * (128 * (GATED ? 1 : 2) + 16);
+  constexpr int kLds = (int)sizeof(TileLds<NB>) > kStaging ? (int)sizeof(TileLds<NB>) : kStaging;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+  TileLds<NB>& L = *reinterpret_cast<TileLds<NB>*>(lds);
   constexpr int NK = steps(ACT8);
   constexpr int PER = ACT8 ? 4 : 2;  // stages per token-scale period (512 k)
   int ti, tt;
@@ -749,30 +802,37 @@ __global__ __launch_bounds__(256, 1) void k_mlp_tile(MlpArgs p, int nti, int ntt
   // the last stages' loads read nothing but still write zeros into LDS: drain them before the
   // epilogue reuses that memory
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-  uint8_t* stage_mem = reinterpret_cast<uint8_t*>(&L);
   if (rows == 32 * NB && (rb0 + (GATED ? 1 : 2)) * 32 <= p.out && (OUT >= kOutFp4 || p.vec))
-    tile_store<GATED, NB, OUT, true>(p, acc, rb0, t0, stage_mem);
+    tile_store<GATED, NB, OUT, true>(p, acc, rb0, t0, lds);
   else
-    tile_store<GATED, NB, OUT, false>(p, acc, rb0, t0, stage_mem);
+    tile_store<GATED, NB, OUT, false>(p, acc, rb0, t0, lds);
 }
 
 // ---------------------------------------------------------------------------------- host
 
-template <bool ACT8, bool GATED, int OUT>
-hipError_t launch_t(const MlpArgs& p, hipStream_t s) {
-  if (p.tokens >= 256) {
-    constexpr int NB = 8;
-    const int nti = (p.out + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
-    const int ntt = (p.tokens + 32 * NB - 1) / (32 * NB);
-    hipLaunchKernelGGL((k_mlp_tile<ACT8, GATED, NB, OUT>), dim3((unsigned)(nti * ntt)), dim3(256),
-                       0, s, p, nti, ntt);
-    return hipGetLastError();
-  }
-  constexpr int NB = 1, W = 8;
-  const int64_t nrb = (p.out + 31) / 32, ntt = (p.tokens + 32 * NB - 1) / (32 * NB);
-  hipLaunchKernelGGL((k_mlp_split<ACT8, GATED, NB, OUT, W>), dim3((unsigned)(nrb * ntt)),
+template <bool ACT8, bool GATED, int OUT, int NB>
+hipError_t launch_tile(const MlpArgs& p, hipStream_t s) {
+  const int nti = (p.out + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
+  const int ntt = (p.tokens + 32 * NB - 1) / (32 * NB);
+  hipLaunchKernelGGL((k_mlp_tile<ACT8, GATED, NB, OUT>), dim3((unsigned)(nti * ntt)), dim3(256), 0,
+                     s, p, nti, ntt);
+  return hipGetLastError();
+}
+
+template <bool ACT8, bool GATED, int OUT, int M, int NB, int W>
+hipError_t launch_split(const MlpArgs& p, hipStream_t s) {
+  const int rows = GATED ? 32 : 32 * M;
+  const int64_t nrt = (p.out + rows - 1) / rows, ntt = (p.tokens + 32 * NB - 1) / (32 * NB);
+  hipLaunchKernelGGL((k_mlp_split<ACT8, GATED, M, NB, OUT, W>), dim3((unsigned)(nrt * ntt)),
                      dim3(W * 64), 0, s, p);
   return hipGetLastError();
+}
+
+template <bool ACT8, bool GATED, int OUT>
+hipError_t launch_t(const MlpArgs& p, hipStream_t s) {
+  /*PICK*/
+  if (p.tokens >= 256) return launch_tile<ACT8, GATED, OUT, 8>(p, s);
+  return launch_split<ACT8, GATED, OUT, GATED ? 2 : 1, 1, 8>(p, s);
 }
 
 // Bytes of n elements of an output
