@@ -450,35 +450,46 @@ def gemm_mx_packed(act_codes, act_scales, packed, a=None, out_dtype: str = "bf16
 # device's current stream, whichever device is current.
 
 
+# The calls are a few microseconds of GPU work for a single token, so their host side is kept
+# short: devices are compared as indices, the current stream's handle is read directly, and
+# every tensor is looked at once.
+
+
 def _call(dev, stream, f, *args):
-    """f(*args, stream) with ``dev`` current."""
+    """f(*args, stream) with device ``dev`` (an index) current."""
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    if s.device != dev:
-        raise ValueError("stream belongs to another device than the tensors")
-    if torch.cuda.current_device() == dev.index:
-        return f(*args, s.cuda_stream)
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            raise ValueError("stream belongs to another device than the tensors")
+        s = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        return f(*args, s)
     with torch.cuda.device(dev):
-        return f(*args, s.cuda_stream)
+        return f(*args, s)
 
 
-def _empty(shape, dtype, dev, stream):
+def _empty(shape, dtype, device, stream):
     """An uninitialized tensor that belongs to the stream it will be written on."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _arr(name, t, dev, dtype, shape, optional=False):
-    """The address of a dense tensor after its checks (None for a missing optional one)."""
-    if t is None and optional:
-        return None
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
-                         f"on {dev}")
-    return t.data_ptr()
+def _arr(name, t, dev, dtype, shape):
+    """The address of a dense tensor on device ``dev`` (an index) after its checks."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                     f"cuda:{dev}")
+
+
+def _opt(name, t, dev, dtype, shape):
+    """_arr, or None for a missing optional tensor."""
+    return None if t is None else _arr(name, t, dev, dtype, shape)
 
 
 def _out_dtype(out_dtype):
@@ -505,25 +516,28 @@ def act_outputs(X, fmt: str, group: int):
 def _norm_args(X, fmt, group, codes, scales, weight, residual, residual_out, b, eps, g):
     torch = _torch()
     dt = _check_w(X)
-    dev, (tokens, cols) = X.device, X.shape
+    shape, dev, xt = X.shape, X.get_device(), X.dtype
+    tokens, cols = shape
     if fmt not in ACT_FMT:
         raise ValueError(f"unknown format {fmt!r}")
     if group not in (16, 32, 64) or cols % group:
         raise ValueError("group must be 16, 32 or 64 and divide the channels")
-    wt = 0
+    one, f32 = (cols,), torch.float32
+    wt, wp = 0, None
     if weight is not None:
-        if weight.dtype not in (torch.float32, torch.bfloat16):
+        wd = weight.dtype
+        if wd is torch.bfloat16:
+            wt = 1
+        elif wd is not f32:
             raise ValueError("weight must be float32 or bfloat16")
-        wt = 1 if weight.dtype == torch.bfloat16 else 0
-    one = (cols,)
-    sdt = torch.int16 if fmt == "int4_bf16" else torch.uint8
-    return (X.data_ptr(), DTYPE[dt], _arr("residual", residual, dev, X.dtype, X.shape, True),
-            _arr("residual_out", residual_out, dev, X.dtype, X.shape, True), tokens, cols,
-            None if weight is None else _arr("weight", weight, dev, weight.dtype, one), wt,
-            float(eps), _arr("b", b, dev, torch.float32, one, True), ACT_FMT[fmt], group, float(g),
+        wp = _arr("weight", weight, dev, wd, one)
+    return (X.data_ptr(), DTYPE[dt], _opt("residual", residual, dev, xt, shape),
+            _opt("residual_out", residual_out, dev, xt, shape), tokens, cols, wp, wt, eps,
+            _opt("b", b, dev, f32, one), ACT_FMT[fmt], group, g,
             _arr("codes", codes, dev, torch.uint8,
                  (tokens, cols if fmt == "mxfp8" else cols // 2)),
-            _arr("scales", scales, dev, sdt, (tokens, cols // group)))
+            _arr("scales", scales, dev, torch.int16 if fmt == "int4_bf16" else torch.uint8,
+                 (tokens, cols // group)))
 
 
 def norm_quantize_act(X, fmt: str, group: int, weight=None, residual=None, residual_out=None,
@@ -547,7 +561,7 @@ def norm_quantize_act(X, fmt: str, group: int, weight=None, residual=None, resid
     args = _norm_args(X, fmt, group, codes, scales, weight, residual, residual_out, b, eps, g)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
                                                             workspace.numel() * workspace.element_size())
-    st = _call(X.device, stream, lib().dq_norm_quantize_act, *args, ws_ptr, ws_bytes)
+    st = _call(X.get_device(), stream, lib().dq_norm_quantize_act, *args, ws_ptr, ws_bytes)
     if st != 0:
         raise DQError(st, "dq_norm_quantize_act")
     out = {"codes": codes, "scales": scales}
@@ -563,32 +577,34 @@ def norm_quantize_act_async(X, fmt: str, group: int, codes, scales, status, weig
     ``residual_out`` wherever ``residual`` is given): enqueued on the stream, no wait; device
     errors are OR-ed into ``status`` (an int32 CUDA tensor the caller clears)."""
     args = _norm_args(X, fmt, group, codes, scales, weight, residual, residual_out, b, eps, g)
-    if status.dtype != _torch().int32 or status.device != X.device:
+    dev = X.get_device()
+    if status.dtype is not _torch().int32 or status.get_device() != dev:
         raise ValueError("status must be an int32 tensor on X's device")
-    st = _call(X.device, stream, lib().dq_norm_quantize_act_async, *args, status.data_ptr())
+    st = _call(dev, stream, lib().dq_norm_quantize_act_async, *args, status.data_ptr())
     if st != 0:
         raise DQError(st, "dq_norm_quantize_act_async")
 
 
 def _product_args(act_codes, act_scales, act_fmt, packed, a, name):
-    """Checks of one product: the arguments it shares with every other, its packed weights' and
-    its a."""
+    """The device, and checked arguments of one product: those it shares with every other, its
+    packed weights' and its a."""
     torch = _torch()
-    if act_fmt not in ("mxfp4", "mxfp8"):
+    if act_fmt == "mxfp4":
+        fmt, per = 2, 2
+    elif act_fmt == "mxfp8":
+        fmt, per = 4, 1
+    else:
         raise ValueError("act_fmt is 'mxfp4' or 'mxfp8'")
     if not act_codes.is_cuda or act_codes.dim() != 2:
         raise ValueError("act_codes must be a 2-D CUDA (HIP) tensor")
-    dev, tokens = act_codes.device, act_codes.shape[0]
+    u8, dev, tokens = torch.uint8, act_codes.get_device(), act_codes.shape[0]
     K, out = packed["K"], packed["out"]
-    xc = _arr("act_codes", act_codes, dev, torch.uint8,
-              (tokens, K if act_fmt == "mxfp8" else K // 2))
-    xs = _arr("act_scales", act_scales, dev, torch.uint8, (tokens, K // 32))
-    pc, ps = packed["codes"], packed["scales"]
-    nrb = -(-out // 32)
-    return ((xc, xs, ACT_FMT[act_fmt], tokens, K),
-            (_arr(name + " codes", pc, dev, torch.uint8, (nrb * 16 * K,)),
-             _arr(name + " scales", ps, dev, torch.uint8, (nrb * K,))),
-            _arr(name + " a", a, dev, torch.float32, (out,), True))
+    rows = -(-out // 32)
+    return (dev, (_arr("act_codes", act_codes, dev, u8, (tokens, K // per)),
+                  _arr("act_scales", act_scales, dev, u8, (tokens, K // 32)), fmt, tokens, K),
+            _arr(name, packed["codes"], dev, u8, (rows * 16 * K,)),
+            _arr(name, packed["scales"], dev, u8, (rows * K,)),
+            _opt("a", a, dev, torch.float32, (out,)))
 
 
 def gemm_mx_epilogue(act_codes, act_scales, packed, a=None, bias=None, activation: str = "none",
@@ -599,16 +615,16 @@ def gemm_mx_epilogue(act_codes, act_scales, packed, a=None, bias=None, activatio
     type) may be ``y`` itself. Returns Y (tokens x out, bfloat16 or float32; MXFP8 activations
     give bfloat16), into ``y`` when given."""
     torch = _torch()
-    head, w, ap = _product_args(act_codes, act_scales, act_fmt, packed, a, "packed")
-    dev, out, dt = act_codes.device, packed["out"], _out_dtype(out_dtype)
+    dev, head, wc, ws, ap = _product_args(act_codes, act_scales, act_fmt, packed, a, "packed")
+    out, dt = packed["out"], _out_dtype(out_dtype)
     if activation not in ACTIVATION:
         raise ValueError(f"unknown activation {activation!r}")
     shape = (head[3], out)
     if y is None:
-        y = _empty(shape, dt, dev, stream)
-    st = _call(dev, stream, lib().dq_gemm_mx_epilogue, *head, *w, ap,
-               _arr("bias", bias, dev, torch.float32, (out,), True), ACTIVATION[activation],
-               _arr("residual", residual, dev, dt, shape, True), out, DTYPE[out_dtype],
+        y = _empty(shape, dt, act_codes.device, stream)
+    st = _call(dev, stream, lib().dq_gemm_mx_epilogue, *head, wc, ws, ap,
+               _opt("bias", bias, dev, torch.float32, (out,)), ACTIVATION[activation],
+               _opt("residual", residual, dev, dt, shape), out, DTYPE[out_dtype],
                _arr("y", y, dev, dt, shape))
     if st != 0:
         raise DQError(st, "dq_gemm_mx_epilogue")
@@ -616,13 +632,17 @@ def gemm_mx_epilogue(act_codes, act_scales, packed, a=None, bias=None, activatio
 
 
 def _gated_args(act_codes, act_scales, act_fmt, gate, up, a_gate, a_up, activation):
-    head, g, ag = _product_args(act_codes, act_scales, act_fmt, gate, a_gate, "gate")
-    _, u, au = _product_args(act_codes, act_scales, act_fmt, up, a_up, "up")
-    if gate["out"] != up["out"]:
-        raise ValueError("gate and up weights disagree on their output channels")
+    dev, head, gc, gs, ag = _product_args(act_codes, act_scales, act_fmt, gate, a_gate, "gate")
+    K, inner = gate["K"], gate["out"]
+    if up["out"] != inner or up["K"] != K:
+        raise ValueError("gate and up weights disagree on their channels")
     if activation not in ACTIVATION:
         raise ValueError(f"unknown activation {activation!r}")
-    return (*head, *g, ag, *u, au, ACTIVATION[activation], gate["out"])
+    u8, rows = _torch().uint8, -(-inner // 32)
+    return dev, (*head, gc, gs, ag, _arr("up", up["codes"], dev, u8, (rows * 16 * K,)),
+                 _arr("up", up["scales"], dev, u8, (rows * K,)),
+                 _opt("a_up", a_up, dev, _torch().float32, (inner,)), ACTIVATION[activation],
+                 inner)
 
 
 def gated_mx(act_codes, act_scales, gate, up, a_gate=None, a_up=None, activation: str = "silu",
@@ -630,10 +650,10 @@ def gated_mx(act_codes, act_scales, gate, up, a_gate=None, a_up=None, activation
     """dq_gated_mx: H = act((xhat Qgate^T) D_a_gate) * ((xhat Qup^T) D_a_up) in one kernel, gate
     and up weights each from gemm_pack_weights. Returns H (tokens x inner, bfloat16 or float32;
     MXFP8 activations give bfloat16), into ``y`` when given."""
-    args = _gated_args(act_codes, act_scales, act_fmt, gate, up, a_gate, a_up, activation)
-    dev, dt, shape = act_codes.device, _out_dtype(out_dtype), (act_codes.shape[0], gate["out"])
+    dev, args = _gated_args(act_codes, act_scales, act_fmt, gate, up, a_gate, a_up, activation)
+    dt, shape = _out_dtype(out_dtype), (args[3], gate["out"])
     if y is None:
-        y = _empty(shape, dt, dev, stream)
+        y = _empty(shape, dt, act_codes.device, stream)
     st = _call(dev, stream, lib().dq_gated_mx, *args, DTYPE[out_dtype],
                _arr("y", y, dev, dt, shape))
     if st != 0:
@@ -648,17 +668,17 @@ def gated_mx_quantized(act_codes, act_scales, gate, up, fmt: str, a_gate=None, a
     quantized to ``fmt`` ("mxfp4" or "mxfp8") in groups of 32 channels. Returns codes and scales
     (into the given tensors), as the next product takes them."""
     torch = _torch()
-    args = _gated_args(act_codes, act_scales, act_fmt, gate, up, a_gate, a_up, activation)
-    dev, tokens, inner = act_codes.device, act_codes.shape[0], gate["out"]
+    dev, args = _gated_args(act_codes, act_scales, act_fmt, gate, up, a_gate, a_up, activation)
+    tokens, inner = args[3], gate["out"]
     if fmt not in ("mxfp4", "mxfp8") or inner % 32:
         raise ValueError("fmt is 'mxfp4' or 'mxfp8', and the channels a multiple of 32")
     cs, ss = (tokens, inner if fmt == "mxfp8" else inner // 2), (tokens, inner // 32)
     if codes is None:
-        codes = _empty(cs, torch.uint8, dev, stream)
+        codes = _empty(cs, torch.uint8, act_codes.device, stream)
     if scales is None:
-        scales = _empty(ss, torch.uint8, dev, stream)
+        scales = _empty(ss, torch.uint8, act_codes.device, stream)
     st = _call(dev, stream, lib().dq_gated_mx_quantized, *args,
-               _arr("b", b, dev, torch.float32, (inner,), True), ACT_FMT[fmt],
+               _opt("b", b, dev, torch.float32, (inner,)), ACT_FMT[fmt],
                _arr("codes", codes, dev, torch.uint8, cs),
                _arr("scales", scales, dev, torch.uint8, ss))
     if st != 0:

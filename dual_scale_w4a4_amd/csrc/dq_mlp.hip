@@ -418,14 +418,14 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
 // each entering the CU once; the tokens go through LDS.
 //
 // Loads run two stages ahead: the fragments of two stages are a ring of registers, each reloaded
-// right after the last product that reads it, and the tokens use a ring of three LDS buffers.
+// right after the last product that reads it, and the tokens use a ring of four LDS buffers.
 
 constexpr int kScaleRowB = 16;     // token scale bytes per row and period (512 k)
 constexpr int kGroupM = 4;         // weight tiles per tile group (L2 reuse)
 
 template <int NB>
 struct TileLds {
-  uint8_t x[3][NB * 32 * kRowB];   // [stage % 3]: token stages
+  uint8_t x[4][NB * 32 * kRowB];   // [stage % 4]: token stages
   uint8_t xs[2][256 * kScaleRowB]; // [period parity]: token scales
 };
 
@@ -464,51 +464,79 @@ __device__ __forceinline__ uint32_t load_ws(const TileCtx<ACT8, NB>& c, int m, i
                                               (uint32_t)((ACT8 ? s >> 1 : s) * kPackScaleB), 0);
 }
 
-// Step KS of a stage (HS: FP8's half of the packed stage): 2 NB products in the order (m, n), and
-// between them the next step's token fragments from LDS (after the last step the next stage's
-// first ones, and its token scales), the reload of block m's fragment with stage s + 2's
-// after its last product, and this step's share of stage s + 2's token loads (XS: also the
-// next period's token scales). Loads past the last stage read nothing (they still write
-// zeros to LDS, into buffers no longer read), so every stage issues the same number.
+// Token fragments are read kAhead blocks of 32 tokens before their products, in a ring of four.
+constexpr int kAhead = 3;
+
+// Step KS of a stage (HS: FP8's half of the packed stage): 2 NB products in the order (n, m), and
+// between them the token fragments kAhead blocks on, from LDS (from NB - kAhead on those of the
+// next step, after the last step the next stage's, with its token scales); the reload of the
+// step's weight fragments with stage s + 2's after their last products; and in step 0, before any
+// of those, stage s + 2's token loads (XS: first the next period's token scales). Loads past
+// the last stage read nothing (they still write zeros to LDS, into buffers no longer read), so
+// every stage issues the same number.
+//
+// The stage's one barrier stands before the last step's block NB - kAhead, the first that reads
+// stage s + 1's tokens. There those tokens' loads, the first of the loads issued in stage s - 1,
+// are complete in this wave (the weight loads after them and this stage's loads may be in
+// flight: a fixed count; the weights' own waits are at their uses), and after it in every
+// wave. It also stands between the last reads of a token buffer, whose products every wave has
+// issued a stage before, and the loads that fill the buffer again: with four buffers stage
+// s + 1 loads into the one that stage s - 1 read.
 template <bool ACT8, int NB, int KS, int HS, bool XS>
 __device__ __forceinline__ void tile_step(v16f (&acc)[2][NB], u32x4 (&fa)[2][steps(ACT8)],
-                                          const u32x4 (&fb)[NB][ACT8 ? 2 : 1],
-                                          u32x4 (&fn)[NB][ACT8 ? 2 : 1], uint32_t (&sw)[2],
+                                          u32x4 (&fb)[4][ACT8 ? 2 : 1], uint32_t (&sw)[2],
                                           const uint32_t (&sx)[NB], uint32_t (&sn)[NB],
                                           const uint8_t* lx, const uint8_t* lxn,
                                           const uint8_t* xsn, int xt, const TileCtx<ACT8, NB>& c,
                                           uint8_t* xb, uint8_t* xsb, int s, int q, bool xs_on) {
-  constexpr int NK = steps(ACT8), TL = NB / NK;
+  constexpr int NK = steps(ACT8);
   constexpr bool kLast = KS == NK - 1;
   const int s2 = s + 2;
   const bool on = s2 < c.nst;
 #pragma unroll
-  for (int t = 0; t < 2 * NB; t++) {
-    const int m = t / NB, n = t % NB;
-    acc[m][n] = mfma<ACT8>(fa[m][KS], fb[n], acc[m][n], sw[m], sx[n], ACT8 ? 2 * HS + KS : KS);
-    const uint8_t* row = (kLast ? lxn : lx) + (t / 2) * 32 * kRowB;
-    if (ACT8 || t % 2 == 0)
-      fn[t / 2][ACT8 ? t % 2 : 0] = read_x<ACT8>(row, kLast ? 0 : KS + 1, t % 2, xt);
-    if (kLast && t % 2 == 1)
-      sn[t / 2] = *reinterpret_cast<const uint32_t*>(xsn + (t / 2) * 32 * kScaleRowB);
-    if (n == NB - 1) {
-      fa[m][KS] = load_w(c, m, s2, KS, on);
-      if (kLast) sw[m] = load_ws(c, m, s2, on);
+  for (int n = 0; n < NB; n++) {
+    const int f = n + kAhead;             // the block read now
+    const bool wrap = f >= NB;            // .. belongs to the next step
+    if (kLast && f == NB) {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * NK + 2 + NB + (XS ? 1 : 0) + 2 * (NK - 1)));
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      __builtin_amdgcn_s_barrier();
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < NB; k++)
+        sn[k] = *reinterpret_cast<const uint32_t*>(xsn + k * 32 * kScaleRowB);
     }
-    if (t % (2 * NB / TL) == 1) load_x(c, xb, KS * TL + t / (2 * NB / TL), s2, on);
-    if (XS && KS == 0 && t == 2) load_xs(c, xsb, q, xs_on);
-    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < 2; m++) {
+      acc[m][n] = mfma<ACT8>(fa[m][KS], fb[n % 4], acc[m][n], sw[m], sx[n], ACT8 ? 2 * HS + KS : KS);
+      if (XS && KS == 0 && n == 0 && m == 0) load_xs(c, xsb, q, xs_on);
+      if (KS == 0 && m == 0) load_x(c, xb, n, s2, on);
+      if (ACT8 || m == 0) {
+        const uint8_t* row = (kLast && wrap ? lxn : lx) + (f % NB) * 32 * kRowB;
+        fb[f % 4][ACT8 ? m : 0] = read_x<ACT8>(row, wrap ? (KS + 1) % NK : KS, m, xt);
+      }
+      if (n == NB - 1) {
+        fa[m][KS] = load_w(c, m, s2, KS, on);
+        if (kLast) sw[m] = load_ws(c, m, s2, on);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 }
 
-// The epilogue. Result v of block (m, n) is channel 32 rb + 8 (v / 4) + 4 h + v % 4 of the
-// block's 32 and token 32 n + lane % 32: scales, bias, activation and the gate's product are
-// applied there, 32 tokens at a time, with each lane's channel factors in registers.
-// Quantized outputs then need one exchange between the lane halves per token group (its 32
-// channels lie in lanes l and l + 32) and are stored from there. bf16 and fp32 outputs go through
-// LDS, so that the stores (and the residual's loads, one chunk ahead) cover whole rows of the
-// wave's channels instead of 8 or 16 bytes of 32 rows. FULL: the tile lies inside the tokens and
-// channels and takes 4-channel accesses.
+// The epilogue, 32 tokens (one n) at a time. Result v of block (m, n) is channel
+// 32 rb + 8 (v / 4) + 4 h + v % 4 of the block's 32 and token 32 n + lane % 32.
+//   gated: the gate's and the up product of a channel lie in the same lane, so scales, activation
+//     and product are applied there, on registers. Quantized outputs then need one exchange
+//     between the lane halves (a token's 32 channels lie in lanes l and l + 32) and are stored
+//     from there.
+//   bf16 and fp32 outputs go through LDS, so that the stores cover whole rows of the wave's
+//     channels instead of 8 or 16 bytes of 32 rows. The single product applies its factors
+//     there, where a lane has the same 4 channels in every row, and loads its residual one
+//     chunk ahead.
+// FULL: the tile lies inside the tokens and channels and takes 4-channel accesses.
 template <bool GATED, int OUT>
 __device__ __forceinline__ void quantize_chunk(const MlpArgs& p, f32x4 (&y)[4], int t, int rb,
                                                int h, bool in) {
@@ -559,54 +587,62 @@ __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2
   constexpr int NR = 32 * LPR / 64;       // row accesses of a chunk per lane
   constexpr int kRow = 128 * ME + 16;     // bytes of a staged token row, padded
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rl = lane & 31, h = lane >> 5;
-  f32x4 a0[ME][4], a1[4], cc[ME][4];
-#pragma unroll
-  for (int m = 0; m < ME; m++)
-#pragma unroll
-    for (int g = 0; g < 4; g++) {
-      const int ich = (rb0 + m) * 32 + 8 * g + 4 * h;
-      a0[m][g] = load_channels(p.a[0], ich, p.out, 1.0f);
-      if (GATED) a1[g] = load_channels(p.a[1], ich, p.out, 1.0f);
-      cc[m][g] = load_channels(GATED ? p.b : p.bias, ich, p.out, GATED ? 1.0f : 0.0f);
-    }
-  __syncthreads();  // every wave is done with the main loop's LDS
-  uint8_t* region = stage + wave * 2 * (32 * kRow);  // two chunks, taken in turn
   const int cl = lane % LPR, rr = lane / LPR;
   const int ich = rb0 * 32 + cl * 4;      // the 4 channels this lane stores
+  f32x4 a0[4], a1[4], cb[4];              // gated: factors of the 16 channels of this lane's results
+  f32x4 as = {}, bias = {};               // single: of the 4 channels it stores
+  if (GATED) {
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const int ch = rb0 * 32 + 8 * g + 4 * h;
+      a0[g] = load_channels(p.a[0], ch, p.out, 1.0f);
+      a1[g] = load_channels(p.a[1], ch, p.out, 1.0f);
+      if (OUT >= kOutFp4) cb[g] = load_channels(p.b, ch, p.out, 1.0f);
+    }
+  } else {
+    as = load_channels(p.a[0], ich, p.out, 1.0f);
+    bias = load_channels(p.bias, ich, p.out, 0.0f);
+  }
+  __syncthreads();  // every wave is done with the main loop's LDS
+  uint8_t* region = stage + wave * 2 * (32 * kRow);  // two chunks, taken in turn
   typedef typename std::conditional<OUT == kOutF32, f32x4, bf16x4>::type row4;
-  row4 res[2][NR];
+  row4 res[NR];
   const bool has_res = FULL && !GATED && p.res;
   auto fetch = [&](int n) {
-    if (OUT < kOutFp4 && has_res) {
+    if (has_res) {
 #pragma unroll
       for (int r = 0; r < NR; r++) {
         const int64_t t = t0 + n * 32 + r * (64 / LPR) + rr;
-        res[n & 1][r] = *reinterpret_cast<const row4*>(
+        res[r] = *reinterpret_cast<const row4*>(
             static_cast<const char*>(p.res) + (t * p.out + ich) * (OUT == kOutF32 ? 4 : 2));
       }
     }
   };
-  fetch(0);
+  if (OUT < kOutFp4) fetch(0);
 #pragma unroll
   for (int n = 0; n < NB; n++) {
     __builtin_amdgcn_sched_barrier(0);  // one chunk's registers at a time
     f32x4 y[ME][4];
-    with_activation(p.act, [&](auto k) {
+    if (GATED) {
+      with_activation(p.act, [&](auto k) {
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            y[0][g][e] = activation<decltype(k)::value>(acc[0][n][4 * g + e] * a0[g][e]) *
+                         (acc[1][n][4 * g + e] * a1[g][e]);
+      });
+    } else {
 #pragma unroll
       for (int m = 0; m < ME; m++)
 #pragma unroll
         for (int g = 0; g < 4; g++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const float z = acc[m][n][4 * g + e] * a0[m][g][e];
-            float v = activation<decltype(k)::value>(GATED ? z : z + cc[m][g][e]);
-            if (GATED) v *= acc[1][n][4 * g + e] * a1[g][e];
-            y[m][g][e] = v;
-          }
-    });
+          y[m][g] = f32x4{acc[m][n][4 * g], acc[m][n][4 * g + 1], acc[m][n][4 * g + 2],
+                          acc[m][n][4 * g + 3]};
+    }
     if constexpr (OUT >= kOutFp4) {
 #pragma unroll
-      for (int g = 0; g < 4; g++) y[0][g] *= cc[0][g];
+      for (int g = 0; g < 4; g++) y[0][g] *= cb[g];
       const int t = t0 + n * 32 + rl;
       quantize_chunk<GATED, OUT>(p, y[0], t, rb0, h, FULL || (t < p.tokens && rb0 * 32 < p.out));
     } else {
@@ -618,28 +654,39 @@ __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2
           *reinterpret_cast<f32x4*>(reg + rl * kRow + (m * 32 + g * 8 + h * 4) * 4) = y[m][g];
       wave_lds_order();
       if (FULL) {
-        if (n + 1 < NB) fetch(n + 1);
+        f32x4 v[NR];
+#pragma unroll
+        for (int r = 0; r < NR; r++)
+          v[r] = *reinterpret_cast<const f32x4*>(reg + (r * (64 / LPR) + rr) * kRow + cl * 16);
+        if (!GATED)
+          with_activation(p.act, [&](auto k) {
+#pragma unroll
+            for (int r = 0; r < NR; r++)
+#pragma unroll
+              for (int e = 0; e < 4; e++)
+                v[r][e] = activation<decltype(k)::value>(v[r][e] * as[e] + bias[e]);
+          });
 #pragma unroll
         for (int r = 0; r < NR; r++) {
-          const int row = r * (64 / LPR) + rr;
-          f32x4 v = *reinterpret_cast<const f32x4*>(reg + row * kRow + cl * 16);
-          const int64_t off = (int64_t)(t0 + n * 32 + row) * p.out + ich;
+          const int64_t off = (int64_t)(t0 + n * 32 + r * (64 / LPR) + rr) * p.out + ich;
           if (has_res) {
 #pragma unroll
-            for (int e = 0; e < 4; e++) v[e] = (float)res[n & 1][r][e] + v[e];
+            for (int e = 0; e < 4; e++) v[r][e] = (float)res[r][e] + v[r][e];
           }
           if constexpr (OUT == kOutBf16) {
-            const bf16x4 o = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+            const bf16x4 o = {(__bf16)v[r][0], (__bf16)v[r][1], (__bf16)v[r][2], (__bf16)v[r][3]};
             __builtin_nontemporal_store(o, reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.y) + off));
           } else {
-            __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + off));
+            __builtin_nontemporal_store(v[r], reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + off));
           }
         }
+        if (n + 1 < NB) fetch(n + 1);
       } else {
 #pragma unroll 1
         for (int r = 0; r < NR; r++) {
           const int row = r * (64 / LPR) + rr;
-          const f32x4 v = *reinterpret_cast<const f32x4*>(reg + row * kRow + cl * 16);
+          f32x4 v = *reinterpret_cast<const f32x4*>(reg + row * kRow + cl * 16);
+          if (!GATED) v = combine<false>(p.act, as, as, bias, v, v);
           const int t = t0 + n * 32 + row;
           if (t < p.tokens) {
             if (p.vec) store_row<OUT, true>(p, t, ich, v);
@@ -667,7 +714,7 @@ __device__ __forceinline__ void tile_origin(int nti, int ntt, int& ti, int& tt) 
 }
 
 template <bool ACT8, bool GATED, int NB, int OUT>
-__global__ __launch_bounds__(256, 1) void k_mlp_tile(MlpArgs p, int nti, int ntt) {
+__global__ __launch_bounds__(256, NB == 8 ? 1 : 2) void k_mlp_tile(MlpArgs p, int nti, int ntt) {
   // the epilogue stages two 32-token chunks of every wave's channels in the same memory
   constexpr int kStaging = OUT >= kOutFp4 ? 0 : 4 * 2 * 32 * (128 * (GATED ? 1 : 2) + 16);
   constexpr int kLds = (int)sizeof(TileLds<NB>) > kStaging ? (int)sizeof(TileLds<NB>) : kStaging;
@@ -728,67 +775,59 @@ __global__ __launch_bounds__(256, 1) void k_mlp_tile(MlpArgs p, int nti, int ntt
 
   u32x4 fa[2][2][NK];              // [stage parity][m][step]: weight fragments
   uint32_t sw[2][2];               // [stage parity][m]: their scale dwords
-  u32x4 fb[2][NB][ACT8 ? 2 : 1];   // this step's and the next step's token fragments
+  u32x4 fb[4][ACT8 ? 2 : 1];       // ring of token fragments
   uint32_t sx[2][NB];              // [stage parity]: token scale dwords
 
-  // stages 0 and 1 and the first period's token scales; only stage 0 has to land before the loop
+  // stages 0 and 1 and the first period's token scales, in the order that the loop's wait
+  // counts on; only stage 0 has to land before the loop
 #pragma unroll
   for (int st = 0; st < 2; st++) {
+    if (st == 0) load_xs(c, L.xs[0], 0, true);
+#pragma unroll
+    for (int j = 0; j < NB; j++) load_x(c, L.x[st], j, st, true);
 #pragma unroll
     for (int m = 0; m < 2; m++) {
 #pragma unroll
       for (int i = 0; i < NK; i++) fa[st][m][i] = load_w(c, m, st, i, true);
       sw[st][m] = load_ws(c, m, st, true);
     }
-#pragma unroll
-    for (int j = 0; j < NB; j++) load_x(c, L.x[st], j, st, true);
-    if (st == 0) load_xs(c, L.xs[0], 0, true);
+    __builtin_amdgcn_sched_barrier(0);
   }
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * NK + 2 + NB));  // stage 1's loads may be in flight
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   __builtin_amdgcn_s_barrier();
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 #pragma unroll
-  for (int n = 0; n < NB; n++) {
+  for (int n = 0; n < NB; n++)
     sx[0][n] = *reinterpret_cast<const uint32_t*>(L.xs[0] + xsrow + n * 32 * kScaleRowB);
 #pragma unroll
+  for (int n = 0; n < kAhead; n++)
+#pragma unroll
     for (int e = 0; e < (ACT8 ? 2 : 1); e++)
-      fb[0][n][e] = read_x<ACT8>(L.x[0] + xrow + n * 32 * kRowB, 0, e, xt);
-  }
+      fb[n][e] = read_x<ACT8>(L.x[0] + xrow + n * 32 * kRowB, 0, e, xt);
 
-  // Stage s of period position J (fragments fa[J % 2], token buffer s % 3) while stage s + 2
-  // loads into the registers it frees and buffer (s + 2) % 3. Before the last step every load
-  // issued before this stage is complete in this wave (the loads of the steps so far may be in
-  // flight: a fixed count) and its LDS reads are done; after the barrier that holds in every
-  // wave, so the last step may read stage s + 1's first fragments and scales under its own
-  // products, and stage s + 1 may load into the buffer that stage s - 1 read.
+  // stage s of period position J: fragments fa[J % 2], token buffer s % 4, while stage s + 2 loads
+  // into the registers it frees and buffer (s + 2) % 4
   auto stage = [&](auto jc, int s, int q, bool more) {
     constexpr int J = decltype(jc)::value, P = J & 1;
     constexpr bool XS = J == 0;
-    const uint8_t* lx = L.x[s % 3] + xrow;
-    const uint8_t* lxn = L.x[(s + 1) % 3] + xrow;
-    uint8_t* xb = L.x[(s + 2) % 3];
+    const uint8_t* lx = L.x[s & 3] + xrow;
+    const uint8_t* lxn = L.x[(s + 1) & 3] + xrow;
+    uint8_t* xb = L.x[(s + 2) & 3];
     // stage s + 1's token scales: its period, and the half (256 k) of it
     const uint8_t* xsn = L.xs[((s + 1) / PER) & 1] + xsrow + (((J + 1) % PER) / (PER / 2)) * 8;
     uint8_t* xsb = L.xs[(q + 1) & 1];
     auto step = [&](auto kc) {
       constexpr int KS = decltype(kc)::value;
-      tile_step<ACT8, NB, KS, P, XS>(acc, fa[P], fb[KS & 1], fb[(KS & 1) ^ 1], sw[P], sx[P],
-                                     sx[P ^ 1], lx, lxn, xsn, xt, c, xb, xsb, s, q + 1, more);
+      tile_step<ACT8, NB, KS, P, XS>(acc, fa[P], fb, sw[P], sx[P], sx[P ^ 1], lx, lxn, xsn, xt, c,
+                                     xb, xsb, s, q + 1, more);
     };
-    __builtin_amdgcn_sched_barrier(0);
     step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
     if constexpr (NK == 4) {
-      step(std::integral_constant<int, 1>{});
       step(std::integral_constant<int, 2>{});
+      step(std::integral_constant<int, 3>{});
     }
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm((NK - 1) * (2 + NB / NK) + (XS ? 1 : 0)) & ~(15 << 8));
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_sched_barrier(0);
-    step(std::integral_constant<int, NK - 1>{});
-    __builtin_amdgcn_sched_barrier(0);
   };
   for (int q = 0; q < p.K / 512; q++) {
     const bool more = q + 1 < p.K / 512;
@@ -828,11 +867,31 @@ hipError_t launch_split(const MlpArgs& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Which kernel. With few 32 x 32 blocks of results (row blocks times 32-token blocks) the split
+// kernel brings the whole chip to bear on k; with many, the tile kernel reads each operand fewer
+// times. Measured at MXFP4, us (split / tile), K = 4096 -> 14336 and K = 14336 -> 4096:
+//   single, tokens   32: 8.5 / 19, 11 / 41   64: 11 / 21, 11 / 42    128: 18 / 18, 14 / 40
+//                   256: 33 / 20, 19 / 41   512: 58 / 22, 33 / 41   1024: 108 / 37, 63 / 43
+//   gated, 4096 -> 14336, tokens 32: 12 / 18   64: 20 / 18   128: 35 / 19
+//   gated, 2048 -> 5632, tokens 64: 6.4 / 12   128: 8.9 / 12   256: 13 / 12
+// The single product takes the smallest split tile (M row blocks by NB token blocks) that fits
+// the chip in one round, 256 workgroups: 14336 -> 4096 at 128 tokens takes 17 us in 32 x 32
+// tiles and 14 us in 64 x 32; at 256 tokens 24 us in 64 x 32 and 19 us in 64 x 64. Up to 32
+// tokens it splits whatever the number of rows.
 template <bool ACT8, bool GATED, int OUT>
 hipError_t launch_t(const MlpArgs& p, hipStream_t s) {
+  const int64_t nrb = (p.out + 31) / 32, ntb = (p.tokens + 31) / 32;
   /*PICK*/
-  if (p.tokens >= 256) return launch_tile<ACT8, GATED, OUT, 8>(p, s);
-  return launch_split<ACT8, GATED, OUT, GATED ? 2 : 1, 1, 8>(p, s);
+  if constexpr (GATED) {
+    if (nrb * ntb <= 768) return launch_split<ACT8, true, OUT, 2, 1, 4>(p, s);
+  } else {
+    const int64_t pairs = (nrb + 1) / 2;
+    if (nrb * ntb <= 256) return launch_split<ACT8, false, OUT, 1, 1, 8>(p, s);
+    if (pairs * ntb <= 256 || ntb == 1) return launch_split<ACT8, false, OUT, 2, 1, 8>(p, s);
+    if (pairs * ((ntb + 1) / 2) <= 256) return launch_split<ACT8, false, OUT, 2, 2, 8>(p, s);
+    if (pairs * ((ntb + 3) / 4) <= 256) return launch_split<ACT8, false, OUT, 2, 4, 4>(p, s);
+  }
+  return launch_tile<ACT8, GATED, OUT, 4>(p, s);
 }
 
 // Bytes of n elements of an output
