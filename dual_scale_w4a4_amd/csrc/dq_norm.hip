@@ -10,9 +10,10 @@
 // the root are taken in fp64: their error (below 2^-45) moves fl32(r) only where 1 / sqrt lies
 // that close to a midpoint of two fp32 values.
 //
-// A workgroup owns one row. Lane l of chunk c holds the 16 consecutive channels
-// 4096 c + 16 l ..; the first sweep forms and stores h and its squares, the second reads h
-// back and quantizes.
+// k_norm: a workgroup has a thread per 16 channels (up to 16384) and takes row after row, w and b
+// staying in registers; the next row's loads are in flight while a row is summed (one barrier)
+// and quantized, so each array is read and written once. k_norm_wide, for wider rows, sweeps
+// the row twice (h is read back).
 #include <float.h>
 #include <math.h>
 
@@ -41,29 +42,35 @@ struct NormArgs {
   bool wbf;           // w is bf16
 };
 
-// 16 values of a bf16 or fp32 array
+// 16 values of a bf16 or fp32 array as loaded, and unpacked to fp32
 template <bool BF>
-__device__ __forceinline__ void load16(const void* p, int64_t off, float (&v)[kNormEpl]) {
-  if (BF) {
-    const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + off);
+struct Raw16 {
+  u32x4 v[BF ? 2 : 4];
+  __device__ __forceinline__ void load(const void* p, int64_t off) {
+    const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + off * (BF ? 2 : 4));
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-      const u32x4 u = s[k];
+    for (int k = 0; k < (BF ? 2 : 4); k++) v[k] = s[k];
+  }
+  __device__ __forceinline__ void unpack(float (&x)[kNormEpl]) const {
+#pragma unroll
+    for (int k = 0; k < (BF ? 2 : 4); k++)
 #pragma unroll
       for (int e = 0; e < 4; e++) {
-        v[8 * k + 2 * e] = u2f(u[e] << 16);
-        v[8 * k + 2 * e + 1] = u2f(u[e] & 0xFFFF0000u);
+        if (BF) {
+          x[8 * k + 2 * e] = u2f(v[k][e] << 16);
+          x[8 * k + 2 * e + 1] = u2f(v[k][e] & 0xFFFF0000u);
+        } else {
+          x[4 * k + e] = u2f(v[k][e]);
+        }
       }
-    }
-  } else {
-    const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + off);
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const u32x4 u = s[k];
-#pragma unroll
-      for (int e = 0; e < 4; e++) v[4 * k + e] = u2f(u[e]);
-    }
   }
+};
+
+template <bool BF>
+__device__ __forceinline__ void load16(const void* p, int64_t off, float (&v)[kNormEpl]) {
+  Raw16<BF> r;
+  r.load(p, off);
+  r.unpack(v);
 }
 
 // nearest bf16 (ties to even) of any fp32 value, as fp32
@@ -89,21 +96,42 @@ __device__ __forceinline__ void store16(void* p, int64_t off, const float (&v)[k
   }
 }
 
-// Codes and scale of one lane's 16 values (all finite; the group of G values lies in G / 16
-// neighbouring lanes) at element offset off of the outputs. `act`: whether the lane's
-// channels exist (the group's lanes agree; all lanes of the wave take part in the maxima).
+// The constants of a call's quantizer (NVFP4)
+struct QuantConst {
+  float g, sixg;
+  double r6;
+};
+
+__device__ __forceinline__ QuantConst quant_const(float g) {
+  const float sixg = 6.0f * g;
+  return QuantConst{g, sixg, 1.0 / (double)sixg};
+}
+
+// Codes and scale of one lane's 16 values (the group of G values lies in G / 16 neighbouring
+// lanes) at element offset off of the outputs. `act`: whether the lane's channels exist (the
+// group's lanes agree; all lanes of the wave take part in the maxima). Returns whether the group
+// holds a NaN or an infinity; it is then written as a group of zeros.
 template <int FMT, int G>
-__device__ __forceinline__ void quantize16(const float (&x)[kNormEpl], float mx, bool act,
-                                           const NormArgs& p, int64_t off, float sixg) {
+__device__ __forceinline__ bool quantize16(float (&x)[kNormEpl], bool act, const NormArgs& p,
+                                           int64_t off, const QuantConst& q) {
   constexpr int LPG = G / kNormEpl;
-  const uint32_t gmb = LPG > 1 ? group_max_bits<LPG>(f2u(mx)) : f2u(mx);
+  uint32_t gmb = 0u;  // the largest |x| as bits, above every finite value's for a NaN
+#pragma unroll
+  for (int k = 0; k < kNormEpl; k++) gmb = max(gmb, f2u(x[k]) & 0x7FFFFFFFu);
+  if (LPG > 1) gmb = group_max_bits<LPG>(gmb);
+  const bool bad = gmb >= 0x7F800000u;
+  if (bad) {
+    gmb = 0u;
+#pragma unroll
+    for (int k = 0; k < kNormEpl; k++) x[k] = 0.0f;
+  }
   uint32_t scode;
   if (FMT == kMxFp8) {
     scode = mx_scale_code<8>(gmb);
     const float rd = u2f((254u - scode) << 23);
     const u32x4 c = {fp8_pack4(x, rd), fp8_pack4(x + 4, rd), fp8_pack4(x + 8, rd),
                      fp8_pack4(x + 12, rd)};
-    if (act) *reinterpret_cast<u32x4*>(p.codes + off) = c;
+    if (act) __builtin_nontemporal_store(c, reinterpret_cast<u32x4*>(p.codes + off));
   } else {
     u32x2 c;
     if (FMT == kMxFp4) {
@@ -111,25 +139,30 @@ __device__ __forceinline__ void quantize16(const float (&x)[kNormEpl], float mx,
       const GroupQ gq = mx_group(scode);
       c = u32x2{fp4_pack<8>(x, gq), fp4_pack<8>(x + 8, gq)};
     } else {
-      // the exact rules of dq_device.h: the power-of-two quotient for MXINT4, the snapped
-      // double quotient for INT4 and NVFP4
-      const GroupQ gq = group_scale<FMT == kMxFp8 ? kMxInt4 : FMT>(u2f(gmb), p.g, sixg);
+      // the exact rules of dq_device.h: the power-of-two quotient for MXINT4, fp32 codes for
+      // NVFP4 where every divisor of the wave allows them, else the snapped double quotient
       constexpr int F = FMT == kMxFp8 ? kMxInt4 : FMT;
-      const double r = F == kMxInt4 ? 0.0 : recip64(gq.d);
+      const GroupQ gq = F == kNvFp4 ? nv_group_scale(u2f(gmb), q.g, q.r6)
+                                    : group_scale<F>(u2f(gmb), q.g, q.sixg);
       scode = gq.scode;
+      if (F == kNvFp4 && __all(gq.d >= 0x1p-100f && gq.d <= 0x1p100f)) {
+        c = u32x2{nv_pack8_fast<true>(x, gq.d, gq.rd), nv_pack8_fast<true>(x + 8, gq.d, gq.rd)};
+      } else {
+        const double r = F == kMxInt4 ? 0.0 : recip64(gq.d);
 #pragma unroll
-      for (int k = 0; k < 2; k++) {
-        uint32_t pk = 0u;
+        for (int k = 0; k < 2; k++) {
+          uint32_t pk = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-          double q = code64<F>(x[8 * k + e], r, gq);
-          if (F == kInt4Bf16) q = int4_clamp(q);
-          pk |= nibble_of<F>((float)q) << (4 * e);
+          for (int e = 0; e < 8; e++) {
+            double v = code64<F>(x[8 * k + e], r, gq);
+            if (F == kInt4Bf16) v = int4_clamp(v);
+            pk |= nibble_of<F>((float)v) << (4 * e);
+          }
+          c[k] = pk;
         }
-        c[k] = pk;
       }
     }
-    if (act) *reinterpret_cast<u32x2*>(p.codes + (off >> 1)) = c;
+    if (act) __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(p.codes + (off >> 1)));
   }
   if (act && (LPG == 1 || (threadIdx.x % LPG) == 0)) {
     const int64_t si = off / G;  // rows hold whole groups
@@ -138,43 +171,136 @@ __device__ __forceinline__ void quantize16(const float (&x)[kNormEpl], float mx,
     else
       static_cast<uint8_t*>(p.scales)[si] = (uint8_t)scode;
   }
+  return bad;
+}
+
+// h = X + R of 16 channels, rounded to the stream's type
+template <bool BF>
+__device__ __forceinline__ void add_residual(float (&h)[kNormEpl], const float (&r)[kNormEpl]) {
+#pragma unroll
+  for (int k = 0; k < kNormEpl; k++) {
+    h[k] += r[k];
+    if (BF) h[k] = to_bf16(h[k]);
+  }
+}
+
+// this lane's sum of squares: not finite exactly where an h is not (finite squares fit fp64)
+__device__ __forceinline__ double sum_squares(const float (&h)[kNormEpl]) {
+  double sum = 0.0;
+#pragma unroll
+  for (int k = 0; k < kNormEpl; k++) sum = fma((double)h[k], (double)h[k], sum);
+  return sum;
+}
+
+__device__ __forceinline__ bool any_nonfinite(const float (&v)[kNormEpl]) {
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < kNormEpl; k++) bad |= !(fabsf(v[k]) <= FLT_MAX);
+  return bad;
+}
+
+// w and b of 16 channels (ones where there is none: a product with 1 is exact)
+__device__ __forceinline__ void load_factors(const NormArgs& p, int64_t c, float (&w)[kNormEpl],
+                                             float (&b)[kNormEpl]) {
+#pragma unroll
+  for (int k = 0; k < kNormEpl; k++) w[k] = b[k] = 1.0f;
+  if (p.w) {
+    if (p.wbf) load16<true>(p.w, c, w);
+    else load16<false>(p.w, c, w);
+  }
+  if (p.b) load16<false>(p.b, c, b);
+}
+
+// sum of v over the workgroup's waves, in wave order, in every thread; red: a double per wave,
+// not written again before the next barrier
+__device__ __forceinline__ double block_sum(double v, double* red, int waves) {
+  v = sum16_dpp(v);
+  const double w = ((__shfl(v, 0, kWave) + __shfl(v, 16, kWave)) + __shfl(v, 32, kWave)) +
+                   __shfl(v, 48, kWave);
+  if (waves == 1) return w;
+  if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = w;
+  __syncthreads();
+  double sum = red[0];
+  for (int k = 1; k < waves; k++) sum += red[k];
+  return sum;
+}
+
+constexpr int kNormThreads = 1024;  // k_norm: rows of up to kNormThreads * kNormEpl channels
+
+template <int FMT, int G, bool BF>
+__global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs p) {
+  __shared__ double red[2][kNormThreads / kWave];
+  const int64_t c = threadIdx.x * kNormEpl;
+  const bool act = c < p.n;
+  const int64_t lc = act ? c : 0;  // lanes past the row's end read its start and store nothing
+  const int waves = blockDim.x / kWave;
+  const QuantConst q = quant_const(p.g);
+  float w[kNormEpl], b[kNormEpl];
+  Raw16<BF> xr, rr;
+  int64_t row = blockIdx.x;
+  xr.load(p.X, row * p.n + lc);
+  if (p.R) rr.load(p.R, row * p.n + lc);
+  load_factors(p, lc, w, b);
+  int flags = 0;
+  for (int par = 0; row < p.m; row += gridDim.x, par ^= 1) {
+    const int64_t off = row * p.n + lc;
+    float h[kNormEpl];
+    xr.unpack(h);
+    if (p.R) {
+      float r[kNormEpl];
+      rr.unpack(r);
+      add_residual<BF>(h, r);
+      if (act) store16<BF>(p.h, off, h);
+    }
+    double sum = act ? sum_squares(h) : 0.0;
+    if (!(sum <= DBL_MAX)) {  // rare
+      float v[kNormEpl];
+      xr.unpack(v);
+      bool in = any_nonfinite(v);
+      if (p.R) {
+        rr.unpack(v);
+        in |= any_nonfinite(v);
+      }
+      flags |= in ? kStNonFinite : kStRange;
+    }
+    const int64_t next = row + gridDim.x;
+    if (next < p.m) {
+      xr.load(p.X, next * p.n + lc);
+      if (p.R) rr.load(p.R, next * p.n + lc);
+    }
+    sum = block_sum(sum, red[par], waves);
+    const float rstd = (float)(1.0 / sqrt(sum / (double)p.n + p.eps));
+#pragma unroll
+    for (int k = 0; k < kNormEpl; k++) h[k] = h[k] * rstd * w[k] * b[k];
+    // an overflow of x, unless the row's h already was not finite (reported above)
+    if (quantize16<FMT, G>(h, act, p, off, q) && sum <= DBL_MAX) flags |= kStRange;
+  }
+  if (flags) atomicOr(p.status, flags);
 }
 
 template <int FMT, int G, bool BF>
-__global__ __launch_bounds__(kBlock) void k_norm(NormArgs p) {
+__global__ __launch_bounds__(kBlock) void k_norm_wide(NormArgs p) {
   __shared__ double red[kWaves];
   const int64_t row = (int64_t)blockIdx.x * p.n;
   int flags = 0;
   double sum = 0.0;
   for (int64_t c = threadIdx.x * kNormEpl; c < p.n; c += kBlock * kNormEpl) {
-    float h[kNormEpl];
+    float h[kNormEpl], r[kNormEpl];
     load16<BF>(p.X, row + c, h);
+    bool in = any_nonfinite(h);
     if (p.R) {
-      float r[kNormEpl];
       load16<BF>(p.R, row + c, r);
-      float in = 0.0f, out = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kNormEpl; k++) {
-        in = fmaf(h[k], 0.0f, fmaf(r[k], 0.0f, in));  // NaN once an input is not finite
-        h[k] += r[k];
-        if (BF) h[k] = to_bf16(h[k]);
-        out = fmaf(h[k], 0.0f, out);
-      }
-      if (in != 0.0f) flags |= kStNonFinite;
-      else if (out != 0.0f) flags |= kStRange;
+      in |= any_nonfinite(r);
+      add_residual<BF>(h, r);
       store16<BF>(p.h, row + c, h);
-    } else {
-      float in = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kNormEpl; k++) in = fmaf(h[k], 0.0f, in);
-      if (in != 0.0f) flags |= kStNonFinite;
     }
-#pragma unroll
-    for (int k = 0; k < kNormEpl; k++) sum = fma((double)h[k], (double)h[k], sum);
+    const double s = sum_squares(h);
+    if (!(s <= DBL_MAX)) flags |= in ? kStNonFinite : kStRange;
+    sum += s;
   }
-  sum = block_sum4(sum, red);
+  sum = block_sum(sum, red, kWaves);
   const float rstd = (float)(1.0 / sqrt(sum / (double)p.n + p.eps));
-  const float sixg = 6.0f * p.g;
+  const QuantConst q = quant_const(p.g);
   const void* src = p.R ? p.h : p.X;
   // every lane of a wave runs the same trips (the group maxima exchange lanes); lanes past the
   // row's end read its start and store nothing
@@ -182,45 +308,33 @@ __global__ __launch_bounds__(kBlock) void k_norm(NormArgs p) {
     const int64_t c = c0 + threadIdx.x * kNormEpl;
     const bool act = c < p.n;
     const int64_t lc = act ? c : 0;
-    float x[kNormEpl], w[kNormEpl];
+    float x[kNormEpl], w[kNormEpl], b[kNormEpl];
     load16<BF>(src, row + lc, x);
+    load_factors(p, lc, w, b);
 #pragma unroll
-    for (int k = 0; k < kNormEpl; k++) x[k] *= rstd;
-    if (p.w) {
-      if (p.wbf) load16<true>(p.w, lc, w);
-      else load16<false>(p.w, lc, w);
-#pragma unroll
-      for (int k = 0; k < kNormEpl; k++) x[k] *= w[k];
-    }
-    if (p.b) {
-      load16<false>(p.b, lc, w);
-#pragma unroll
-      for (int k = 0; k < kNormEpl; k++) x[k] *= w[k];
-    }
-    float mx = 0.0f, chk = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kNormEpl; k++) {
-      mx = fmaxf(mx, fabsf(x[k]));
-      chk = fmaf(x[k], 0.0f, chk);
-    }
-    if (chk != 0.0f) {  // not finite: a bad h in the row (reported above) or an overflow
-      if (fabs(sum) <= DBL_MAX) flags |= kStRange;
-      mx = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kNormEpl; k++) x[k] = 0.0f;
-    }
-    quantize16<FMT, G>(x, mx, act, p, row + lc, sixg);
+    for (int k = 0; k < kNormEpl; k++) x[k] = x[k] * rstd * w[k] * b[k];
+    if (quantize16<FMT, G>(x, act, p, row + lc, q) && sum <= DBL_MAX) flags |= kStRange;
   }
   if (flags) atomicOr(p.status, flags);
 }
 
 template <int FMT, int G>
 static hipError_t norm_launch(bool bf16, const NormArgs& p, hipStream_t s) {
-  const dim3 grid((unsigned)p.m);
+  if (p.n > kNormThreads * kNormEpl) {
+    const dim3 grid((unsigned)p.m);
+    if (bf16)
+      hipLaunchKernelGGL((k_norm_wide<FMT, G, true>), grid, dim3(kBlock), 0, s, p);
+    else
+      hipLaunchKernelGGL((k_norm_wide<FMT, G, false>), grid, dim3(kBlock), 0, s, p);
+    return hipGetLastError();
+  }
+  const int waves = (int)((p.n + kWave * kNormEpl - 1) / (kWave * kNormEpl));
+  const int64_t most = 256 * (16 / waves);  // sixteen waves per CU
+  const dim3 grid((unsigned)(p.m < most ? p.m : most));
   if (bf16)
-    hipLaunchKernelGGL((k_norm<FMT, G, true>), grid, dim3(kBlock), 0, s, p);
+    hipLaunchKernelGGL((k_norm<FMT, G, true>), grid, dim3(waves * kWave), 0, s, p);
   else
-    hipLaunchKernelGGL((k_norm<FMT, G, false>), grid, dim3(kBlock), 0, s, p);
+    hipLaunchKernelGGL((k_norm<FMT, G, false>), grid, dim3(waves * kWave), 0, s, p);
   return hipGetLastError();
 }
 
