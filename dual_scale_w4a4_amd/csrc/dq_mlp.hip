@@ -207,6 +207,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr int vmcnt_imm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 
 constexpr int kRowB = 128;         // bytes of a token row in a stage
+constexpr int kScaleRowB = 16;     // token scale bytes per row and period (512 k)
 constexpr int steps(bool act8) { return act8 ? 2 : 4; }
 
 // 16 bytes per lane from memory to LDS: lane l's at dst + 16 l
@@ -248,30 +249,38 @@ __device__ __forceinline__ v16f mfma(const u32x4& a, const u32x4* b, v16f c, uin
 // ------------------------------------------------------------------- split-k kernel
 // A workgroup owns M row blocks of 32 (the product's M neighbouring ones; gated: the gate's and
 // the up weights' block of the same 32 channels) and 32 NB tokens; its W waves share k between
-// them, wave w taking stages w, w + W, .., and their partial sums are joined in LDS in wave
-// order. Every wave runs by itself: its weights go from memory straight to registers, its tokens
-// through a ring of two LDS stages of its own, both loaded two of its stages ahead.
+// them in periods of 512, wave w taking periods w, w + W, .., and their partial sums are joined
+// in LDS in wave order. Every wave runs by itself: its weights go from memory straight to
+// registers, its tokens through a ring of two LDS stages of its own, both loaded two of its
+// stages ahead, and the token scales (16 bytes of a row for a whole period, instead of 4 of
+// every row and stage: 14336 -> 4096 at 256 tokens 20 -> 17 us) through LDS as well. Token
+// fragments are read kAhead blocks before their products.
 
 // LDS row of one token's 32 partial sums, padded so that 8 rows cover distinct banks
 constexpr int kPartRow = 36;
 constexpr int kPartBlock = 32 * kPartRow;  // floats of one 32 x 32 block
 
-// One stage's operands of a wave, but for the tokens in LDS.
-template <bool ACT8, int M, int NB>
+// Token fragments are read kAhead blocks of 32 tokens before their products, in a ring of four.
+constexpr int kAhead = 3;
+
+// One stage's weights of a wave.
+template <bool ACT8, int M>
 struct Frags {
   u32x4 a[M][steps(ACT8)];
   uint32_t sa[M];
-  uint32_t sb[NB];
 };
 
 template <bool ACT8, bool GATED, int M, int NB, int OUT, int W>
 __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
   static_assert(!GATED || M == 2, "gate and up");
   constexpr int NK = steps(ACT8);
+  constexpr int PER = ACT8 ? 4 : 2;       // stages of a period
+  constexpr int NS = (NB + 1) / 2;        // scale loads of a period, 64 rows each
   constexpr int kRing = NB * 32 * kRowB;  // one stage of a wave's tokens
+  constexpr int kXs = NS * 1024;          // one period of a wave's token scales
+  constexpr int kWave = 2 * kRing + 2 * kXs;
   constexpr int kPart = W * M * kPartBlock * 4;
-  constexpr int kLds = 2 * W * kRing > kPart ? 2 * W * kRing : kPart;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[W * kWave > kPart ? W * kWave : kPart];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rl = lane & 31, h = lane >> 5;
@@ -281,7 +290,7 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
   const int t0 = (blockIdx.x / ntr) * (32 * NB);
   const int rows = min(p.tokens - t0, 32 * NB);
   const int ldb = ACT8 ? p.K : p.K / 2, nkb = p.K / 32, npk = p.K / kStage;
-  const int nst = p.K / (ACT8 ? 128 : 256);
+  const int nper = p.K / 512;
 
   __amdgpu_buffer_rsrc_t rw[M], rs[M];
 #pragma unroll
@@ -294,7 +303,7 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
   }
   const __amdgpu_buffer_rsrc_t rx = rsrc(p.xc + (int64_t)t0 * ldb, (uint32_t)rows * (uint32_t)ldb);
   const __amdgpu_buffer_rsrc_t rxs = rsrc(p.xs + (int64_t)t0 * nkb, (uint32_t)rows * (uint32_t)nkb);
-  uint32_t vx[4 * NB], vs[NB];
+  uint32_t vx[4 * NB], vs[NS];
 #pragma unroll
   for (int j = 0; j < 4 * NB; j++) {
     // lane l writes piece position l % 8 of row r, which holds the row's piece (l % 8) ^ term
@@ -304,11 +313,12 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
                      : kOob;
   }
 #pragma unroll
-  for (int n = 0; n < NB; n++) {
-    const int r = n * 32 + rl;
-    vs[n] = r < rows ? (uint32_t)r * (uint32_t)nkb + 4u * (uint32_t)h : kOob;
+  for (int j = 0; j < NS; j++) {
+    const int r = 64 * j + lane;
+    vs[j] = r < rows ? (uint32_t)r * (uint32_t)nkb : kOob;
   }
-  uint8_t* ring = lds + wave * 2 * kRing;
+  uint8_t* ring = lds + wave * kWave;
+  uint8_t* xsb = ring + 2 * kRing;
   const int xt = (rl & 7) ^ ((rl >> 3) & 1) ^ (ACT8 ? h : 4 * h);
 
   v16f acc[M][NB];
@@ -317,65 +327,107 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
 #pragma unroll
     for (int n = 0; n < NB; n++) acc[m][n] = v16f{};
 
-  auto load = [&](int s, uint8_t* xb, Frags<ACT8, M, NB>& f) {
+  // the loads of stage J of period q: kLoads, and before them on a period's first the scales.
+  // Past the last period they read nothing, so that every stage issues the same number and the
+  // loop body stays one basic block.
+  constexpr int kLoads = 4 * NB + M * (NK + 1);
+  static_assert(kLoads + NS < 64, "the wait counts to 63");
+  const __amdgpu_buffer_rsrc_t rnone = rsrc(p.xc, 0u);
+  auto load = [&](auto jc, int q, int par, Frags<ACT8, M>& f) {
+    constexpr int J = decltype(jc)::value;
+    const int s = q * PER + J;
+    const bool on = q < nper;
+    if (J == 0)
+#pragma unroll
+      for (int j = 0; j < NS; j++)
+        load_lds(on ? rxs : rnone, xsb + par * kXs + j * 1024, vs[j], q * 16);
 #pragma unroll
     for (int j = 0; j < 4 * NB; j++)
-      load_lds(rx, xb + j * 1024, vx[j], ACT8 ? (s >> 1) * 256 + (s & 1) * 64 : s * kRowB);
+      load_lds(on ? rx : rnone, ring + (J & 1) * kRing + j * 1024, vx[j],
+               ACT8 ? (s >> 1) * 256 + (s & 1) * 64 : s * kRowB);
 #pragma unroll
     for (int m = 0; m < M; m++) {
 #pragma unroll
       for (int i = 0; i < NK; i++)
-        f.a[m][i] = __builtin_amdgcn_raw_buffer_load_b128(rw[m], (uint32_t)lane * 16u,
+        f.a[m][i] = __builtin_amdgcn_raw_buffer_load_b128(on ? rw[m] : rnone, (uint32_t)lane * 16u,
                                                           (uint32_t)((s * NK + i) * kPackStepB), 0);
-      f.sa[m] = __builtin_amdgcn_raw_buffer_load_b32(rs[m], (uint32_t)lane * 4u,
+      f.sa[m] = __builtin_amdgcn_raw_buffer_load_b32(on ? rs[m] : rnone, (uint32_t)lane * 4u,
                                                      (uint32_t)((ACT8 ? s >> 1 : s) * kPackScaleB), 0);
     }
-#pragma unroll
-    for (int n = 0; n < NB; n++)
-      f.sb[n] = __builtin_amdgcn_raw_buffer_load_b32(rxs, vs[n], (uint32_t)((ACT8 ? s >> 1 : s) * 8), 0);
   };
-  constexpr int kLoads = 4 * NB + M * (NK + 1) + NB;  // of one stage
-  static_assert(kLoads < 64, "the wait counts to 63");
-  // the products of stage s (its loads are done)
-  auto products = [&](int s, const uint8_t* xb, const Frags<ACT8, M, NB>& f) {
-    // FP8: the stage's half of the packed stage picks its scale bytes
-    uint32_t sa[M], sb[NB];
+  // the products of stage J of a period whose scales are in xsb + par * kXs
+  auto products = [&](auto jc, int par, const Frags<ACT8, M>& f) {
+    constexpr int J = decltype(jc)::value, HS = ACT8 ? J & 1 : 0, F = NK * NB;
+    const uint8_t* xb = ring + (J & 1) * kRing + rl * kRowB;
+    const uint8_t* xp = xsb + par * kXs + rl * kScaleRowB + 4 * h + (ACT8 ? J >> 1 : J) * 8;
+    u32x4 b[4][ACT8 ? 2 : 1];
+    uint32_t sx[NB];
+    auto read = [&](int k) {
 #pragma unroll
-    for (int m = 0; m < M; m++) sa[m] = ACT8 ? f.sa[m] >> (16 * (s & 1)) : f.sa[m];
+      for (int e = 0; e < (ACT8 ? 2 : 1); e++)
+        b[k % 4][e] = read_x<ACT8>(xb + (k % NB) * 32 * kRowB, k / NB, e, xt);
+    };
 #pragma unroll
-    for (int n = 0; n < NB; n++) sb[n] = ACT8 ? f.sb[n] >> (16 * (s & 1)) : f.sb[n];
+    for (int n = 0; n < NB; n++) sx[n] = *reinterpret_cast<const uint32_t*>(xp + n * 32 * kScaleRowB);
 #pragma unroll
-    for (int i = 0; i < NK; i++)
+    for (int k = 0; k < (F < kAhead ? F : kAhead); k++) read(k);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int n = 0; n < NB; n++) {
-        u32x4 b[ACT8 ? 2 : 1];
+    for (int k = 0; k < F; k++) {
+      if (k + kAhead < F) read(k + kAhead);
 #pragma unroll
-        for (int e = 0; e < (ACT8 ? 2 : 1); e++)
-          b[e] = read_x<ACT8>(xb + (n * 32 + rl) * kRowB, i, e, xt);
-#pragma unroll
-        for (int m = 0; m < M; m++) acc[m][n] = mfma<ACT8>(f.a[m][i], b, acc[m][n], sa[m], sb[n], i);
-      }
+      for (int m = 0; m < M; m++)
+        acc[m][k % NB] = mfma<ACT8>(f.a[m][k / NB], b[k % 4], acc[m][k % NB], f.sa[m], sx[k % NB],
+                                    ACT8 ? 2 * HS + k / NB : k / NB);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
-  // a stage's token reads are done before its buffer is loaded again, and its loads are done
-  // before it is read: no other wave touches the ring
-  auto stage = [&](int s, uint8_t* xb, Frags<ACT8, M, NB>& f) {
-    if (s + W < nst) __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLoads));
-    else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  Frags<ACT8, M> f0, f1;
+  // A stage's loads are done before it is read (only the next stage's are newer), and its reads
+  // are done before its buffer is loaded again with the stage after the next: no other wave
+  // touches the ring.
+  auto stage = [&](auto jc, int q, int par) {
+    constexpr int J = decltype(jc)::value;
+    Frags<ACT8, M>& f = (J & 1) ? f1 : f0;
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLoads + (J + 1 < PER ? 0 : NS)));
     wave_lds_order();
-    products(s, xb, f);
+    products(jc, par, f);
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
     wave_lds_order();
-    if (s + 2 * W < nst) load(s + 2 * W, xb, f);
+    if constexpr (J + 2 < PER)
+      load(std::integral_constant<int, J + 2>{}, q, par, f);
+    else
+      load(std::integral_constant<int, J + 2 - PER>{}, q + W, par ^ 1, f);
+    __builtin_amdgcn_sched_barrier(0);
   };
-  Frags<ACT8, M, NB> f0, f1;
-  if (wave < nst) load(wave, ring, f0);
-  if (wave + W < nst) load(wave + W, ring + kRing, f1);
-  for (int s = wave; s < nst; s += 2 * W) {
-    stage(s, ring, f0);
-    if (s + W < nst) stage(s + W, ring + kRing, f1);
+  load(std::integral_constant<int, 0>{}, wave, 0, f0);
+  __builtin_amdgcn_sched_barrier(0);
+  load(std::integral_constant<int, 1>{}, wave, 0, f1);
+  for (int q = wave, par = 0; q < nper; q += W, par ^= 1) {
+    stage(std::integral_constant<int, 0>{}, q, par);
+    stage(std::integral_constant<int, 1>{}, q, par);
+    if constexpr (PER == 4) {
+      stage(std::integral_constant<int, 2>{}, q, par);
+      stage(std::integral_constant<int, 3>{}, q, par);
+    }
   }
+  // the last loads read nothing but still write zeros into LDS: drain them before the join
+  // reuses that memory
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
 
-  // join: block (m, n) of every wave as rows of tokens, then thread x adds the W partial sums
+  // the factors of the 4 channels whose sums this thread finishes
+  constexpr int MS = GATED ? 1 : M;                         // blocks of results
+  constexpr int NX = (256 * MS + W * 64 - 1) / (W * 64);    // 4-channel pieces per thread and n
+  const int ch = (threadIdx.x & 7) * 4;
+  f32x4 a0[NX], a1[NX], cc[NX];
+#pragma unroll
+  for (int x = 0; x < NX; x++) {
+    const int ich = (rb0 + (threadIdx.x + x * W * 64) / 256) * 32 + ch;
+    a0[x] = load_channels(p.a[0], ich, p.out, 1.0f);
+    a1[x] = load_channels(GATED ? p.a[1] : nullptr, ich, p.out, 1.0f);
+    cc[x] = load_channels(GATED ? p.b : p.bias, ich, p.out, GATED ? 1.0f : 0.0f);
+  }
+  // join: block (m, n) of every wave as rows of tokens, then each thread adds the W partial sums
   // of 4 channels of one token in wave order
   float* part = reinterpret_cast<float*>(lds);
 #pragma unroll
@@ -388,9 +440,11 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
         *reinterpret_cast<f32x4*>(part + (wave * M + m) * kPartBlock + rl * kPartRow + g * 8 + h * 4) =
             f32x4{acc[m][n][g * 4], acc[m][n][g * 4 + 1], acc[m][n][g * 4 + 2], acc[m][n][g * 4 + 3]};
     __syncthreads();
-    constexpr int MS = GATED ? 1 : M;  // blocks of results
-    for (int x = threadIdx.x; x < 256 * MS; x += W * 64) {
-      const int mr = x >> 8, tr = (x >> 3) & 31, ch = (x & 7) * 4;
+#pragma unroll
+    for (int x = 0; x < NX; x++) {
+      const int id = threadIdx.x + x * W * 64, mr = id / 256, tr = (id >> 3) & 31;
+      const int t = t0 + n * 32 + tr, ich = (rb0 + mr) * 32 + ch;
+      if (mr >= MS || t >= p.tokens) continue;  // the same for the 8 lanes of a group of channels
       f32x4 s[2] = {f32x4{}, f32x4{}};
 #pragma unroll
       for (int k = 0; k < (GATED ? 2 : 1); k++)
@@ -398,13 +452,8 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
         for (int w = 0; w < W; w++)
           s[k] += *reinterpret_cast<const f32x4*>(part + (w * M + (GATED ? k : mr)) * kPartBlock +
                                                   tr * kPartRow + ch);
-      const int t = t0 + n * 32 + tr, ich = (rb0 + mr) * 32 + ch;
-      if (t >= p.tokens) continue;  // the same for the 8 lanes of a group of channels
-      const f32x4 a0 = load_channels(p.a[0], ich, p.out, 1.0f);
-      const f32x4 a1 = load_channels(GATED ? p.a[1] : nullptr, ich, p.out, 1.0f);
-      const f32x4 c = load_channels(GATED ? p.b : p.bias, ich, p.out, GATED ? 1.0f : 0.0f);
-      const f32x4 y = combine<GATED>(p.act, a0, a1, c, s[0], s[1]);
-      if constexpr (OUT >= kOutFp4) store_quantized<OUT>(p, t, ich, c, y);
+      const f32x4 y = combine<GATED>(p.act, a0[x], a1[x], cc[x], s[0], s[1]);
+      if constexpr (OUT >= kOutFp4) store_quantized<OUT>(p, t, ich, cc[x], y);
       else if (p.vec) store_row<OUT, true>(p, t, ich, y);
       else store_row<OUT, false>(p, t, ich, y);
     }
@@ -420,7 +469,6 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
 // Loads run two stages ahead: the fragments of two stages are a ring of registers, each reloaded
 // right after the last product that reads it, and the tokens use a ring of four LDS buffers.
 
-constexpr int kScaleRowB = 16;     // token scale bytes per row and period (512 k)
 constexpr int kGroupM = 4;         // weight tiles per tile group (L2 reuse)
 
 template <int NB>
@@ -463,9 +511,6 @@ __device__ __forceinline__ uint32_t load_ws(const TileCtx<ACT8, NB>& c, int m, i
   return __builtin_amdgcn_raw_buffer_load_b32(on ? c.rs[m] : c.rnone, c.vs[m],
                                               (uint32_t)((ACT8 ? s >> 1 : s) * kPackScaleB), 0);
 }
-
-// Token fragments are read kAhead blocks of 32 tokens before their products, in a ring of four.
-constexpr int kAhead = 3;
 
 // Step KS of a stage (HS: FP8's half of the packed stage): 2 NB products in the order (n, m), and
 // between them the token fragments kAhead blocks on, from LDS (from NB - kAhead on those of the
@@ -579,14 +624,17 @@ __device__ __forceinline__ void quantize_chunk(const MlpArgs& p, f32x4 (&y)[4], 
   if (h == 0) p.scales[off >> 5] = bad ? 0xFFu : (uint8_t)sc;
 }
 
+template <bool GATED>
+constexpr int kWaveStaging = 2 * 32 * (128 * (GATED ? 1 : 2) + 16);  // LDS bytes of a wave
+
 template <bool GATED, int NB, int OUT, bool FULL>
 __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2][NB], int rb0,
-                                           int t0, uint8_t* stage) {
+                                           int t0, uint8_t* region) {
   constexpr int ME = GATED ? 1 : 2;       // row blocks of results
   constexpr int LPR = 8 * ME;             // lanes per token row in the read-back
   constexpr int NR = 32 * LPR / 64;       // row accesses of a chunk per lane
   constexpr int kRow = 128 * ME + 16;     // bytes of a staged token row, padded
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rl = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & 63, rl = lane & 31, h = lane >> 5;
   const int cl = lane % LPR, rr = lane / LPR;
   const int ich = rb0 * 32 + cl * 4;      // the 4 channels this lane stores
   f32x4 a0[4], a1[4], cb[4];              // gated: factors of the 16 channels of this lane's results
@@ -604,7 +652,6 @@ __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2
     bias = load_channels(p.bias, ich, p.out, 0.0f);
   }
   __syncthreads();  // every wave is done with the main loop's LDS
-  uint8_t* region = stage + wave * 2 * (32 * kRow);  // two chunks, taken in turn
   typedef typename std::conditional<OUT == kOutF32, f32x4, bf16x4>::type row4;
   row4 res[NR];
   const bool has_res = FULL && !GATED && p.res;
@@ -646,7 +693,7 @@ __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2
       const int t = t0 + n * 32 + rl;
       quantize_chunk<GATED, OUT>(p, y[0], t, rb0, h, FULL || (t < p.tokens && rb0 * 32 < p.out));
     } else {
-      uint8_t* reg = region + (n & 1) * (32 * kRow);
+      uint8_t* reg = region + (n & 1) * (32 * kRow);  // two chunks, taken in turn
 #pragma unroll
       for (int m = 0; m < ME; m++)
 #pragma unroll
@@ -714,36 +761,37 @@ __device__ __forceinline__ void tile_origin(int nti, int ntt, int& ti, int& tt) 
 }
 
 template <bool ACT8, bool GATED, int NB, int OUT>
-__global__ __launch_bounds__(256, NB == 8 ? 1 : 2) void k_mlp_tile(MlpArgs p, int nti, int ntt) {
+__global__ __launch_bounds__(256, 2) void k_mlp_tile(MlpArgs p, int nti, int ntt) {
   // the epilogue stages two 32-token chunks of every wave's channels in the same memory
-  constexpr int kStaging = OUT >= kOutFp4 ? 0 : 4 * 2 * 32 * (128 * (GATED ? 1 : 2) + 16);
-  constexpr int kLds = (int)sizeof(TileLds<NB>) > kStaging ? (int)sizeof(TileLds<NB>) : kStaging;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
-  TileLds<NB>& L = *reinterpret_cast<TileLds<NB>*>(lds);
+  constexpr int kStaging = OUT >= kOutFp4 ? 0 : 4 * kWaveStaging<GATED>;
+  constexpr int kRings = (int)sizeof(TileLds<NB>);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRings > kStaging ? kRings : kStaging];
   constexpr int NK = steps(ACT8);
-  constexpr int PER = ACT8 ? 4 : 2;  // stages per token-scale period (512 k)
+  constexpr int PER = ACT8 ? 4 : 2;  // stages per period (512 k)
   int ti, tt;
   tile_origin(nti, ntt, ti, tt);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  TileLds<NB>& L = *reinterpret_cast<TileLds<NB>*>(lds);
   const int rl = lane & 31, h = lane >> 5;
   const int t0 = tt * 32 * NB;
   const int rows = min(p.tokens - t0, 32 * NB);
   const int ldb = ACT8 ? p.K : p.K / 2, nkb = p.K / 32, npk = p.K / kStage;
   const int nrb = (p.out + 31) / 32;
   const int rb0 = ti * (GATED ? 4 : 8) + wave * (GATED ? 1 : 2);  // this wave's first row block
+  const int periods = p.K / 512;
 
   TileCtx<ACT8, NB> c;
   c.wave = wave;
-  c.nst = p.K / (ACT8 ? 128 : 256);
+  c.nst = PER * periods;
 #pragma unroll
   for (int m = 0; m < 2; m++) {
     // a block past the last weight row reads nothing: a descriptor without records
     const int rb = GATED ? rb0 : rb0 + m;
     const bool in = rb < nrb;
-    const int64_t at = in ? rb : 0;
-    c.rw[m] = rsrc(p.wc[GATED ? m : 0] + at * npk * kPackStageB, in ? (uint32_t)npk * kPackStageB : 0u);
-    c.rs[m] = rsrc(p.ws[GATED ? m : 0] + at * npk * kPackScaleB, in ? (uint32_t)npk * kPackScaleB : 0u);
+    const int64_t at = in ? (int64_t)rb * npk : 0;
+    c.rw[m] = rsrc(p.wc[GATED ? m : 0] + at * kPackStageB, in ? (uint32_t)npk * kPackStageB : 0u);
+    c.rs[m] = rsrc(p.ws[GATED ? m : 0] + at * kPackScaleB, in ? (uint32_t)npk * kPackScaleB : 0u);
     c.vw[m] = (uint32_t)lane * 16u;
     c.vs[m] = (uint32_t)lane * 4u;
   }
@@ -829,8 +877,8 @@ __global__ __launch_bounds__(256, NB == 8 ? 1 : 2) void k_mlp_tile(MlpArgs p, in
       step(std::integral_constant<int, 3>{});
     }
   };
-  for (int q = 0; q < p.K / 512; q++) {
-    const bool more = q + 1 < p.K / 512;
+  for (int q = 0; q < periods; q++) {
+    const bool more = q + 1 < periods;
     stage(std::integral_constant<int, 0>{}, PER * q, q, more);
     stage(std::integral_constant<int, 1>{}, PER * q + 1, q, more);
     if constexpr (PER == 4) {
@@ -841,16 +889,18 @@ __global__ __launch_bounds__(256, NB == 8 ? 1 : 2) void k_mlp_tile(MlpArgs p, in
   // the last stages' loads read nothing but still write zeros into LDS: drain them before the
   // epilogue reuses that memory
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  uint8_t* region = lds + (OUT >= kOutFp4 ? 0 : wave * kWaveStaging<GATED>);
   if (rows == 32 * NB && (rb0 + (GATED ? 1 : 2)) * 32 <= p.out && (OUT >= kOutFp4 || p.vec))
-    tile_store<GATED, NB, OUT, true>(p, acc, rb0, t0, lds);
+    tile_store<GATED, NB, OUT, true>(p, acc, rb0, t0, region);
   else
-    tile_store<GATED, NB, OUT, false>(p, acc, rb0, t0, lds);
+    tile_store<GATED, NB, OUT, false>(p, acc, rb0, t0, region);
 }
 
 // ---------------------------------------------------------------------------------- host
 
-template <bool ACT8, bool GATED, int OUT, int NB>
+template <bool ACT8, bool GATED, int OUT>
 hipError_t launch_tile(const MlpArgs& p, hipStream_t s) {
+  constexpr int NB = 4;
   const int nti = (p.out + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
   const int ntt = (p.tokens + 32 * NB - 1) / (32 * NB);
   hipLaunchKernelGGL((k_mlp_tile<ACT8, GATED, NB, OUT>), dim3((unsigned)(nti * ntt)), dim3(256), 0,
@@ -858,8 +908,9 @@ hipError_t launch_tile(const MlpArgs& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool ACT8, bool GATED, int OUT, int M, int NB, int W>
+template <bool ACT8, bool GATED, int OUT, int M, int NB>
 hipError_t launch_split(const MlpArgs& p, hipStream_t s) {
+  constexpr int W = 4;
   const int rows = GATED ? 32 : 32 * M;
   const int64_t nrt = (p.out + rows - 1) / rows, ntt = (p.tokens + 32 * NB - 1) / (32 * NB);
   hipLaunchKernelGGL((k_mlp_split<ACT8, GATED, M, NB, OUT, W>), dim3((unsigned)(nrt * ntt)),
@@ -867,31 +918,36 @@ hipError_t launch_split(const MlpArgs& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Which kernel. With few 32 x 32 blocks of results (row blocks times 32-token blocks) the split
-// kernel brings the whole chip to bear on k; with many, the tile kernel reads each operand fewer
-// times. Measured at MXFP4, us (split / tile), K = 4096 -> 14336 and K = 14336 -> 4096:
-//   single, tokens   32: 8.5 / 19, 11 / 41   64: 11 / 21, 11 / 42    128: 18 / 18, 14 / 40
-//                   256: 33 / 20, 19 / 41   512: 58 / 22, 33 / 41   1024: 108 / 37, 63 / 43
-//   gated, 4096 -> 14336, tokens 32: 12 / 18   64: 20 / 18   128: 35 / 19
-//   gated, 2048 -> 5632, tokens 64: 6.4 / 12   128: 8.9 / 12   256: 13 / 12
-// The single product takes the smallest split tile (M row blocks by NB token blocks) that fits
-// the chip in one round, 256 workgroups: 14336 -> 4096 at 128 tokens takes 17 us in 32 x 32
-// tiles and 14 us in 64 x 32; at 256 tokens 24 us in 64 x 32 and 19 us in 64 x 64. Up to 32
-// tokens it splits whatever the number of rows.
+// Which kernel, by the number of 32 x 32 blocks of results (row blocks times 32-token blocks).
+// With few the split kernel brings the whole chip to bear on k, in the smallest tile (M row
+// blocks by NB token blocks) that still fits it in about one round; with many the tile kernel
+// reads each operand fewer times. Measured, us (MXFP4 / MXFP8 activations):
+//   single 4096 -> 4096     tokens   64 (256 blocks)   128 (512)   256 (1024)  512 (2048)  1024
+//     32 x 32                         5.2 /  7.6        7.1 / 11    11 / 19     18 / 34     32 / 62
+//     64 x 32                         6.6 /  7.8        6.8 / 8.4   9.5 / 12    15 / 21     26 / 36
+//     64 x 64                         8.4 / 11          8.5 / 11    8.9 / 12    13 / 19     24 / 34
+//     64 x 128                        11  / 13          13  / 16    13 / 17     14 / 22     27 / 40
+//     tile                            22  / 27          17  / 22    17 / 22     17 / 23     18 / 24
+//   single 14336 -> 4096, 512 tokens (2048): 64 x 64 33 / 49, 64 x 128 28 / 48, tile 41 / 60
+//   gated 2048 -> 5632, tokens 128 (704): 32 x 32 8.9 / 10, 32 x 64 9.3 / 11, tile 11 / 14
+//   gated 4096 -> 14336, tokens 32 (448): 12.7 / 14, 13.6 / 16, -;  64 (896): 21 / 24, 15 / 20,
+//     17 / 22;  96 (1344): 30 / 33, 24 / 30, 18 / 23
+// A single block of tokens always splits: 8192 -> 28672 at 32 tokens 29 / 36 in 64 x 32.
 template <bool ACT8, bool GATED, int OUT>
 hipError_t launch_t(const MlpArgs& p, hipStream_t s) {
-  const int64_t nrb = (p.out + 31) / 32, ntb = (p.tokens + 31) / 32;
-  /*PICK*/
+  const int64_t ntb = (p.tokens + 31) / 32, blocks = (p.out + 31) / 32 * ntb;
   if constexpr (GATED) {
-    if (nrb * ntb <= 768) return launch_split<ACT8, true, OUT, 2, 1, 4>(p, s);
+    if (blocks <= 768 || ntb == 1) return launch_split<ACT8, true, OUT, 2, 1>(p, s);
+    if (blocks <= 1024) return launch_split<ACT8, true, OUT, 2, 2>(p, s);
   } else {
-    const int64_t pairs = (nrb + 1) / 2;
-    if (nrb * ntb <= 256) return launch_split<ACT8, false, OUT, 1, 1, 8>(p, s);
-    if (pairs * ntb <= 256 || ntb == 1) return launch_split<ACT8, false, OUT, 2, 1, 8>(p, s);
-    if (pairs * ((ntb + 1) / 2) <= 256) return launch_split<ACT8, false, OUT, 2, 2, 8>(p, s);
-    if (pairs * ((ntb + 3) / 4) <= 256) return launch_split<ACT8, false, OUT, 2, 4, 4>(p, s);
+    if (blocks <= 256) return launch_split<ACT8, false, OUT, 1, 1>(p, s);
+    if (blocks <= 512 || ntb == 1) return launch_split<ACT8, false, OUT, 2, 1>(p, s);
+    if (blocks <= 2048) {
+      if (ACT8 || blocks <= 1024 || ntb == 2) return launch_split<ACT8, false, OUT, 2, 2>(p, s);
+      if constexpr (!ACT8) return launch_split<ACT8, false, OUT, 2, 4>(p, s);
+    }
   }
-  return launch_tile<ACT8, GATED, OUT, 4>(p, s);
+  return launch_tile<ACT8, GATED, OUT>(p, s);
 }
 
 // Bytes of n elements of an output
