@@ -1,8 +1,9 @@
 """Python binding of libdq.so, the MI355X dual-scale weight-reconstruction solver.
 
-Argument marshalling only: every step of the solver runs in the HIP kernels behind the C ABI
-declared in include/dq.h. PyTorch provides device memory and the current stream. There is
-no CPU fallback: if libdq.so is missing or no GPU is present, calls raise.
+Argument marshalling only: every step runs in the HIP kernels behind the C ABI declared in
+include/dq.h (through ctypes) and include/dq_mlp.h (through the compiled _bind.so). PyTorch
+provides device memory and the current stream. There is no CPU fallback: if libdq.so is missing
+or no GPU is present, calls raise.
 
     import dual_scale_w4a4_amd as dq
     out = dq.solve(W_cuda_bf16, "mxfp4", group=32, T=20)
@@ -16,11 +17,10 @@ from typing import Dict, Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdq.so")
+BIND_PATH = os.path.join(_HERE, "_bind.so")  # the compiled part of this binding
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "dq.h")
 
 FMT = {"int4_bf16": 0, "mxint4": 1, "mxfp4": 2, "nvfp4": 3}
-ACT_FMT = {**FMT, "mxfp8": 4}  # formats of the MLP operators (include/dq_mlp.h)
-ACTIVATION = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 DTYPE = {"f32": 0, "bf16": 1}
 STATUS = {0: "DQ_OK", 1: "DQ_ERR_ARG", 2: "DQ_ERR_UNSUPPORTED", 3: "DQ_ERR_NONFINITE",
           4: "DQ_ERR_RANGE", 5: "DQ_ERR_WORKSPACE", 6: "DQ_ERR_HIP", 7: "DQ_ERR_INTERNAL"}
@@ -104,20 +104,6 @@ def lib() -> ctypes.CDLL:
         L.dq_gemm_pack_weights.restype = I
         L.dq_gemm_mx_packed.argtypes = [P, P, I64, I64, P, P, P, I64, I, P, P]
         L.dq_gemm_mx_packed.restype = I
-        D, F = ctypes.c_double, ctypes.c_float
-        L.dq_norm_quantize_act_async.argtypes = [P, I, P, P, I64, I64, P, I, D, P, I, I, F, P, P,
-                                                 P, P]
-        L.dq_norm_quantize_act_async.restype = I
-        L.dq_norm_quantize_act.argtypes = [P, I, P, P, I64, I64, P, I, D, P, I, I, F, P, P, P, SZ,
-                                           P]
-        L.dq_norm_quantize_act.restype = I
-        L.dq_gemm_mx_epilogue.argtypes = [P, P, I, I64, I64, P, P, P, P, I, P, I64, I, P, P]
-        L.dq_gemm_mx_epilogue.restype = I
-        L.dq_gated_mx.argtypes = [P, P, I, I64, I64, P, P, P, P, P, P, I, I64, I, P, P]
-        L.dq_gated_mx.restype = I
-        L.dq_gated_mx_quantized.argtypes = [P, P, I, I64, I64, P, P, P, P, P, P, I, I64, P, I, P, P,
-                                            P]
-        L.dq_gated_mx_quantized.restype = I
         L.dq_status_str.argtypes = [I]
         L.dq_status_str.restype = ctypes.c_char_p
         _lib = L
@@ -446,98 +432,34 @@ def gemm_mx_packed(act_codes, act_scales, packed, a=None, out_dtype: str = "bf16
 
 
 # ------------------------------------------------------------------ the MLP operators
-# (include/dq_mlp.h) Every tensor lies on one device; the call runs on `stream`, or on that
-# device's current stream, whichever device is current.
+# (include/dq_mlp.h) Every tensor of a call is contiguous and lies on one device; the work goes
+# to `stream`, or to that device's current stream, whichever device is current. Checks and calls
+# are compiled (csrc/dq_bind.cpp): a refused argument raises ValueError, a failed call DQError.
+
+_mlp = None
 
 
-# The calls are a few microseconds of GPU work for a single token, so their host side is kept
-# short: devices are compared as indices, the current stream's handle is read directly, and
-# every tensor is looked at once.
+def _calls():
+    """The compiled binding; raise if it is not there."""
+    global _mlp
+    if _mlp is None:
+        torch = _torch()
+        lib()
+        if not os.path.exists(BIND_PATH):
+            raise ImportError(f"{BIND_PATH} is missing: build it with "
+                              "`python -m dual_scale_w4a4_amd.build` (hipcc, gfx950)")
+        from . import _bind as m
 
-
-def _call(dev, stream, f, *args):
-    """f(*args, stream) with device ``dev`` (an index) current."""
-    torch = _torch()
-    if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        if stream.device.index != dev:
-            raise ValueError("stream belongs to another device than the tensors")
-        s = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        return f(*args, s)
-    with torch.cuda.device(dev):
-        return f(*args, s)
-
-
-def _empty(shape, dtype, device, stream):
-    """An uninitialized tensor that belongs to the stream it will be written on."""
-    torch = _torch()
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _arr(name, t, dev, dtype, shape):
-    """The address of a dense tensor on device ``dev`` (an index) after its checks."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                     f"cuda:{dev}")
-
-
-def _opt(name, t, dev, dtype, shape):
-    """_arr, or None for a missing optional tensor."""
-    return None if t is None else _arr(name, t, dev, dtype, shape)
-
-
-def _out_dtype(out_dtype):
-    torch = _torch()
-    if out_dtype not in DTYPE:
-        raise ValueError("out_dtype is 'bf16' or 'f32'")
-    return torch.bfloat16 if out_dtype == "bf16" else torch.float32
+        m.bind(DQError, torch._C._cuda_getCurrentRawStream)
+        _mlp = m
+    return _mlp
 
 
 def act_outputs(X, fmt: str, group: int):
     """The (codes, scales) tensors that quantizing X (tokens x cols) writes: codes tokens x
     cols/2 uint8 (MXFP8: tokens x cols), scales tokens x cols/group (int16 holding bf16 bits for
     int4_bf16, else uint8)."""
-    torch = _torch()
-    if fmt not in ACT_FMT:
-        raise ValueError(f"unknown format {fmt!r}")
-    tokens, cols = X.shape
-    codes = torch.empty((tokens, cols if fmt == "mxfp8" else cols // 2), dtype=torch.uint8,
-                        device=X.device)
-    sdt = torch.int16 if fmt == "int4_bf16" else torch.uint8
-    return codes, torch.empty((tokens, cols // group), dtype=sdt, device=X.device)
-
-
-def _norm_args(X, fmt, group, codes, scales, weight, residual, residual_out, b, eps, g):
-    torch = _torch()
-    dt = _check_w(X)
-    shape, dev, xt = X.shape, X.get_device(), X.dtype
-    tokens, cols = shape
-    if fmt not in ACT_FMT:
-        raise ValueError(f"unknown format {fmt!r}")
-    if group not in (16, 32, 64) or cols % group:
-        raise ValueError("group must be 16, 32 or 64 and divide the channels")
-    one, f32 = (cols,), torch.float32
-    wt, wp = 0, None
-    if weight is not None:
-        wd = weight.dtype
-        if wd is torch.bfloat16:
-            wt = 1
-        elif wd is not f32:
-            raise ValueError("weight must be float32 or bfloat16")
-        wp = _arr("weight", weight, dev, wd, one)
-    return (X.data_ptr(), DTYPE[dt], _opt("residual", residual, dev, xt, shape),
-            _opt("residual_out", residual_out, dev, xt, shape), tokens, cols, wp, wt, eps,
-            _opt("b", b, dev, f32, one), ACT_FMT[fmt], group, g,
-            _arr("codes", codes, dev, torch.uint8,
-                 (tokens, cols if fmt == "mxfp8" else cols // 2)),
-            _arr("scales", scales, dev, torch.int16 if fmt == "int4_bf16" else torch.uint8,
-                 (tokens, cols // group)))
+    return _calls().act_outputs(X, fmt, group)
 
 
 def norm_quantize_act(X, fmt: str, group: int, weight=None, residual=None, residual_out=None,
@@ -547,23 +469,18 @@ def norm_quantize_act(X, fmt: str, group: int, weight=None, residual=None, resid
     column inverse scales ``b``, quantized as quantize_act does (any of its formats; NVFP4 takes
     a fixed ``g`` > 0) or to "mxfp8". Returns codes, scales and, with a residual, "residual": h
     in ``residual_out`` (``residual`` itself updates it in place) or a new tensor."""
-    torch = _torch()
-    if fmt in ACT_FMT and X.dim() == 2 and group in (16, 32, 64):
-        tokens, cols = X.shape
-        codes = _empty((tokens, cols if fmt == "mxfp8" else cols // 2), torch.uint8, X.device,
-                       stream)
-        scales = _empty((tokens, cols // group),
-                        torch.int16 if fmt == "int4_bf16" else torch.uint8, X.device, stream)
+    m = _calls()
+    if stream is None:
+        codes, scales = m.act_outputs(X, fmt, group)
+        if residual is not None and residual_out is None:
+            residual_out = _torch().empty_like(X)
     else:
-        codes = scales = None  # refused below
-    if residual is not None and residual_out is None:
-        residual_out = _empty(X.shape, X.dtype, X.device, stream)
-    args = _norm_args(X, fmt, group, codes, scales, weight, residual, residual_out, b, eps, g)
-    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                            workspace.numel() * workspace.element_size())
-    st = _call(X.get_device(), stream, lib().dq_norm_quantize_act, *args, ws_ptr, ws_bytes)
-    if st != 0:
-        raise DQError(st, "dq_norm_quantize_act")
+        with _torch().cuda.stream(stream):  # the outputs belong to the stream that writes them
+            codes, scales = m.act_outputs(X, fmt, group)
+            if residual is not None and residual_out is None:
+                residual_out = _torch().empty_like(X)
+    m.norm(X, fmt, group, codes, scales, None, weight, residual, residual_out, b, eps, g, workspace,
+           stream)
     out = {"codes": codes, "scales": scales}
     if residual is not None:
         out["residual"] = residual_out
@@ -576,73 +493,22 @@ def norm_quantize_act_async(X, fmt: str, group: int, codes, scales, status, weig
     """dq_norm_quantize_act_async into caller-allocated outputs (codes, scales from act_outputs;
     ``residual_out`` wherever ``residual`` is given): enqueued on the stream, no wait; device
     errors are OR-ed into ``status`` (an int32 CUDA tensor the caller clears)."""
-    args = _norm_args(X, fmt, group, codes, scales, weight, residual, residual_out, b, eps, g)
-    dev = X.get_device()
-    if status.dtype is not _torch().int32 or status.get_device() != dev:
+    if status is None:
         raise ValueError("status must be an int32 tensor on X's device")
-    st = _call(dev, stream, lib().dq_norm_quantize_act_async, *args, status.data_ptr())
-    if st != 0:
-        raise DQError(st, "dq_norm_quantize_act_async")
-
-
-def _product_args(act_codes, act_scales, act_fmt, packed, a, name):
-    """The device, and checked arguments of one product: those it shares with every other, its
-    packed weights' and its a."""
-    torch = _torch()
-    if act_fmt == "mxfp4":
-        fmt, per = 2, 2
-    elif act_fmt == "mxfp8":
-        fmt, per = 4, 1
-    else:
-        raise ValueError("act_fmt is 'mxfp4' or 'mxfp8'")
-    if not act_codes.is_cuda or act_codes.dim() != 2:
-        raise ValueError("act_codes must be a 2-D CUDA (HIP) tensor")
-    u8, dev, tokens = torch.uint8, act_codes.get_device(), act_codes.shape[0]
-    K, out = packed["K"], packed["out"]
-    rows = -(-out // 32)
-    return (dev, (_arr("act_codes", act_codes, dev, u8, (tokens, K // per)),
-                  _arr("act_scales", act_scales, dev, u8, (tokens, K // 32)), fmt, tokens, K),
-            _arr(name, packed["codes"], dev, u8, (rows * 16 * K,)),
-            _arr(name, packed["scales"], dev, u8, (rows * K,)),
-            _opt("a", a, dev, torch.float32, (out,)))
+    _calls().norm(X, fmt, group, codes, scales, status, weight, residual, residual_out, b, eps, g,
+                 None, stream)
 
 
 def gemm_mx_epilogue(act_codes, act_scales, packed, a=None, bias=None, activation: str = "none",
                      residual=None, act_fmt: str = "mxfp4", out_dtype: str = "bf16", y=None,
                      stream=None):
     """dq_gemm_mx_epilogue: Y = residual + act((xhat Qhat^T) D_a + bias) with weights from
-    gemm_pack_weights and MXFP4 or MXFP8 activations. ``residual`` (tokens x out, of the output
-    type) may be ``y`` itself. Returns Y (tokens x out, bfloat16 or float32; MXFP8 activations
-    give bfloat16), into ``y`` when given."""
-    torch = _torch()
-    dev, head, wc, ws, ap = _product_args(act_codes, act_scales, act_fmt, packed, a, "packed")
-    out, dt = packed["out"], _out_dtype(out_dtype)
-    if activation not in ACTIVATION:
-        raise ValueError(f"unknown activation {activation!r}")
-    shape = (head[3], out)
-    if y is None:
-        y = _empty(shape, dt, act_codes.device, stream)
-    st = _call(dev, stream, lib().dq_gemm_mx_epilogue, *head, wc, ws, ap,
-               _opt("bias", bias, dev, torch.float32, (out,)), ACTIVATION[activation],
-               _opt("residual", residual, dev, dt, shape), out, DTYPE[out_dtype],
-               _arr("y", y, dev, dt, shape))
-    if st != 0:
-        raise DQError(st, "dq_gemm_mx_epilogue")
-    return y
-
-
-def _gated_args(act_codes, act_scales, act_fmt, gate, up, a_gate, a_up, activation):
-    dev, head, gc, gs, ag = _product_args(act_codes, act_scales, act_fmt, gate, a_gate, "gate")
-    K, inner = gate["K"], gate["out"]
-    if up["out"] != inner or up["K"] != K:
-        raise ValueError("gate and up weights disagree on their channels")
-    if activation not in ACTIVATION:
-        raise ValueError(f"unknown activation {activation!r}")
-    u8, rows = _torch().uint8, -(-inner // 32)
-    return dev, (*head, gc, gs, ag, _arr("up", up["codes"], dev, u8, (rows * 16 * K,)),
-                 _arr("up", up["scales"], dev, u8, (rows * K,)),
-                 _opt("a_up", a_up, dev, _torch().float32, (inner,)), ACTIVATION[activation],
-                 inner)
+    gemm_pack_weights and MXFP4 or MXFP8 activations; ``activation`` one of "none", "relu",
+    "silu", "gelu", "gelu_tanh". ``residual`` (tokens x out, of the output type) may be ``y``
+    itself. Returns Y (tokens x out, bfloat16 or float32; MXFP8 activations give bfloat16), into
+    ``y`` when given."""
+    return _calls().epilogue(act_codes, act_scales, packed, a, bias, activation, residual, act_fmt,
+                            out_dtype, y, stream)
 
 
 def gated_mx(act_codes, act_scales, gate, up, a_gate=None, a_up=None, activation: str = "silu",
@@ -650,15 +516,8 @@ def gated_mx(act_codes, act_scales, gate, up, a_gate=None, a_up=None, activation
     """dq_gated_mx: H = act((xhat Qgate^T) D_a_gate) * ((xhat Qup^T) D_a_up) in one kernel, gate
     and up weights each from gemm_pack_weights. Returns H (tokens x inner, bfloat16 or float32;
     MXFP8 activations give bfloat16), into ``y`` when given."""
-    dev, args = _gated_args(act_codes, act_scales, act_fmt, gate, up, a_gate, a_up, activation)
-    dt, shape = _out_dtype(out_dtype), (args[3], gate["out"])
-    if y is None:
-        y = _empty(shape, dt, act_codes.device, stream)
-    st = _call(dev, stream, lib().dq_gated_mx, *args, DTYPE[out_dtype],
-               _arr("y", y, dev, dt, shape))
-    if st != 0:
-        raise DQError(st, "dq_gated_mx")
-    return y
+    return _calls().gated(act_codes, act_scales, gate, up, a_gate, a_up, activation, act_fmt,
+                         out_dtype, y, stream)
 
 
 def gated_mx_quantized(act_codes, act_scales, gate, up, fmt: str, a_gate=None, a_up=None,
@@ -667,22 +526,8 @@ def gated_mx_quantized(act_codes, act_scales, gate, up, fmt: str, a_gate=None, a
     """dq_gated_mx_quantized: gated_mx's H times ``b`` (the next product's column inverse scales),
     quantized to ``fmt`` ("mxfp4" or "mxfp8") in groups of 32 channels. Returns codes and scales
     (into the given tensors), as the next product takes them."""
-    torch = _torch()
-    dev, args = _gated_args(act_codes, act_scales, act_fmt, gate, up, a_gate, a_up, activation)
-    tokens, inner = args[3], gate["out"]
-    if fmt not in ("mxfp4", "mxfp8") or inner % 32:
-        raise ValueError("fmt is 'mxfp4' or 'mxfp8', and the channels a multiple of 32")
-    cs, ss = (tokens, inner if fmt == "mxfp8" else inner // 2), (tokens, inner // 32)
-    if codes is None:
-        codes = _empty(cs, torch.uint8, act_codes.device, stream)
-    if scales is None:
-        scales = _empty(ss, torch.uint8, act_codes.device, stream)
-    st = _call(dev, stream, lib().dq_gated_mx_quantized, *args,
-               _opt("b", b, dev, torch.float32, (inner,)), ACT_FMT[fmt],
-               _arr("codes", codes, dev, torch.uint8, cs),
-               _arr("scales", scales, dev, torch.uint8, ss))
-    if st != 0:
-        raise DQError(st, "dq_gated_mx_quantized")
+    codes, scales = _calls().gated_quantized(act_codes, act_scales, gate, up, a_gate, a_up,
+                                            activation, act_fmt, fmt, b, codes, scales, stream)
     return {"codes": codes, "scales": scales}
 
 

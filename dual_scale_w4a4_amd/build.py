@@ -1,4 +1,5 @@
-"""Build libdq.so in-tree with hipcc for gfx950.
+"""Build libdq.so in-tree with hipcc for gfx950, and _bind.so, the compiled part of its Python
+binding.
 
     python -m dual_scale_w4a4_amd.build
 
@@ -15,6 +16,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libdq.so")
+BIND_PATH = os.path.join(HERE, "_bind.so")
 SOURCES = ["dq_kernels.hip", "dq_pass.hip", "dq_rowres.hip", "dq_act.hip", "dq_gemm.hip",
            "dq_norm.hip", "dq_mlp.hip",
            "dq_api.hip"]
@@ -41,12 +43,30 @@ def _run(cmd, verbose):
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed building libdq.so")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed building libdq.so or _bind.so")
+
+
+def bind_cmd(out: str):
+    """The compiler call for the Python binding of the MLP operators (host code only, against
+    torch's headers and the libdq.so beside it)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [f"-I{p}" for p in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+                              os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"))]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            "-D__HIP_PLATFORM_AMD__",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+            os.path.join(CSRC, "dq_bind.cpp"), "-o", out, f"-L{tlib}", "-ltorch_python",
+            "-ltorch_cpu", "-lc10", f"-L{HERE}", "-l:libdq.so", "-Wl,-rpath,$ORIGIN"]
 
 
 def build(verbose: bool = False) -> str:
     """Compile every source to an object in parallel (no device code crosses files), then
-    link the shared library."""
+    link the shared library and build the Python binding that calls it."""
     from concurrent.futures import ThreadPoolExecutor
 
     objdir = os.path.join(HERE, "_build")
@@ -62,6 +82,8 @@ def build(verbose: bool = False) -> str:
     _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", LIB_PATH + ".tmp"],
          verbose)
     os.replace(LIB_PATH + ".tmp", LIB_PATH)
+    _run(bind_cmd(BIND_PATH + ".tmp"), verbose)
+    os.replace(BIND_PATH + ".tmp", BIND_PATH)
     return LIB_PATH
 
 

@@ -26,6 +26,14 @@ def dqlib():
         from dual_scale_w4a4_amd import build
 
         build.build()
+    L = dq.lib()  # the package calls these through its compiled binding; here through ctypes
+    P, I, I64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+    norm = [P, I, P, P, I64, I64, P, I, ctypes.c_double, P, I, I, F, P, P]
+    L.dq_norm_quantize_act_async.argtypes = [*norm, P, P]
+    L.dq_norm_quantize_act.argtypes = [*norm, P, ctypes.c_size_t, P]
+    L.dq_gemm_mx_epilogue.argtypes = [P, P, I, I64, I64, P, P, P, P, I, P, I64, I, P, P]
+    L.dq_gated_mx.argtypes = [P, P, I, I64, I64, P, P, P, P, P, P, I, I64, I, P, P]
+    L.dq_gated_mx_quantized.argtypes = [P, P, I, I64, I64, P, P, P, P, P, P, I, I64, P, I, P, P, P]
     return dq
 
 
@@ -124,6 +132,29 @@ def test_gated_arguments_are_refused(dqlib, change, want):
 ])
 def test_gated_quantized_arguments_are_refused(dqlib, change, want):
     assert dqlib.lib().dq_gated_mx_quantized(*dict(GATEDQ, **change).values(), None) == want
+
+
+def test_binding_refuses_without_a_gpu(dqlib):
+    import torch
+
+    t = torch.zeros(2, 64)
+    u = torch.zeros(2, 256, dtype=torch.uint8)
+    pk = dict(codes=u, scales=u, out=64, K=512)
+    calls = dqlib._calls()
+    for f in (lambda: dqlib.act_outputs(t, "mxfp8", 32), lambda: dqlib.act_outputs(3, "mxfp8", 32),
+              lambda: dqlib.norm_quantize_act(t, "mxfp8", 32),
+              lambda: dqlib.norm_quantize_act_async(t, "mxfp8", 32, u, u, None),
+              lambda: dqlib.gemm_mx_epilogue(u, u, pk), lambda: dqlib.gemm_mx_epilogue(u, u, {}),
+              lambda: dqlib.gemm_mx_epilogue(u, u, [1]),
+              lambda: dqlib.gemm_mx_epilogue(u, u, dict(pk, K=500)),
+              lambda: dqlib.gated_mx(u, u, pk, pk),
+              lambda: dqlib.gated_mx_quantized(u, u, pk, dict(pk, out=0), "mxfp8")):
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(TypeError):
+        calls.epilogue(u)  # a fixed number of positional arguments
+    with pytest.raises(TypeError):
+        dqlib.gemm_mx_epilogue(u, u, dict(pk, K="512"))
 
 
 def test_mxfp8_is_no_format_of_the_solver(dqlib):
