@@ -513,16 +513,15 @@ __device__ __forceinline__ uint32_t load_ws(const TileCtx<ACT8, NB>& c, int m, i
 }
 
 // Step KS of a stage (HS: FP8's half of the packed stage): 2 NB products in the order (n, m), and
-// between them the token fragments kAhead blocks on, from LDS (from NB - kAhead on those of the
-// next step, after the last step the next stage's, with its token scales); the reload of the
-// step's weight fragments with stage s + 2's after their last products; and in step 0, before any
-// of those, stage s + 2's token loads (XS: first the next period's token scales). Loads past
-// the last stage read nothing (they still write zeros to LDS, into buffers no longer read), so
-// every stage issues the same number.
+// between them the token fragments kAhead blocks on, from LDS (past the stage's last those of
+// the next stage, with its token scales); the reload of the step's weight fragments with stage
+// s + 2's after their last products; and in step 0, before any of those, stage s + 2's token
+// loads (XS: first the next period's token scales). Loads past the last stage read nothing (they
+// still write zeros to LDS, into buffers no longer read), so every stage issues the same number.
 //
-// The stage's one barrier stands before the last step's block NB - kAhead, the first that reads
-// stage s + 1's tokens. There those tokens' loads, the first of the loads issued in stage s - 1,
-// are complete in this wave (the weight loads after them and this stage's loads may be in
+// The stage's one barrier stands before the block kAhead from its end, the first at which stage
+// s + 1's tokens are read. There those tokens' loads, the first of the loads issued in stage
+// s - 1, are complete in this wave (the weight loads after them and this stage's loads may be in
 // flight: a fixed count; the weights' own waits are at their uses), and after it in every
 // wave. It also stands between the last reads of a token buffer, whose products every wave has
 // issued a stage before, and the loads that fill the buffer again: with four buffers stage
@@ -534,17 +533,19 @@ __device__ __forceinline__ void tile_step(v16f (&acc)[2][NB], u32x4 (&fa)[2][ste
                                           const uint8_t* lx, const uint8_t* lxn,
                                           const uint8_t* xsn, int xt, const TileCtx<ACT8, NB>& c,
                                           uint8_t* xb, uint8_t* xsb, int s, int q, bool xs_on) {
-  constexpr int NK = steps(ACT8);
-  constexpr bool kLast = KS == NK - 1;
+  constexpr int NK = steps(ACT8), F = NK * NB, kBar = F - kAhead;
+  static_assert(F % 4 == 0 && kBar > 0, "the ring of fragments");
   const int s2 = s + 2;
   const bool on = s2 < c.nst;
 #pragma unroll
   for (int n = 0; n < NB; n++) {
-    const int f = n + kAhead;             // the block read now
-    const bool wrap = f >= NB;            // .. belongs to the next step
-    if (kLast && f == NB) {
+    const int i = KS * NB + n;            // this block of the stage
+    const int f = (i + kAhead) % F;       // the block read now, of the next stage once it wraps
+    const bool next = i + kAhead >= F;
+    if (i == kBar) {
       __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * NK + 2 + NB + (XS ? 1 : 0) + 2 * (NK - 1)));
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * NK + 2 + (XS ? 1 : 0) + (kBar < NB ? kBar : NB) +
+                                           2 * (kBar / NB)));
       __atomic_signal_fence(__ATOMIC_SEQ_CST);
       __builtin_amdgcn_s_barrier();
       __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -555,16 +556,14 @@ __device__ __forceinline__ void tile_step(v16f (&acc)[2][NB], u32x4 (&fa)[2][ste
     }
 #pragma unroll
     for (int m = 0; m < 2; m++) {
-      acc[m][n] = mfma<ACT8>(fa[m][KS], fb[n % 4], acc[m][n], sw[m], sx[n], ACT8 ? 2 * HS + KS : KS);
+      acc[m][n] = mfma<ACT8>(fa[m][KS], fb[i % 4], acc[m][n], sw[m], sx[n], ACT8 ? 2 * HS + KS : KS);
       if (XS && KS == 0 && n == 0 && m == 0) load_xs(c, xsb, q, xs_on);
       if (KS == 0 && m == 0) load_x(c, xb, n, s2, on);
-      if (ACT8 || m == 0) {
-        const uint8_t* row = (kLast && wrap ? lxn : lx) + (f % NB) * 32 * kRowB;
-        fb[f % 4][ACT8 ? m : 0] = read_x<ACT8>(row, wrap ? (KS + 1) % NK : KS, m, xt);
-      }
+      if (ACT8 || m == 0)
+        fb[f % 4][ACT8 ? m : 0] = read_x<ACT8>((next ? lxn : lx) + (f % NB) * 32 * kRowB, f / NB, m, xt);
       if (n == NB - 1) {
         fa[m][KS] = load_w(c, m, s2, KS, on);
-        if (kLast) sw[m] = load_ws(c, m, s2, on);
+        if (KS == NK - 1) sw[m] = load_ws(c, m, s2, on);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -852,7 +851,7 @@ __global__ __launch_bounds__(256, 2) void k_mlp_tile(MlpArgs p, int nti, int ntt
   for (int n = 0; n < kAhead; n++)
 #pragma unroll
     for (int e = 0; e < (ACT8 ? 2 : 1); e++)
-      fb[n][e] = read_x<ACT8>(L.x[0] + xrow + n * 32 * kRowB, 0, e, xt);
+      fb[n][e] = read_x<ACT8>(L.x[0] + xrow + (n % NB) * 32 * kRowB, n / NB, e, xt);
 
   // stage s of period position J: fragments fa[J % 2], token buffer s % 4, while stage s + 2 loads
   // into the registers it frees and buffer (s + 2) % 4
@@ -898,9 +897,8 @@ __global__ __launch_bounds__(256, 2) void k_mlp_tile(MlpArgs p, int nti, int ntt
 
 // ---------------------------------------------------------------------------------- host
 
-template <bool ACT8, bool GATED, int OUT>
+template <bool ACT8, bool GATED, int OUT, int NB>
 hipError_t launch_tile(const MlpArgs& p, hipStream_t s) {
-  constexpr int NB = 4;
   const int nti = (p.out + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
   const int ntt = (p.tokens + 32 * NB - 1) / (32 * NB);
   hipLaunchKernelGGL((k_mlp_tile<ACT8, GATED, NB, OUT>), dim3((unsigned)(nti * ntt)), dim3(256), 0,
@@ -920,34 +918,34 @@ hipError_t launch_split(const MlpArgs& p, hipStream_t s) {
 
 // Which kernel, by the number of 32 x 32 blocks of results (row blocks times 32-token blocks).
 // With few the split kernel brings the whole chip to bear on k, in the smallest tile (M row
-// blocks by NB token blocks) that still fits it in about one round; with many the tile kernel
-// reads each operand fewer times. Measured, us (MXFP4 / MXFP8 activations):
-//   single 4096 -> 4096     tokens   64 (256 blocks)   128 (512)   256 (1024)  512 (2048)  1024
-//     32 x 32                         5.2 /  7.6        7.1 / 11    11 / 19     18 / 34     32 / 62
-//     64 x 32                         6.6 /  7.8        6.8 / 8.4   9.5 / 12    15 / 21     26 / 36
-//     64 x 64                         8.4 / 11          8.5 / 11    8.9 / 12    13 / 19     24 / 34
-//     64 x 128                        11  / 13          13  / 16    13 / 17     14 / 22     27 / 40
-//     tile                            22  / 27          17  / 22    17 / 22     17 / 23     18 / 24
-//   single 14336 -> 4096, 512 tokens (2048): 64 x 64 33 / 49, 64 x 128 28 / 48, tile 41 / 60
-//   gated 2048 -> 5632, tokens 128 (704): 32 x 32 8.9 / 10, 32 x 64 9.3 / 11, tile 11 / 14
-//   gated 4096 -> 14336, tokens 32 (448): 12.7 / 14, 13.6 / 16, -;  64 (896): 21 / 24, 15 / 20,
-//     17 / 22;  96 (1344): 30 / 33, 24 / 30, 18 / 23
+// blocks by NB token blocks) that still fits it in about one round; with more the tile kernel
+// reads each operand fewer times, in tiles of 64 tokens as long as those do not fill the chip
+// twice over (one a CU), else of 128. Measured, us (MXFP4 / MXFP8 activations):
+//   single 4096 -> 4096     tokens   64 (256 blocks)  128 (512)  256 (1024)  512 (2048)  1024
+//     split 32 x 32                   5.2 /  7.6       7.1 / 11   11  / 19    18 / 34     32 / 62
+//     split 64 x 32                   6.6 /  7.8       6.8 / 8.4  9.5 / 12    15 / 21     26 / 36
+//     split 64 x 64                   8.4 / 11         8.5 / 11   8.9 / 12    14 / 19     24 / 34
+//     tile of 64 tokens               10  / 13         13  / 15   13  / 15    13 / 16     16 / 21
+//     tile of 128 tokens              22  / 27         17  / 22   17  / 22    17 / 23     18 / 24
+//   single 4096 -> 14336, tokens 64 (896): split 64 x 64 11 / 15, tiles 13 / 16, 25 / 31;
+//     256 (224 tiles of 64 tokens): 27 / 36, 16 / 18, 18 / 24;  512 (448): 44 / 63, 25 / 31, 22 / 29
+//   gated 2048 -> 5632, tokens 128 (704): split 8.9 / 10, tiles 8.9 / 10, 11 / 14
+//   gated 4096 -> 14336, tokens 32 (448): split 13 / 14;  64 (896): 21 / 24, tiles 14 / 17, 17 / 23
 // A single block of tokens always splits: 8192 -> 28672 at 32 tokens 29 / 36 in 64 x 32.
 template <bool ACT8, bool GATED, int OUT>
 hipError_t launch_t(const MlpArgs& p, hipStream_t s) {
-  const int64_t ntb = (p.tokens + 31) / 32, blocks = (p.out + 31) / 32 * ntb;
+  const int64_t nrb = (p.out + 31) / 32, ntb = (p.tokens + 31) / 32, blocks = nrb * ntb;
   if constexpr (GATED) {
-    if (blocks <= 768 || ntb == 1) return launch_split<ACT8, true, OUT, 2, 1>(p, s);
-    if (blocks <= 1024) return launch_split<ACT8, true, OUT, 2, 2>(p, s);
+    if (blocks <= 704 || ntb == 1) return launch_split<ACT8, true, OUT, 2, 1>(p, s);
   } else {
     if (blocks <= 256) return launch_split<ACT8, false, OUT, 1, 1>(p, s);
     if (blocks <= 512 || ntb == 1) return launch_split<ACT8, false, OUT, 2, 1>(p, s);
-    if (blocks <= 2048) {
-      if (ACT8 || blocks <= 1024 || ntb == 2) return launch_split<ACT8, false, OUT, 2, 2>(p, s);
-      if constexpr (!ACT8) return launch_split<ACT8, false, OUT, 2, 4>(p, s);
-    }
+    if (blocks <= 1024) return launch_split<ACT8, false, OUT, 2, 2>(p, s);
   }
-  return launch_tile<ACT8, GATED, OUT>(p, s);
+  constexpr int kRows = GATED ? 4 : 8;
+  const int64_t tiles64 = ((nrb + kRows - 1) / kRows) * ((ntb + 1) / 2);
+  if (tiles64 <= 256) return launch_tile<ACT8, GATED, OUT, 2>(p, s);
+  return launch_tile<ACT8, GATED, OUT, 4>(p, s);
 }
 
 // Bytes of n elements of an output

@@ -231,8 +231,18 @@ def _residual(rng, tokens, out, dtype):
     return r, to_device(_bits(r), "bf16")
 
 
+def _sampled(rng, n, sample):
+    """All of 0 .. n - 1, or about `sample` of them: both ends, the neighbours of every 256-tile
+    edge and others at random."""
+    if sample is None or n <= sample:
+        return np.arange(n)
+    edges = np.concatenate([np.arange(0, n, 256), np.arange(255, n, 256), [0, n - 1]])
+    rest = rng.choice(n, max(1, sample - len(edges)), replace=False)
+    return np.unique(np.concatenate([edges, rest]))
+
+
 def _epilogue_check(dq, tokens, out, K, act_fmt="mxfp4", dtype="bf16", kind="none", a=True,
-                    bias=False, residual=False, inplace=False, seed=0):
+                    bias=False, residual=False, inplace=False, seed=0, sample=None):
     print(f"[epilogue] tokens={tokens} out={out} K={K} {act_fmt}->{dtype} {kind} a={a} bias={bias} "
           f"res={residual} inplace={inplace}", flush=True)
     rng = np.random.default_rng(seed + 77)
@@ -244,19 +254,27 @@ def _epilogue_check(dq, tokens, out, K, act_fmt="mxfp4", dtype="bf16", kind="non
     y = dq.gemm_mx_epilogue(_dev(xc), _dev(xs), _pack(dq, wc, ws), a=_dev(av), bias=_dev(bv),
                             activation=kind, residual=rd, act_fmt=act_fmt, out_dtype=dtype,
                             y=rd if inplace else None)
-    want, dy = ref.epilogue(xc, xs, act_fmt, wc, ws, av, bv, kind, rh)
-    ref.check_rounded(_f64(y), want, dy, dtype)
+    ts, cs = _sampled(rng, tokens, sample), _sampled(rng, out, sample)
+    want, dy = ref.epilogue(xc[ts], xs[ts], act_fmt, wc[cs], ws[cs], None if av is None else av[cs],
+                            None if bv is None else bv[cs], kind,
+                            None if rh is None else rh[np.ix_(ts, cs)])
+    ref.check_rounded(_f64(y)[np.ix_(ts, cs)], want, dy, dtype)
 
 
+# tokens, channels, K: single tokens, ragged sizes, every k count around the waves' shares, and
+# sizes that reach each kernel of the selection (32 x 32 blocks: up to 256, 512, 1024 and beyond;
+# tiles of 64 tokens up to 256 of them, then of 128)
 SHAPES = [(1, 4, 512), (1, 70, 1024), (2, 1000, 512), (17, 33, 1536), (32, 256, 512),
           (33, 260, 2048), (64, 96, 5120), (97, 131, 1024), (128, 512, 512), (130, 300, 2560),
-          (256, 256, 1024), (300, 520, 1536)]
+          (256, 256, 1024), (300, 520, 1536), (20, 9000, 512), (31, 8212, 1536),
+          (160, 3200, 1024), (300, 3300, 512), (333, 4004, 1536), (510, 6000, 512),
+          (700, 9001, 512), (1030, 5555, 1024)]
 
 
 @pytest.mark.parametrize("tokens,out,K", SHAPES)
 @pytest.mark.parametrize("act_fmt,dtype", [("mxfp4", "bf16"), ("mxfp4", "f32"), ("mxfp8", "bf16")])
 def test_epilogue_shapes(dq, tokens, out, K, act_fmt, dtype):
-    _epilogue_check(dq, tokens, out, K, act_fmt, dtype, residual=True, seed=tokens)
+    _epilogue_check(dq, tokens, out, K, act_fmt, dtype, residual=True, seed=tokens, sample=300)
 
 
 @pytest.mark.parametrize("kind", ACTS)
@@ -289,30 +307,44 @@ def test_epilogue_unaligned_output(dq, tokens):
         assert float(big[0]) == 7.0 and torch.all(big[1 + tokens * out:] == 7.0)
 
 
-def _gated_check(dq, tokens, inner, K, act_fmt="mxfp4", dtype="bf16", kind="silu", a=True, seed=0):
+def _gated_check(dq, tokens, inner, K, act_fmt="mxfp4", dtype="bf16", kind="silu", a=True, seed=0,
+                 sample=None):
     print(f"[gated] tokens={tokens} inner={inner} K={K} {act_fmt}->{dtype} {kind} a={a}", flush=True)
     xc, xs = _acts(tokens, K, act_fmt, seed + 1)
     gate, up = _weights(inner, K, seed + 2), _weights(inner, K, seed + 3)
     if not a:
         gate, up = (*gate[:2], None), (*up[:2], None)
     gp, upk = _pack(dq, *gate[:2]), _pack(dq, *up[:2])
-    want, dh = ref.gated(xc, xs, act_fmt, gate, up, kind)
+    rng = np.random.default_rng(seed + 8)
+    ts = _sampled(rng, tokens, sample)
+    if dtype in ("bf16", "f32"):
+        cs = _sampled(rng, inner, sample)
+    else:  # whole groups of 32 channels
+        gs = _sampled(rng, inner // 32, None if sample is None else sample // 32)
+        cs = (gs[:, None] * 32 + np.arange(32)).reshape(-1)
+    cut = lambda w: (w[0][cs], w[1][cs], None if w[2] is None else w[2][cs])  # noqa: E731
+    want, dh = ref.gated(xc[ts], xs[ts], act_fmt, cut(gate), cut(up), kind)
     kw = dict(a_gate=_dev(gate[2]), a_up=_dev(up[2]), activation=kind, act_fmt=act_fmt)
     if dtype in ("bf16", "f32"):
         h = dq.gated_mx(_dev(xc), _dev(xs), gp, upk, out_dtype=dtype, **kw)
-        ref.check_rounded(_f64(h), want, dh, dtype)
+        ref.check_rounded(_f64(h)[np.ix_(ts, cs)], want, dh, dtype)
         return
     b = np.random.default_rng(seed + 9).uniform(0.5, 2.0, inner).astype(np.float32) if a else None
     q = dq.gated_mx_quantized(_dev(xc), _dev(xs), gp, upk, dtype, b=_dev(b), **kw)
     if b is not None:
-        want, dh = want * b, dh * b + np.abs(want * b) * ref.U24
-    ref.check_quantized(host(q["codes"]), host(q["scales"]), want, dh, dtype)
+        want, dh = want * b[cs], dh * b[cs] + np.abs(want * b[cs]) * ref.U24
+    codes = host(q["codes"])
+    per = codes.shape[1] * 32 // inner  # code bytes of a group
+    codes = codes.reshape(tokens, inner // 32, per)[np.ix_(ts, gs)].reshape(len(ts), -1)
+    ref.check_quantized(codes, host(q["scales"])[np.ix_(ts, gs)], want, dh, dtype)
 
 
 @pytest.mark.parametrize("tokens,inner,K", [(1, 32, 512), (1, 1056, 1024), (2, 64, 512),
                                             (31, 96, 1536), (32, 256, 512), (33, 160, 2048),
                                             (64, 128, 5120), (100, 416, 1024), (129, 256, 512),
-                                            (256, 128, 1024), (300, 544, 1536)])
+                                            (256, 128, 1024), (300, 544, 1536),
+                                            (20, 22560, 512), (90, 8000, 512), (190, 5632, 1536),
+                                            (400, 3200, 1024), (610, 6464, 512)])
 @pytest.mark.parametrize("act_fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32", "mxfp4", "mxfp8"])
 def test_gated_shapes(dq, tokens, inner, K, act_fmt, dtype):
@@ -320,7 +352,7 @@ def test_gated_shapes(dq, tokens, inner, K, act_fmt, dtype):
         dtype, kind = "bf16", "relu"  # fp32 is refused for MXFP8 activations
     else:
         kind = "silu"
-    _gated_check(dq, tokens, inner, K, act_fmt, dtype, kind, seed=tokens)
+    _gated_check(dq, tokens, inner, K, act_fmt, dtype, kind, seed=tokens, sample=320)
 
 
 @pytest.mark.parametrize("kind", ACTS)
