@@ -32,6 +32,7 @@ namespace dqm {
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
@@ -41,6 +42,7 @@ constexpr int kPackStageB = 4096;     // packed codes of (row block, stage)
 constexpr int kPackScaleB = 256;      // packed scales of (row block, stage)
 constexpr uint32_t kBufRsrcWord3 = 0x00020000u;  // raw buffer, 32-bit data format
 constexpr uint32_t kOob = 0x80000000u;           // an offset past every buffer: reads zero
+constexpr int kNt = 2;  // cache policy of buffer stores: nontemporal (written once, not read here)
 
 enum Out : int { kOutF32 = 0, kOutBf16 = 1, kOutFp4 = 2, kOutFp8 = 3 };
 
@@ -580,7 +582,8 @@ __device__ __forceinline__ void tile_step(v16f (&acc)[2][NB], u32x4 (&fa)[2][ste
 //     channels instead of 8 or 16 bytes of 32 rows. The single product applies its factors
 //     there, where a lane has the same 4 channels in every row, and loads its residual one
 //     chunk ahead.
-// FULL: the tile lies inside the tokens and channels and takes 4-channel accesses.
+// FULL: the tile lies inside the tokens and channels and takes 4-channel accesses (and its rows'
+// offsets stay below 2^31).
 template <bool GATED, int OUT>
 __device__ __forceinline__ void quantize_chunk(const MlpArgs& p, f32x4 (&y)[4], int t, int rb,
                                                int h, bool in) {
@@ -651,20 +654,29 @@ __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2
     bias = load_channels(p.bias, ich, p.out, 0.0f);
   }
   __syncthreads();  // every wave is done with the main loop's LDS
-  typedef typename std::conditional<OUT == kOutF32, f32x4, bf16x4>::type row4;
-  row4 res[NR];
+  // FULL: rows through buffer accesses relative to the wave's first channel of the tile's first
+  // token, the row step in the scalar offset
+  constexpr int kEs = OUT == kOutF32 ? 4 : 2;
+  const int pitch = p.out * kEs;
+  const int64_t corner = ((int64_t)t0 * p.out + rb0 * 32) * kEs;
+  const uint32_t span = FULL ? (uint32_t)(32 * NB - 1) * (uint32_t)pitch + 32u * ME * kEs : 0u;
+  const __amdgpu_buffer_rsrc_t ry = rsrc(static_cast<char*>(p.y) + corner, span);
   const bool has_res = FULL && !GATED && p.res;
+  const __amdgpu_buffer_rsrc_t rr4 = rsrc(static_cast<const char*>(has_res ? p.res : p.y) + corner, span);
+  const uint32_t vrow = (uint32_t)rr * (uint32_t)pitch + (uint32_t)(cl * 4 * kEs);
+  typedef typename std::conditional<OUT == kOutF32, u32x4, u32x2>::type raw4;
+  raw4 res[NR];
   auto fetch = [&](int n) {
     if (has_res) {
 #pragma unroll
       for (int r = 0; r < NR; r++) {
-        const int64_t t = t0 + n * 32 + r * (64 / LPR) + rr;
-        res[r] = *reinterpret_cast<const row4*>(
-            static_cast<const char*>(p.res) + (t * p.out + ich) * (OUT == kOutF32 ? 4 : 2));
+        const uint32_t so = (uint32_t)(n * 32 + r * (64 / LPR)) * (uint32_t)pitch;
+        if constexpr (OUT == kOutF32) res[r] = __builtin_amdgcn_raw_buffer_load_b128(rr4, vrow, so, 0);
+        else res[r] = __builtin_amdgcn_raw_buffer_load_b64(rr4, vrow, so, 0);
       }
     }
   };
-  if (OUT < kOutFp4) fetch(0);
+  if constexpr (OUT < kOutFp4) fetch(0);
 #pragma unroll
   for (int n = 0; n < NB; n++) {
     __builtin_amdgcn_sched_barrier(0);  // one chunk's registers at a time
@@ -712,21 +724,29 @@ __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2
               for (int e = 0; e < 4; e++)
                 v[r][e] = activation<decltype(k)::value>(v[r][e] * as[e] + bias[e]);
           });
+        if (has_res) {
+#pragma unroll
+          for (int r = 0; r < NR; r++) {
+            if constexpr (OUT == kOutF32) {
+              v[r] = __builtin_bit_cast(f32x4, res[r]) + v[r];
+            } else {
+              const bf16x4 x = __builtin_bit_cast(bf16x4, res[r]);
+#pragma unroll
+              for (int e = 0; e < 4; e++) v[r][e] = (float)x[e] + v[r][e];
+            }
+          }
+          if (n + 1 < NB) fetch(n + 1);
+        }
 #pragma unroll
         for (int r = 0; r < NR; r++) {
-          const int64_t off = (int64_t)(t0 + n * 32 + r * (64 / LPR) + rr) * p.out + ich;
-          if (has_res) {
-#pragma unroll
-            for (int e = 0; e < 4; e++) v[r][e] = (float)res[r][e] + v[r][e];
-          }
-          if constexpr (OUT == kOutBf16) {
-            const bf16x4 o = {(__bf16)v[r][0], (__bf16)v[r][1], (__bf16)v[r][2], (__bf16)v[r][3]};
-            __builtin_nontemporal_store(o, reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.y) + off));
+          const uint32_t so = (uint32_t)(n * 32 + r * (64 / LPR)) * (uint32_t)pitch;
+          if constexpr (OUT == kOutF32) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v[r]), ry, vrow, so, kNt);
           } else {
-            __builtin_nontemporal_store(v[r], reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + off));
+            const bf16x4 o = {(__bf16)v[r][0], (__bf16)v[r][1], (__bf16)v[r][2], (__bf16)v[r][3]};
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), ry, vrow, so, kNt);
           }
         }
-        if (n + 1 < NB) fetch(n + 1);
       } else {
 #pragma unroll 1
         for (int r = 0; r < NR; r++) {
@@ -889,7 +909,8 @@ __global__ __launch_bounds__(256, 2) void k_mlp_tile(MlpArgs p, int nti, int ntt
   // epilogue reuses that memory
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
   uint8_t* region = lds + (OUT >= kOutFp4 ? 0 : wave * kWaveStaging<GATED>);
-  if (rows == 32 * NB && (rb0 + (GATED ? 1 : 2)) * 32 <= p.out && (OUT >= kOutFp4 || p.vec))
+  if (rows == 32 * NB && (rb0 + (GATED ? 1 : 2)) * 32 <= p.out &&
+      (OUT >= kOutFp4 || (p.vec && p.out <= (1 << 21))))
     tile_store<GATED, NB, OUT, true>(p, acc, rb0, t0, region);
   else
     tile_store<GATED, NB, OUT, false>(p, acc, rb0, t0, region);
