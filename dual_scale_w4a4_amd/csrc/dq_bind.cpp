@@ -134,12 +134,12 @@ constexpr const char* kActs[] = {"none", "relu", "silu", "gelu", "gelu_tanh"};
 // ------------------------------------------------------------------- norm and quantizer
 
 struct QuantShape {
-  int fmt, group;
-  int64_t tokens, cols;
+  int fmt;
+  int64_t group, tokens, cols;
   at::ScalarType scale_type;
 
   QuantShape(const at::Tensor& X, PyObject* f, PyObject* g)
-      : fmt(choice(f, kFmts, "format")), group((int)integer(g)), tokens(X.size(0)), cols(X.size(1)) {
+      : fmt(choice(f, kFmts, "format")), group(integer(g)), tokens(X.size(0)), cols(X.size(1)) {
     if ((group != 16 && group != 32 && group != 64) || cols % group)
       refuse("group must be 16, 32 or 64 and divide the channels");
     scale_type = fmt == DQ_FMT_INT4_BF16 ? at::kShort : at::kByte;
@@ -194,7 +194,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t) {
       refuse("status must be an int32 tensor on X's device");
     const Place place(arr.dev, a[13]);
     check(dq_norm_quantize_act_async(X.data_ptr(), dt, residual, residual_out, q.tokens, q.cols,
-                                     weight, wt, eps, b, (dq_format)q.fmt, q.group, g,
+                                     weight, wt, eps, b, (dq_format)q.fmt, (int)q.group, g,
                                      static_cast<uint8_t*>(codes), scales,
                                      static_cast<int*>(st.data_ptr()), place.stream),
           "dq_norm_quantize_act_async");
@@ -208,10 +208,13 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t) {
       bytes = w.nbytes();
     }
     const Place place(arr.dev, a[13]);
-    check(dq_norm_quantize_act(X.data_ptr(), dt, residual, residual_out, q.tokens, q.cols, weight,
-                               wt, eps, b, (dq_format)q.fmt, q.group, g,
-                               static_cast<uint8_t*>(codes), scales, ws, bytes, place.stream),
-          "dq_norm_quantize_act");
+    dq_status st;
+    Py_BEGIN_ALLOW_THREADS  // it waits for the stream
+    st = dq_norm_quantize_act(X.data_ptr(), dt, residual, residual_out, q.tokens, q.cols, weight,
+                              wt, eps, b, (dq_format)q.fmt, (int)q.group, g,
+                              static_cast<uint8_t*>(codes), scales, ws, bytes, place.stream);
+    Py_END_ALLOW_THREADS
+    check(st, "dq_norm_quantize_act");
   }
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS

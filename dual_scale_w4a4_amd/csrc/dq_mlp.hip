@@ -653,7 +653,6 @@ __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2
     as = load_channels(p.a[0], ich, p.out, 1.0f);
     bias = load_channels(p.bias, ich, p.out, 0.0f);
   }
-  __syncthreads();  // every wave is done with the main loop's LDS
   // FULL: rows through buffer accesses relative to the wave's first channel of the tile's first
   // token, the row step in the scalar offset
   constexpr int kEs = OUT == kOutF32 ? 4 : 2;
@@ -908,6 +907,7 @@ __global__ __launch_bounds__(256, 2) void k_mlp_tile(MlpArgs p, int nti, int ntt
   // the last stages' loads read nothing but still write zeros into LDS: drain them before the
   // epilogue reuses that memory
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  __syncthreads();  // every wave is done with the main loop's LDS
   uint8_t* region = lds + (OUT >= kOutFp4 ? 0 : wave * kWaveStaging<GATED>);
   if (rows == 32 * NB && (rb0 + (GATED ? 1 : 2)) * 32 <= p.out &&
       (OUT >= kOutFp4 || (p.vec && p.out <= (1 << 21))))
@@ -1001,11 +1001,6 @@ hipError_t launch_o(const MlpArgs& whole, bool act8, hipStream_t s) {
   return hipSuccess;
 }
 
-bool overlap(const void* p, size_t pb, const void* q, size_t qb) {
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  return a < b + qb && b < a + pb;
-}
-
 // The checks that the products share. Sizes first: they bound the rest.
 dq_status check_product(const void* xc, const void* xs, dq_format act_fmt, int64_t tokens,
                         int64_t K, const void* wc, const void* ws, const void* a, int64_t out,
@@ -1014,11 +1009,17 @@ dq_status check_product(const void* xc, const void* xs, dq_format act_fmt, int64
   if ((int)act < 0 || (int)act > DQ_ACTIVATION_GELU_TANH) return DQ_ERR_UNSUPPORTED;
   if (!xc || !xs || !wc || !ws) return DQ_ERR_ARG;
   if (tokens < 1 || out < 1 || K < 512 || K % 512 != 0 || K > (1 << 22)) return DQ_ERR_ARG;
-  if (tokens > INT32_MAX - 256 || out > INT32_MAX - 256) return DQ_ERR_ARG;
+  if (tokens > INT32_MAX - 256 || out > (1 << 28)) return DQ_ERR_ARG;
   if (((uintptr_t)xc | (uintptr_t)xs | (uintptr_t)wc | (uintptr_t)a) & 15u) return DQ_ERR_ARG;
   if ((uintptr_t)ws & 3u) return DQ_ERR_ARG;
   return DQ_OK;
 }
+
+// The bytes of a product's operands
+size_t act_bytes(dq_format fmt, int64_t tokens, int64_t K) {
+  return (size_t)tokens * (size_t)(fmt == DQ_FMT_MXFP8 ? K : K / 2);
+}
+size_t packed_bytes(int64_t out, int64_t K) { return (size_t)((out + 31) / 32) * 16 * (size_t)K; }
 
 }  // namespace dqm
 
@@ -1040,7 +1041,16 @@ dq_status dq_gemm_mx_epilogue(const uint8_t* act_codes, const uint8_t* act_scale
   if (!Y || ((uintptr_t)bias & 15u) || (((uintptr_t)Y | (uintptr_t)residual) & (esz - 1)))
     return DQ_ERR_ARG;
   const size_t bytes = (size_t)tokens * (size_t)out * esz;
-  if (residual && residual != Y && overlap(residual, bytes, Y, bytes)) return DQ_ERR_ARG;
+  const size_t wb = packed_bytes(out, K), vb = (size_t)out * 4;
+  if (dq::any_overlap({{Y, bytes}},
+                      {{residual == Y ? nullptr : residual, bytes},
+                       {act_codes, act_bytes(act_fmt, tokens, K)},
+                       {act_scales, (size_t)(tokens * (K / 32))},
+                       {packed_codes, wb},
+                       {packed_scales, wb / 16},
+                       {a, vb},
+                       {bias, vb}}))
+    return DQ_ERR_ARG;
   MlpArgs p{};
   p.xc = act_codes;
   p.xs = act_scales;
@@ -1077,6 +1087,17 @@ dq_status dq_gated_mx(const uint8_t* act_codes, const uint8_t* act_scales, dq_fo
     return DQ_ERR_UNSUPPORTED;
   const size_t esz = yt == DQ_BF16 ? 2 : 4;
   if (!H || ((uintptr_t)H & (esz - 1))) return DQ_ERR_ARG;
+  const size_t wb = packed_bytes(inner, K), vb = (size_t)inner * 4;
+  if (dq::any_overlap({{H, (size_t)tokens * (size_t)inner * esz}},
+                      {{act_codes, act_bytes(act_fmt, tokens, K)},
+                       {act_scales, (size_t)(tokens * (K / 32))},
+                       {gate_codes, wb},
+                       {gate_scales, wb / 16},
+                       {up_codes, wb},
+                       {up_scales, wb / 16},
+                       {a_gate, vb},
+                       {a_up, vb}}))
+    return DQ_ERR_ARG;
   MlpArgs p{};
   p.xc = act_codes;
   p.xs = act_scales;
@@ -1116,6 +1137,19 @@ dq_status dq_gated_mx_quantized(const uint8_t* act_codes, const uint8_t* act_sca
   if (fmt != DQ_FMT_MXFP4 && fmt != DQ_FMT_MXFP8) return DQ_ERR_UNSUPPORTED;
   if (!codes || !scales || inner % 32 != 0) return DQ_ERR_ARG;
   if (((uintptr_t)codes | (uintptr_t)b) & 15u) return DQ_ERR_ARG;
+  const size_t wb = packed_bytes(inner, K), vb = (size_t)inner * 4;
+  if (dq::any_overlap({{codes, act_bytes(fmt, tokens, inner)},
+                       {scales, (size_t)(tokens * (inner / 32))}},
+                      {{act_codes, act_bytes(act_fmt, tokens, K)},
+                       {act_scales, (size_t)(tokens * (K / 32))},
+                       {gate_codes, wb},
+                       {gate_scales, wb / 16},
+                       {up_codes, wb},
+                       {up_scales, wb / 16},
+                       {a_gate, vb},
+                       {a_up, vb},
+                       {b, vb}}))
+    return DQ_ERR_ARG;
   MlpArgs p{};
   p.xc = act_codes;
   p.xs = act_scales;

@@ -375,12 +375,6 @@ static hipError_t launch_norm(int fmt, int G, bool bf16, const NormArgs& whole, 
   return hipSuccess;
 }
 
-// whether [p, p + bytes) and [q, q + bytes) overlap without being the same array
-static bool clash(const void* p, const void* q, size_t bytes) {
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  return a != b && a < b + bytes && b < a + bytes;
-}
-
 // The host-side checks of both forms, and the kernel's arguments but for the status word.
 static dq_status norm_args(const void* X, dq_dtype xt, const void* residual, void* residual_out,
                            int64_t tokens, int64_t cols, const void* weight, dq_dtype wt,
@@ -401,7 +395,14 @@ static dq_status norm_args(const void* X, dq_dtype xt, const void* residual, voi
   if ((uintptr_t)codes & (fmt == DQ_FMT_MXFP8 ? 15u : 7u)) return DQ_ERR_ARG;
   if (fmt == DQ_FMT_INT4_BF16 && ((uintptr_t)inner_scales & 1u)) return DQ_ERR_ARG;
   const size_t bytes = (size_t)tokens * (size_t)cols * (xt == DQ_BF16 ? 2 : 4);
-  if (residual && (clash(residual_out, residual, bytes) || clash(residual_out, X, bytes)))
+  const size_t n = (size_t)tokens * (size_t)cols, vb = (size_t)cols * 4;
+  if (any_overlap({{codes, fmt == DQ_FMT_MXFP8 ? n : n / 2},
+                   {inner_scales, n / (size_t)group * (fmt == DQ_FMT_INT4_BF16 ? 2 : 1)},
+                   {residual_out, bytes}},
+                  {{X == residual_out ? nullptr : X, bytes},
+                   {residual == residual_out ? nullptr : residual, bytes},
+                   {weight, wt == DQ_BF16 ? vb / 2 : vb},
+                   {b, vb}}))
     return DQ_ERR_ARG;
   p->X = X;
   p->R = residual;
@@ -444,11 +445,11 @@ dq_status dq_norm_quantize_act(const void* X, dq_dtype xt, const void* residual,
                                void* inner_scales, void* workspace, size_t workspace_bytes,
                                hipStream_t stream) {
   using namespace dq;
+  if (workspace && workspace_bytes < DQ_NORM_WORKSPACE_BYTES) return DQ_ERR_WORKSPACE;
   NormArgs p{};
   dq_status st = norm_args(X, xt, residual, residual_out, tokens, cols, weight, wt, eps, b, fmt,
                            group, g, codes, inner_scales, &p);
   if (st != DQ_OK) return st;
-  if (workspace && workspace_bytes < DQ_NORM_WORKSPACE_BYTES) return DQ_ERR_WORKSPACE;
   if ((uintptr_t)workspace & 255u) return DQ_ERR_ARG;
   void* ws = workspace;
   if (!ws && hipMallocAsync(&ws, DQ_NORM_WORKSPACE_BYTES, stream) != hipSuccess) return DQ_ERR_HIP;

@@ -6,6 +6,29 @@
 
 namespace dq {
 
+// An array of a call, for the host's checks of what may overlap
+struct Span {
+  const void* p;  // null: not given
+  size_t bytes;
+};
+
+inline bool overlap(const Span& s, const Span& t) {
+  const uintptr_t a = (uintptr_t)s.p, b = (uintptr_t)t.p;
+  return s.p && t.p && a < b + t.bytes && b < a + s.bytes;
+}
+
+// whether an output overlaps an input or another output
+template <size_t O, size_t I>
+bool any_overlap(const Span (&out)[O], const Span (&in)[I]) {
+  for (size_t o = 0; o < O; o++) {
+    for (size_t i = 0; i < I; i++)
+      if (overlap(out[o], in[i])) return true;
+    for (size_t k = 0; k < o; k++)
+      if (overlap(out[o], out[k])) return true;
+  }
+  return false;
+}
+
 constexpr int kMxFp8 = 4;  // DQ_FMT_MXFP8
 
 // The E8M0 divisor of an MXFP4 (EMAX 2) or MXFP8 (EMAX 8) group from the bits of its largest

@@ -12,7 +12,8 @@
  *
  * The conventions are dq.h's: dense row-major device arrays owned by the caller, host-side
  * argument checks before anything is enqueued, no state between calls, deterministic results
- * (no floating-point atomics; the order of every sum depends on the shape alone). The calls
+ * (no floating-point atomics; the order of every sum depends on the shape alone). An output
+ * overlaps neither an input nor another output (DQ_ERR_ARG) but where a call says so. The calls
  * allocate nothing and use no workspace unless they say so, so they can be captured into a
  * graph. `stream` belongs to the current device, where the arrays are.
  */
@@ -49,8 +50,7 @@ typedef enum {
  * and then the group quantizer of dq_quantize_act on x, bit for bit.
  *  X:            tokens x cols, fp32 or bf16 (xt), 16-byte aligned.
  *  residual:     as X, or NULL.  residual_out: out, h, as X; both are given or neither is.
- *                residual_out may equal residual or X (updated in place); otherwise the arrays
- *                must not overlap.
+ *                residual_out may equal residual or X (updated in place).
  *  weight:       cols values of type wt (fp32 or bf16), 16-byte aligned, or NULL for ones.
  *  eps:          > 0, finite.
  *  b:            cols floats > 0, 16-byte aligned, or NULL for ones.
@@ -86,13 +86,12 @@ dq_status dq_norm_quantize_act(const void* X, dq_dtype xt, const void* residual,
  *                (tokens x K bytes), group 32, both 16-byte aligned; scales tokens x K/32.
  *  packed_codes, packed_scales: as for dq_gemm_mx_packed (out x K, K % 512 == 0, K <= 2^22).
  *  a, bias:      out floats, 16-byte aligned, or NULL (ones / zeros).
- *  residual:     tokens x out of Y's type, or NULL; may equal Y, and must not overlap it
- *                otherwise.
+ *  residual:     tokens x out of Y's type, or NULL; may equal Y.
  *  Y:            out, tokens x out, fp32 or bf16 (yt), aligned to its element; likewise residual.
  * MXFP8 activations give bf16 only: in its 8-bit mode the matrix instruction aligns the products
  * of 16 neighbouring k to about 14 bits below the largest, which bf16 does not show and fp32
- * would. An E8M0 byte 0xFF makes the outputs it reaches NaN. tokens, out < 2^31 - 256. Only
- * enqueues. */
+ * would. An E8M0 byte 0xFF makes the outputs it reaches NaN. tokens < 2^31 - 256, out <= 2^28.
+ * Only enqueues. */
 dq_status dq_gemm_mx_epilogue(const uint8_t* act_codes, const uint8_t* act_scales,
                               dq_format act_fmt, int64_t tokens, int64_t K,
                               const uint8_t* packed_codes, const uint8_t* packed_scales,

@@ -307,6 +307,28 @@ def test_epilogue_unaligned_output(dq, tokens):
         assert float(big[0]) == 7.0 and torch.all(big[1 + tokens * out:] == 7.0)
 
 
+def test_epilogue_channels_past_two_million(dq):
+    # whole tiles whose rows lie further apart than a 31-bit tile offset allows: 4096 weight rows
+    # repeated, so that every block of 4096 channels must equal the first, in place on a residual
+    import torch
+
+    tokens, K, rows, out = 130, 512, 4096, (1 << 21) + 36
+    print(f"[epilogue] tokens={tokens} out={out}", flush=True)
+    xc, xs = _acts(tokens, K, "mxfp4", 6)
+    wc, ws, _ = _weights(rows, K, 7)
+    many = lambda w: _dev(w).repeat(out // rows + 1, 1)[:out].contiguous()  # noqa: E731
+    pk = dq.gemm_pack_weights(many(wc), many(ws))
+    y = torch.full((tokens, out), 2.0, dtype=torch.bfloat16, device="cuda")
+    assert dq.gemm_mx_epilogue(_dev(xc), _dev(xs), pk, residual=y, y=y) is y
+    whole = y[:, :out // rows * rows].view(tokens, -1, rows)
+    assert torch.equal(whole, whole[:, :1].expand_as(whole))
+    assert torch.equal(y[:, out // rows * rows:], y[:, :out % rows])
+    ts = _sampled(np.random.default_rng(8), tokens, 16)
+    want, dy = ref.epilogue(xc[ts], xs[ts], "mxfp4", wc, ws, None, None, "none",
+                            np.full((len(ts), rows), 2.0))
+    ref.check_rounded(_f64(y[:, :rows])[ts], want, dy, "bf16")
+
+
 def _gated_check(dq, tokens, inner, K, act_fmt="mxfp4", dtype="bf16", kind="silu", a=True, seed=0,
                  sample=None):
     print(f"[gated] tokens={tokens} inner={inner} K={K} {act_fmt}->{dtype} {kind} a={a}", flush=True)
@@ -516,6 +538,51 @@ def test_block_in_a_graph_on_other_streams_and_twice(dq):
         for other in (graphed, side):
             assert all(torch.equal(p, q) for p, q in zip(eager, other)), k
     assert int(status.item()) == 0
+
+
+def test_a_stream_added_to_itself(dq, oracle_lib):
+    # X, residual and residual_out the same array
+    for dtype in ("bf16", "f32"):
+        for cols in (1024, 16416):
+            c = _norm_case(5, cols, dtype, seed=87)
+            c["R"], c["Rf"] = c["X"], c["Xf"]
+            x = to_device(c["X"], dtype)
+            got = dq.norm_quantize_act(x, "mxfp8", 32, residual=x, residual_out=x)
+            h, codes, scales = _norm_want(oracle_lib, c, "mxfp8", 32, 1e-5, w=False, b=False)
+            assert got["residual"] is x and np.array_equal(x.float().cpu().numpy(), h)
+            assert np.array_equal(host(got["codes"]), codes)
+            assert np.array_equal(host(got["scales"]), scales)
+
+
+def test_blocking_norm_from_two_threads(dq):
+    # the wait lets other Python threads run, and each call reports its own rows' errors
+    import threading
+
+    import torch
+
+    X = torch.randn(64, 1024, device="cuda")
+    bad = X.clone()
+    bad[3, 5] = float("nan")
+    want = dq.norm_quantize_act(X, "mxfp8", 32)["codes"]
+    seen = {}
+
+    def work(name, x):
+        s = torch.cuda.Stream()
+        seen[name] = []
+        for _ in range(8):
+            try:
+                q = dq.norm_quantize_act(x, "mxfp8", 32, stream=s)
+                seen[name].append(bool(torch.equal(q["codes"], want)))
+            except dq.DQError as e:
+                seen[name].append(e.status)
+
+    torch.cuda.synchronize()
+    ts = [threading.Thread(target=work, args=a) for a in (("good", X), ("bad", bad))]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert seen == {"good": [True] * 8, "bad": [3] * 8}
 
 
 def test_rows_behind_the_last_token_stay(dq):

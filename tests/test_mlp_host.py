@@ -134,6 +134,51 @@ def test_gated_quantized_arguments_are_refused(dqlib, change, want):
     assert dqlib.lib().dq_gated_mx_quantized(*dict(GATEDQ, **change).values(), None) == want
 
 
+def _apart(call, **pointers):
+    """The call with every array at an address of its own (never dereferenced)."""
+    names = [k for k, v in call.items() if isinstance(v, ctypes.c_void_p)]
+    return {**call, **{k: ctypes.c_void_p((i + 1) << 44) for i, k in enumerate(names)}, **pointers}
+
+
+def _at(call, other, offset=0):
+    return ctypes.c_void_p(_apart(call)[other].value + offset)
+
+
+@pytest.mark.parametrize("call,entry,out,others", [
+    (NORM, "dq_norm_quantize_act_async", "codes", ["X", "R", "h", "w", "b", "scales"]),
+    (NORM, "dq_norm_quantize_act_async", "scales", ["X", "R", "h", "w", "b", "codes"]),
+    (NORM, "dq_norm_quantize_act_async", "h", ["w", "b"]),
+    (EPI, "dq_gemm_mx_epilogue", "y", ["xc", "xs", "wc", "ws", "a", "bias"]),
+    (GATED, "dq_gated_mx", "y", ["xc", "xs", "gc", "gs", "ag", "uc", "us", "au"]),
+    (GATEDQ, "dq_gated_mx_quantized", "codes", ["xc", "xs", "gc", "gs", "ag", "uc", "us", "au", "b"]),
+    (GATEDQ, "dq_gated_mx_quantized", "scales", ["xc", "gs", "au", "b", "codes"]),
+])
+def test_overlapping_outputs_are_refused(dqlib, call, entry, out, others):
+    tail = [FAKE, None] if entry.endswith("async") else [None]
+    for o in others:
+        for offset in (0, 16):
+            args = list(_apart(call, **{out: _at(call, o, offset)}).values())
+            assert getattr(dqlib.lib(), entry)(*args, *tail) == ARG, (out, o, offset)
+
+
+def test_in_place_residuals_overlap_exactly_or_not_at_all(dqlib):
+    L = dqlib.lib()
+    for other in ("X", "R"):
+        args = list(_apart(NORM, h=_at(NORM, other, 16)).values())
+        assert L.dq_norm_quantize_act_async(*args, FAKE, None) == ARG
+    shifted = _apart(NORM, h=_at(NORM, "X"), R=_at(NORM, "X", 32))  # h is X, but cuts into R
+    assert L.dq_norm_quantize_act_async(*shifted.values(), FAKE, None) == ARG
+    args = list(_apart(EPI, y=_at(EPI, "res", 16)).values())
+    assert L.dq_gemm_mx_epilogue(*args, None) == ARG
+
+
+def test_channels_past_the_limit_are_refused(dqlib):
+    L, out = dqlib.lib(), (1 << 28) + 32
+    assert L.dq_gemm_mx_epilogue(*_apart(EPI, out=out).values(), None) == ARG
+    assert L.dq_gated_mx(*_apart(GATED, inner=out).values(), None) == ARG
+    assert L.dq_gated_mx_quantized(*_apart(GATEDQ, inner=out).values(), None) == ARG
+
+
 def test_binding_refuses_without_a_gpu(dqlib):
     import torch
 
