@@ -35,6 +35,9 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+// 4 channels of an output or residual, which are aligned to their element only
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef bf16x4 bf16x4_any __attribute__((aligned(2)));
 
 constexpr int kStage = 256;           // k values per packed stage
 constexpr int kPackStepB = 1024;      // packed codes of (row block, stage, step)
@@ -43,6 +46,8 @@ constexpr int kPackScaleB = 256;      // packed scales of (row block, stage)
 constexpr uint32_t kBufRsrcWord3 = 0x00020000u;  // raw buffer, 32-bit data format
 constexpr uint32_t kOob = 0x80000000u;           // an offset past every buffer: reads zero
 constexpr int kNt = 2;  // cache policy of buffer stores: nontemporal (written once, not read here)
+
+constexpr int64_t kMaxOut = 1 << 22;  // 127 rows of fp32 outputs span less than 2^31 bytes
 
 enum Out : int { kOutF32 = 0, kOutBf16 = 1, kOutFp4 = 2, kOutFp8 = 3 };
 
@@ -59,7 +64,6 @@ struct MlpArgs {
   uint8_t* codes;        // quantized
   uint8_t* scales;
   int tokens, out, K, act;
-  bool vec;              // whole 4-channel accesses: out % 4 == 0 and aligned arrays
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
@@ -128,42 +132,25 @@ __device__ __forceinline__ f32x4 combine(int act, const f32x4& a0, const f32x4& 
   return y;
 }
 
-// Store channels ich .. ich + 3 of token t, after adding the residual. VEC: whole 4-channel
-// accesses (then ich < out means that all four exist).
-template <int OUT, bool VEC>
+// Store channels ich .. ich + 3 of token t, those that exist, after adding the residual.
+template <int OUT>
 __device__ __forceinline__ void store_row(const MlpArgs& p, int64_t t, int ich, f32x4 y) {
-  if (VEC && ich >= p.out) return;
   const int64_t off = t * p.out + ich;
-  if (OUT == kOutBf16) {
-    __bf16* yp = static_cast<__bf16*>(p.y) + off;
-    const __bf16* rp = static_cast<const __bf16*>(p.res) + off;
-    if (VEC) {
-      if (p.res) {
-        const bf16x4 r = *reinterpret_cast<const bf16x4*>(rp);
+  typedef typename std::conditional<OUT == kOutF32, float, __bf16>::type T;
+  typedef typename std::conditional<OUT == kOutF32, f32x4_any, bf16x4_any>::type T4;
+  T* yp = static_cast<T*>(p.y) + off;
+  const T* rp = static_cast<const T*>(p.res) + off;
+  if (ich + 3 < p.out) {
+    if (p.res) {
+      const T4 r = *reinterpret_cast<const T4*>(rp);
 #pragma unroll
-        for (int e = 0; e < 4; e++) y[e] = (float)r[e] + y[e];
-      }
-      *reinterpret_cast<bf16x4*>(yp) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; e++)
-        if (ich + e < p.out) yp[e] = (__bf16)(p.res ? (float)rp[e] + y[e] : y[e]);
+      for (int e = 0; e < 4; e++) y[e] = (float)r[e] + y[e];
     }
+    *reinterpret_cast<T4*>(yp) = T4{(T)y[0], (T)y[1], (T)y[2], (T)y[3]};
   } else {
-    float* yp = static_cast<float*>(p.y) + off;
-    const float* rp = static_cast<const float*>(p.res) + off;
-    if (VEC) {
-      if (p.res) {
-        const f32x4 r = *reinterpret_cast<const f32x4*>(rp);
 #pragma unroll
-        for (int e = 0; e < 4; e++) y[e] = r[e] + y[e];
-      }
-      *reinterpret_cast<f32x4*>(yp) = y;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; e++)
-        if (ich + e < p.out) yp[e] = p.res ? rp[e] + y[e] : y[e];
-    }
+    for (int e = 0; e < 3; e++)
+      if (ich + e < p.out) yp[e] = (T)(p.res ? (float)rp[e] + y[e] : y[e]);
   }
 }
 
@@ -456,8 +443,7 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
                                                   tr * kPartRow + ch);
       const f32x4 y = combine<GATED>(p.act, a0[x], a1[x], cc[x], s[0], s[1]);
       if constexpr (OUT >= kOutFp4) store_quantized<OUT>(p, t, ich, cc[x], y);
-      else if (p.vec) store_row<OUT, true>(p, t, ich, y);
-      else store_row<OUT, false>(p, t, ich, y);
+      else store_row<OUT>(p, t, ich, y);
     }
   }
 }
@@ -581,9 +567,10 @@ __device__ __forceinline__ void tile_step(v16f (&acc)[2][NB], u32x4 (&fa)[2][ste
 //   bf16 and fp32 outputs go through LDS, so that the stores cover whole rows of the wave's
 //     channels instead of 8 or 16 bytes of 32 rows. The single product applies its factors
 //     there, where a lane has the same 4 channels in every row, and loads its residual one
-//     chunk ahead.
-// FULL: the tile lies inside the tokens and channels and takes 4-channel accesses (and its rows'
-// offsets stay below 2^31).
+//     chunk ahead. Where the channels or the arrays do not fit 4-channel accesses they are made
+//     all the same, at addresses aligned to the element only (out 9001, 700 tokens, K 2560: 15.8
+//     us in bf16, 19.9 in fp32; out 9004 15.2 and 19.5; one channel per lane instead 18.2 and
+//     21.6), and the last 1 .. 3 channels element by element.
 template <bool GATED, int OUT>
 __device__ __forceinline__ void quantize_chunk(const MlpArgs& p, f32x4 (&y)[4], int t, int rb,
                                                int h, bool in) {
@@ -629,9 +616,9 @@ __device__ __forceinline__ void quantize_chunk(const MlpArgs& p, f32x4 (&y)[4], 
 template <bool GATED>
 constexpr int kWaveStaging = 2 * 32 * (128 * (GATED ? 1 : 2) + 16);  // LDS bytes of a wave
 
-template <bool GATED, int NB, int OUT, bool FULL>
+template <bool GATED, int NB, int OUT>
 __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2][NB], int rb0,
-                                           int t0, uint8_t* region) {
+                                           int t0, int rows, uint8_t* region) {
   constexpr int ME = GATED ? 1 : 2;       // row blocks of results
   constexpr int LPR = 8 * ME;             // lanes per token row in the read-back
   constexpr int NR = 32 * LPR / 64;       // row accesses of a chunk per lane
@@ -653,25 +640,33 @@ __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2
     as = load_channels(p.a[0], ich, p.out, 1.0f);
     bias = load_channels(p.bias, ich, p.out, 0.0f);
   }
-  // FULL: rows through buffer accesses relative to the wave's first channel of the tile's first
-  // token, the row step in the scalar offset
+  // rows through buffer accesses relative to the wave's first channel of the tile's first token;
+  // rows past the last token lie past the buffer's end, and pieces that the channels do not fill
+  // take an offset past it (offsets below 2^31 by kMaxOut, plus kOob below 2^32): such loads read
+  // zeros, such stores write nothing
   constexpr int kEs = OUT == kOutF32 ? 4 : 2;
   const int pitch = p.out * kEs;
   const int64_t corner = ((int64_t)t0 * p.out + rb0 * 32) * kEs;
-  const uint32_t span = FULL ? (uint32_t)(32 * NB - 1) * (uint32_t)pitch + 32u * ME * kEs : 0u;
+  // (readfirstlane: the compiler takes the clamp for a per-lane value, and each access for a loop
+  // over descriptors)
+  const uint32_t span = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(rows - 1) * (uint32_t)pitch + (uint32_t)min(32 * ME, max(p.out - rb0 * 32, 0)) * kEs);
   const __amdgpu_buffer_rsrc_t ry = rsrc(static_cast<char*>(p.y) + corner, span);
-  const bool has_res = FULL && !GATED && p.res;
+  const bool has_res = !GATED && p.res;
   const __amdgpu_buffer_rsrc_t rr4 = rsrc(static_cast<const char*>(has_res ? p.res : p.y) + corner, span);
-  const uint32_t vrow = (uint32_t)rr * (uint32_t)pitch + (uint32_t)(cl * 4 * kEs);
+  const uint32_t vrow = ich + 3 < p.out ? (uint32_t)rr * (uint32_t)pitch + (uint32_t)(cl * 4 * kEs) : kOob;
+  // whether the channels end in this wave's with a piece of 1 .. 3
+  const bool ragged = (p.out & 3) && p.out > rb0 * 32 && p.out < (rb0 + ME) * 32;
   typedef typename std::conditional<OUT == kOutF32, u32x4, u32x2>::type raw4;
+  typedef typename std::conditional<OUT == kOutF32, float, __bf16>::type T;
   raw4 res[NR];
   auto fetch = [&](int n) {
     if (has_res) {
 #pragma unroll
       for (int r = 0; r < NR; r++) {
-        const uint32_t so = (uint32_t)(n * 32 + r * (64 / LPR)) * (uint32_t)pitch;
-        if constexpr (OUT == kOutF32) res[r] = __builtin_amdgcn_raw_buffer_load_b128(rr4, vrow, so, 0);
-        else res[r] = __builtin_amdgcn_raw_buffer_load_b64(rr4, vrow, so, 0);
+        const uint32_t vo = vrow + (uint32_t)(n * 32 + r * (64 / LPR)) * (uint32_t)pitch;
+        if constexpr (OUT == kOutF32) res[r] = __builtin_amdgcn_raw_buffer_load_b128(rr4, vo, 0, 0);
+        else res[r] = __builtin_amdgcn_raw_buffer_load_b64(rr4, vo, 0, 0);
       }
     }
   };
@@ -701,7 +696,7 @@ __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2
 #pragma unroll
       for (int g = 0; g < 4; g++) y[0][g] *= cb[g];
       const int t = t0 + n * 32 + rl;
-      quantize_chunk<GATED, OUT>(p, y[0], t, rb0, h, FULL || (t < p.tokens && rb0 * 32 < p.out));
+      quantize_chunk<GATED, OUT>(p, y[0], t, rb0, h, t < p.tokens && rb0 * 32 < p.out);
     } else {
       uint8_t* reg = region + (n & 1) * (32 * kRow);  // two chunks, taken in turn
 #pragma unroll
@@ -710,53 +705,51 @@ __device__ __forceinline__ void tile_store(const MlpArgs& p, const v16f (&acc)[2
         for (int g = 0; g < 4; g++)
           *reinterpret_cast<f32x4*>(reg + rl * kRow + (m * 32 + g * 8 + h * 4) * 4) = y[m][g];
       wave_lds_order();
-      if (FULL) {
-        f32x4 v[NR];
-#pragma unroll
-        for (int r = 0; r < NR; r++)
-          v[r] = *reinterpret_cast<const f32x4*>(reg + (r * (64 / LPR) + rr) * kRow + cl * 16);
-        if (!GATED)
-          with_activation(p.act, [&](auto k) {
-#pragma unroll
-            for (int r = 0; r < NR; r++)
-#pragma unroll
-              for (int e = 0; e < 4; e++)
-                v[r][e] = activation<decltype(k)::value>(v[r][e] * as[e] + bias[e]);
-          });
-        if (has_res) {
-#pragma unroll
-          for (int r = 0; r < NR; r++) {
-            if constexpr (OUT == kOutF32) {
-              v[r] = __builtin_bit_cast(f32x4, res[r]) + v[r];
-            } else {
-              const bf16x4 x = __builtin_bit_cast(bf16x4, res[r]);
-#pragma unroll
-              for (int e = 0; e < 4; e++) v[r][e] = (float)x[e] + v[r][e];
-            }
+      if (ragged && rl < rows - n * 32) {  // a row per lane of each half, channel by channel
+        for (int ch = (p.out & ~3) + h; ch < p.out; ch += 2) {
+          float v = *reinterpret_cast<const float*>(reg + rl * kRow + (ch - rb0 * 32) * 4);
+          if (!GATED) {
+            v = v * (p.a[0] ? p.a[0][ch] : 1.0f) + (p.bias ? p.bias[ch] : 0.0f);
+            with_activation(p.act, [&](auto k) { v = activation<decltype(k)::value>(v); });
           }
-          if (n + 1 < NB) fetch(n + 1);
+          const int64_t off = (int64_t)(t0 + n * 32 + rl) * p.out + ch;
+          if (p.res) v = (float)static_cast<const T*>(p.res)[off] + v;
+          static_cast<T*>(p.y)[off] = (T)v;
         }
+      }
+      f32x4 v[NR];
+#pragma unroll
+      for (int r = 0; r < NR; r++)
+        v[r] = *reinterpret_cast<const f32x4*>(reg + (r * (64 / LPR) + rr) * kRow + cl * 16);
+      if (!GATED)
+        with_activation(p.act, [&](auto k) {
+#pragma unroll
+          for (int r = 0; r < NR; r++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              v[r][e] = activation<decltype(k)::value>(v[r][e] * as[e] + bias[e]);
+        });
+      if (has_res) {
 #pragma unroll
         for (int r = 0; r < NR; r++) {
-          const uint32_t so = (uint32_t)(n * 32 + r * (64 / LPR)) * (uint32_t)pitch;
           if constexpr (OUT == kOutF32) {
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v[r]), ry, vrow, so, kNt);
+            v[r] = __builtin_bit_cast(f32x4, res[r]) + v[r];
           } else {
-            const bf16x4 o = {(__bf16)v[r][0], (__bf16)v[r][1], (__bf16)v[r][2], (__bf16)v[r][3]};
-            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), ry, vrow, so, kNt);
+            const bf16x4 x = __builtin_bit_cast(bf16x4, res[r]);
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[r][e] = (float)x[e] + v[r][e];
           }
         }
-      } else {
-#pragma unroll 1
-        for (int r = 0; r < NR; r++) {
-          const int row = r * (64 / LPR) + rr;
-          f32x4 v = *reinterpret_cast<const f32x4*>(reg + row * kRow + cl * 16);
-          if (!GATED) v = combine<false>(p.act, as, as, bias, v, v);
-          const int t = t0 + n * 32 + row;
-          if (t < p.tokens) {
-            if (p.vec) store_row<OUT, true>(p, t, ich, v);
-            else store_row<OUT, false>(p, t, ich, v);
-          }
+        if (n + 1 < NB) fetch(n + 1);
+      }
+#pragma unroll
+      for (int r = 0; r < NR; r++) {
+        const uint32_t vo = vrow + (uint32_t)(n * 32 + r * (64 / LPR)) * (uint32_t)pitch;
+        if constexpr (OUT == kOutF32) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v[r]), ry, vo, 0, kNt);
+        } else {
+          const bf16x4 o = {(__bf16)v[r][0], (__bf16)v[r][1], (__bf16)v[r][2], (__bf16)v[r][3]};
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), ry, vo, 0, kNt);
         }
       }
       wave_lds_order();
@@ -909,11 +902,7 @@ __global__ __launch_bounds__(256, 2) void k_mlp_tile(MlpArgs p, int nti, int ntt
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
   __syncthreads();  // every wave is done with the main loop's LDS
   uint8_t* region = lds + (OUT >= kOutFp4 ? 0 : wave * kWaveStaging<GATED>);
-  if (rows == 32 * NB && (rb0 + (GATED ? 1 : 2)) * 32 <= p.out &&
-      (OUT >= kOutFp4 || (p.vec && p.out <= (1 << 21))))
-    tile_store<GATED, NB, OUT, true>(p, acc, rb0, t0, region);
-  else
-    tile_store<GATED, NB, OUT, false>(p, acc, rb0, t0, region);
+  tile_store<GATED, NB, OUT>(p, acc, rb0, t0, rows, region);
 }
 
 // ---------------------------------------------------------------------------------- host
@@ -1009,7 +998,7 @@ dq_status check_product(const void* xc, const void* xs, dq_format act_fmt, int64
   if ((int)act < 0 || (int)act > DQ_ACTIVATION_GELU_TANH) return DQ_ERR_UNSUPPORTED;
   if (!xc || !xs || !wc || !ws) return DQ_ERR_ARG;
   if (tokens < 1 || out < 1 || K < 512 || K % 512 != 0 || K > (1 << 22)) return DQ_ERR_ARG;
-  if (tokens > INT32_MAX - 256 || out > (1 << 28)) return DQ_ERR_ARG;
+  if (tokens > INT32_MAX - 256 || out > kMaxOut) return DQ_ERR_ARG;
   if (((uintptr_t)xc | (uintptr_t)xs | (uintptr_t)wc | (uintptr_t)a) & 15u) return DQ_ERR_ARG;
   if ((uintptr_t)ws & 3u) return DQ_ERR_ARG;
   return DQ_OK;
@@ -1064,7 +1053,6 @@ dq_status dq_gemm_mx_epilogue(const uint8_t* act_codes, const uint8_t* act_scale
   p.out = (int)out;
   p.K = (int)K;
   p.act = activation;
-  p.vec = out % 4 == 0 && (((uintptr_t)Y | (uintptr_t)residual) & (4 * esz - 1)) == 0;
   const bool act8 = act_fmt == DQ_FMT_MXFP8;
   const hipError_t e = yt == DQ_BF16 ? launch_o<false, kOutBf16>(p, act8, stream)
                                      : launch_o<false, kOutF32>(p, false, stream);
@@ -1112,7 +1100,6 @@ dq_status dq_gated_mx(const uint8_t* act_codes, const uint8_t* act_scales, dq_fo
   p.out = (int)inner;
   p.K = (int)K;
   p.act = activation;
-  p.vec = inner % 4 == 0 && ((uintptr_t)H & (4 * esz - 1)) == 0;
   const bool act8 = act_fmt == DQ_FMT_MXFP8;
   const hipError_t e = yt == DQ_BF16 ? launch_o<true, kOutBf16>(p, act8, stream)
                                      : launch_o<true, kOutF32>(p, false, stream);

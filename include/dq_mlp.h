@@ -90,7 +90,7 @@ dq_status dq_norm_quantize_act(const void* X, dq_dtype xt, const void* residual,
  *  Y:            out, tokens x out, fp32 or bf16 (yt), aligned to its element; likewise residual.
  * MXFP8 activations give bf16 only: in its 8-bit mode the matrix instruction aligns the products
  * of 16 neighbouring k to about 14 bits below the largest, which bf16 does not show and fp32
- * would. An E8M0 byte 0xFF makes the outputs it reaches NaN. tokens < 2^31 - 256, out <= 2^28.
+ * would. An E8M0 byte 0xFF makes the outputs it reaches NaN. tokens < 2^31 - 256, out <= 2^22.
  * Only enqueues. */
 dq_status dq_gemm_mx_epilogue(const uint8_t* act_codes, const uint8_t* act_scales,
                               dq_format act_fmt, int64_t tokens, int64_t K,

@@ -173,7 +173,7 @@ def test_in_place_residuals_overlap_exactly_or_not_at_all(dqlib):
 
 
 def test_channels_past_the_limit_are_refused(dqlib):
-    L, out = dqlib.lib(), (1 << 28) + 32
+    L, out = dqlib.lib(), (1 << 22) + 32
     assert L.dq_gemm_mx_epilogue(*_apart(EPI, out=out).values(), None) == ARG
     assert L.dq_gated_mx(*_apart(GATED, inner=out).values(), None) == ARG
     assert L.dq_gated_mx_quantized(*_apart(GATEDQ, inner=out).values(), None) == ARG
