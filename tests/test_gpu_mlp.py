@@ -307,6 +307,34 @@ def test_epilogue_unaligned_output(dq, tokens):
         assert float(big[0]) == 7.0 and torch.all(big[1 + tokens * out:] == 7.0)
 
 
+@pytest.mark.parametrize("tokens,out", [(300, 4097), (300, 4100), (1100, 4099), (1100, 4098)])
+def test_epilogue_unaligned_tiles(dq, tokens, out):
+    # the tile kernels on rows that start at any element, updated in place inside a larger array
+    # whose other values stay; rows behind the last token and a ragged end of the channels
+    import torch
+
+    K = 512
+    xc, xs = _acts(tokens, K, "mxfp4", 13)
+    wc, ws, a = _weights(out, K, 14)
+    pk = _pack(dq, wc, ws)
+    rng = np.random.default_rng(15)
+    ts, cs = _sampled(rng, tokens, 300), _sampled(rng, out, 300)
+    for dtype, dt in (("bf16", torch.bfloat16), ("f32", torch.float32)):
+        for lead in (1, 2, 3):
+            print(f"[epilogue] tokens={tokens} out={out} {dtype} lead={lead}", flush=True)
+            rh, rd = _residual(rng, tokens, out, dtype)
+            behind = 40 * out
+            big = torch.full((lead + tokens * out + behind,), 7.0, dtype=dt, device="cuda")
+            y = big[lead:lead + tokens * out].view(tokens, out)
+            y.copy_(rd)
+            dq.gemm_mx_epilogue(_dev(xc), _dev(xs), pk, a=_dev(a), activation="relu", residual=y,
+                                out_dtype=dtype, y=y)
+            want, dy = ref.epilogue(xc[ts], xs[ts], "mxfp4", wc[cs], ws[cs], a[cs], None, "relu",
+                                    rh[np.ix_(ts, cs)])
+            ref.check_rounded(_f64(y)[np.ix_(ts, cs)], want, dy, dtype)
+            assert torch.all(big[:lead] == 7.0) and torch.all(big[lead + tokens * out:] == 7.0)
+
+
 def test_epilogue_channels_past_two_million(dq):
     # whole tiles whose rows lie further apart than a 31-bit tile offset allows: 4096 weight rows
     # repeated, so that every block of 4096 channels must equal the first, in place on a residual
@@ -389,6 +417,12 @@ def test_gated_activations(dq, kind, dtype):
 @pytest.mark.parametrize("act_fmt,dtype", [("mxfp4", "bf16"), ("mxfp4", "f32"), ("mxfp8", "bf16")])
 def test_gated_odd_channels(dq, tokens, inner, act_fmt, dtype):
     _gated_check(dq, tokens, inner, 512, act_fmt, dtype, seed=31)
+
+
+@pytest.mark.parametrize("tokens,inner", [(300, 3201), (333, 3302), (610, 6467)])
+@pytest.mark.parametrize("act_fmt,dtype", [("mxfp4", "bf16"), ("mxfp4", "f32"), ("mxfp8", "bf16")])
+def test_gated_odd_channels_in_tiles(dq, tokens, inner, act_fmt, dtype):
+    _gated_check(dq, tokens, inner, 512, act_fmt, dtype, seed=33, sample=320)
 
 
 @pytest.mark.parametrize("tokens", [1, 40, 300])
@@ -599,6 +633,25 @@ def test_rows_behind_the_last_token_stay(dq):
     scales = torch.full((64, out // 32), 9, device="cuda", dtype=torch.uint8)
     dq.gated_mx_quantized(_dev(xc)[:tokens], _dev(xs)[:tokens], pk, pk, "mxfp8",
                           codes=codes[:tokens], scales=scales[:tokens])
+    assert torch.all(codes[tokens:] == 9) and torch.all(scales[tokens:] == 9)
+
+
+def test_rows_behind_the_last_token_stay_in_tiles(dq):
+    import torch
+
+    tokens, K, out = 205, 512, 5600
+    xc, xs = _acts(320, K, "mxfp4", 93)
+    pk = _pack(dq, *_weights(out, K, 94)[:2])
+    x, s = _dev(xc)[:tokens], _dev(xs)[:tokens]
+    for dt, name in ((torch.bfloat16, "bf16"), (torch.float32, "f32")):
+        for f in (lambda y: dq.gemm_mx_epilogue(x, s, pk, y=y, out_dtype=name),
+                  lambda y: dq.gated_mx(x, s, pk, pk, y=y, out_dtype=name)):
+            y = torch.full((320, out), 5.0, device="cuda", dtype=dt)
+            f(y[:tokens])
+            assert torch.all(y[tokens:] == 5.0) and not torch.all(y[tokens - 1] == 5.0)
+    codes = torch.full((320, out), 9, device="cuda", dtype=torch.uint8)
+    scales = torch.full((320, out // 32), 9, device="cuda", dtype=torch.uint8)
+    dq.gated_mx_quantized(x, s, pk, pk, "mxfp8", codes=codes[:tokens], scales=scales[:tokens])
     assert torch.all(codes[tokens:] == 9) and torch.all(scales[tokens:] == 9)
 
 
