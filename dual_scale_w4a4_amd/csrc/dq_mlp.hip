@@ -45,7 +45,9 @@ constexpr int kPackStageB = 4096;     // packed codes of (row block, stage)
 constexpr int kPackScaleB = 256;      // packed scales of (row block, stage)
 constexpr uint32_t kBufRsrcWord3 = 0x00020000u;  // raw buffer, 32-bit data format
 constexpr uint32_t kOob = 0x80000000u;           // an offset past every buffer: reads zero
-constexpr int kNt = 2;  // cache policy of buffer stores: nontemporal (written once, not read here)
+// cache policy of buffer stores: nontemporal, since outputs are written once and not read here (ordinary
+// stores 1% slower: 14336 -> 4096, 2048 tokens 60.1 against 59.4 us)
+constexpr int kNt = 2;
 
 constexpr int64_t kMaxOut = 1 << 22;  // 127 rows of fp32 outputs span less than 2^31 bytes
 
@@ -243,7 +245,9 @@ __device__ __forceinline__ v16f mfma(const u32x4& a, const u32x4* b, v16f c, uin
 // registers, its tokens through a ring of two LDS stages of its own, both loaded two of its
 // stages ahead, and the token scales (16 bytes of a row for a whole period, instead of 4 of
 // every row and stage: 14336 -> 4096 at 256 tokens 20 -> 17 us) through LDS as well. Token
-// fragments are read kAhead blocks before their products.
+// fragments are read kAhead blocks before their products. Bound by the weights' memory traffic:
+// gated 4096 -> 14336 with 32 tokens 12.3 us for 63 MB (5.1 TB/s, a copy's rate), 14336 -> 4096 with
+// one token 8.0 us for 31 MB (3.9 TB/s: about 2 us of it launch, ramp and join).
 
 // LDS row of one token's 32 partial sums, padded so that 8 rows cover distinct banks
 constexpr int kPartRow = 36;
@@ -456,6 +460,12 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p) {
 //
 // Loads run two stages ahead: the fragments of two stages are a ring of registers, each reloaded
 // right after the last product that reads it, and the tokens use a ring of four LDS buffers.
+//
+// Two workgroups fit a CU (one of 256 x 256: gated 4096 -> 14336 with 8192 tokens 470 us against
+// 450). Bound by the matrix cores at the clock that the chip's power allows: that product runs
+// at 4.1 - 4.35 PFLOP/s (443 - 466 us by the box), 62% busy at 1.47 GHz, where a stream of the
+// instruction on random register operands reaches 6.4; 14336 -> 4096 with MXFP8 activations and
+// 2048 tokens at 2.8 (86 us) of 4.1.
 
 constexpr int kGroupM = 4;         // weight tiles per tile group (L2 reuse)
 
