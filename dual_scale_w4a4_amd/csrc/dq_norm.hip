@@ -111,8 +111,8 @@ __device__ __forceinline__ QuantConst quant_const(float g) {
 
 // Codes and scale of one lane's 16 values (the group of G values lies in G / 16 neighbouring
 // lanes) at element offset off of the outputs. `act`: whether the lane's channels exist (the
-// group's lanes agree; all lanes of the wave take part in the maxima). Returns whether the group
-// holds a NaN or an infinity; it is then written as a group of zeros.
+// group's lanes agree; all lanes of the wave take part in the maxima). Returns whether a group
+// that exists holds a NaN or an infinity; it is then written as a group of zeros.
 template <int FMT, int G>
 __device__ __forceinline__ bool quantize16(float (&x)[kNormEpl], bool act, const NormArgs& p,
                                            int64_t off, const QuantConst& q) {
@@ -173,7 +173,7 @@ __device__ __forceinline__ bool quantize16(float (&x)[kNormEpl], bool act, const
     else
       static_cast<uint8_t*>(p.scales)[si] = (uint8_t)scode;
   }
-  return bad;
+  return bad && act;
 }
 
 // h = X + R of 16 channels, rounded to the stream's type
@@ -232,20 +232,23 @@ constexpr int kNormThreads = 1024;  // k_norm: rows of up to kNormThreads * kNor
 template <int FMT, int G, bool BF>
 __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs p) {
   __shared__ double red[2][kNormThreads / kWave];
+  // Lanes past the row's end hold zeros: they load nothing, since where h replaces X or R another
+  // wave may have stored already what they would read, and they store and report nothing.
   const int64_t c = threadIdx.x * kNormEpl;
   const bool act = c < p.n;
-  const int64_t lc = act ? c : 0;  // lanes past the row's end read its start and store nothing
   const int waves = blockDim.x / kWave;
   const QuantConst q = quant_const(p.g);
   float w[kNormEpl], b[kNormEpl];
-  Raw16<BF> xr, rr;
+  Raw16<BF> xr = {}, rr = {};
   int64_t row = blockIdx.x;
-  xr.load(p.X, row * p.n + lc);
-  if (p.R) rr.load(p.R, row * p.n + lc);
-  load_factors(p, lc, w, b);
+  if (act) {
+    xr.load(p.X, row * p.n + c);
+    if (p.R) rr.load(p.R, row * p.n + c);
+  }
+  load_factors(p, act ? c : 0, w, b);
   int flags = 0;
   for (int par = 0; row < p.m; row += gridDim.x, par ^= 1) {
-    const int64_t off = row * p.n + lc;
+    const int64_t off = row * p.n + c;
     float h[kNormEpl];
     xr.unpack(h);
     if (p.R) {
@@ -254,7 +257,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs p) {
       add_residual<BF>(h, r);
       if (act) store16<BF>(p.h, off, h);
     }
-    double sum = act ? sum_squares(h) : 0.0;
+    double sum = sum_squares(h);
     if (!(sum <= DBL_MAX)) {  // rare
       float v[kNormEpl];
       xr.unpack(v);
@@ -266,9 +269,9 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs p) {
       flags |= in ? kStNonFinite : kStRange;
     }
     const int64_t next = row + gridDim.x;
-    if (next < p.m) {
-      xr.load(p.X, next * p.n + lc);
-      if (p.R) rr.load(p.R, next * p.n + lc);
+    if (act && next < p.m) {
+      xr.load(p.X, next * p.n + c);
+      if (p.R) rr.load(p.R, next * p.n + c);
     }
     sum = block_sum(sum, red[par], waves);
     const float rstd = (float)(1.0 / sqrt(sum / (double)p.n + p.eps));
