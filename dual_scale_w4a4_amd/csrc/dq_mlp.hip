@@ -79,11 +79,34 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }
 
+// (1 + erf(z / sqrt 2)) / 2 to a few fp32 roundings of itself on both sides of zero: a sum of 1 and
+// erf cancels for negative z (up to 1% off at z = -4.5, zero or one step below -5.6), and a
+// group of negative channels is quantized by its own largest. For w = |z| the smaller half is
+// exp(-w^2 / 2) times exp(w^2 / 2) erfc(w / sqrt 2) / 2, which is smooth and between 1/2 and 0: a
+// polynomial in 1 / (1 + 0.23 w), fitted to the least largest relative error over w <= 14 (3.2e-8;
+// beyond, the exponential is zero). The exponent's roundings leave 0.75 w^2 2^-23. No branches:
+// 14336 -> 4096 with 2048 tokens 61 us, where the sum with erff took 66 and erfcf 69 (no activation
+// 59); gated 4096 -> 14336 118, 118 and 135 (112).
+__device__ __forceinline__ float normal_below(float z) {
+  const float w = fabsf(z), t = __builtin_amdgcn_rcpf(fmaf(w, 0.23f, 1.0f));
+  float g = -0.0790351118f;
+  g = fmaf(g, t, 0.293058358f);
+  g = fmaf(g, t, -0.283361436f);
+  g = fmaf(g, t, 0.307211192f);
+  g = fmaf(g, t, -0.0367220469f);
+  g = fmaf(g, t, 0.121069719f);
+  g = fmaf(g, t, 0.0853795898f);
+  g = fmaf(g, t, 0.0924304118f);
+  g = fmaf(g, t, -3.07274420e-05f);
+  const float q = g * __builtin_amdgcn_exp2f(w * w * -0.721347520f);
+  return z < 0.0f ? q : 1.0f - q;
+}
+
 template <int ACT>
 __device__ __forceinline__ float activation(float z) {
   if (ACT == DQ_ACTIVATION_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
   if (ACT == DQ_ACTIVATION_SILU) return z * sigmoid(z);
-  if (ACT == DQ_ACTIVATION_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if (ACT == DQ_ACTIVATION_GELU) return z * normal_below(z);
   if (ACT == DQ_ACTIVATION_GELU_TANH)  // (1 + tanh u) / 2 = sigmoid(2 u)
     return z * sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
   return z;
