@@ -380,11 +380,12 @@ static hipError_t launch_norm(int fmt, int G, bool bf16, const NormArgs& whole, 
   return hipSuccess;
 }
 
-// The host-side checks of both forms, and the kernel's arguments but for the status word.
+// The host-side checks of both forms, and the kernel's arguments. `word`: the status word, or the
+// workspace that holds it (null: neither is the caller's); it is an output like the others.
 static dq_status norm_args(const void* X, dq_dtype xt, const void* residual, void* residual_out,
                            int64_t tokens, int64_t cols, const void* weight, dq_dtype wt,
                            double eps, const float* b, dq_format fmt, int group, float g,
-                           uint8_t* codes, void* inner_scales, NormArgs* p) {
+                           uint8_t* codes, void* inner_scales, const Span& word, NormArgs* p) {
   if ((int)fmt < 0 || (int)fmt > kMxFp8 || (xt != DQ_F32 && xt != DQ_BF16)) return DQ_ERR_UNSUPPORTED;
   if (weight && wt != DQ_F32 && wt != DQ_BF16) return DQ_ERR_UNSUPPORTED;
   if (!X || !codes || !inner_scales) return DQ_ERR_ARG;
@@ -403,7 +404,8 @@ static dq_status norm_args(const void* X, dq_dtype xt, const void* residual, voi
   const size_t n = (size_t)tokens * (size_t)cols, vb = (size_t)cols * 4;
   if (any_overlap({{codes, fmt == DQ_FMT_MXFP8 ? n : n / 2},
                    {inner_scales, n / (size_t)group * (fmt == DQ_FMT_INT4_BF16 ? 2 : 1)},
-                   {residual_out, bytes}},
+                   {residual_out, bytes},
+                   word},
                   {{X == residual_out ? nullptr : X, bytes},
                    {residual == residual_out ? nullptr : residual, bytes},
                    {weight, wt == DQ_BF16 ? vb / 2 : vb},
@@ -420,6 +422,7 @@ static dq_status norm_args(const void* X, dq_dtype xt, const void* residual, voi
   p->g = fmt == DQ_FMT_NVFP4 ? g : 1.0f;
   p->codes = codes;
   p->scales = inner_scales;
+  p->status = static_cast<int*>(const_cast<void*>(word.p));
   p->wbf = wt == DQ_BF16;
   return DQ_OK;
 }
@@ -436,10 +439,9 @@ dq_status dq_norm_quantize_act_async(const void* X, dq_dtype xt, const void* res
   using namespace dq;
   NormArgs p{};
   const dq_status st = norm_args(X, xt, residual, residual_out, tokens, cols, weight, wt, eps, b,
-                                 fmt, group, g, codes, inner_scales, &p);
+                                 fmt, group, g, codes, inner_scales, {status, sizeof *status}, &p);
   if (st != DQ_OK) return st;
   if (!status || ((uintptr_t)status & 3u)) return DQ_ERR_ARG;
-  p.status = status;
   return launch_norm(fmt, group, xt == DQ_BF16, p, stream) == hipSuccess ? DQ_OK : DQ_ERR_HIP;
 }
 
@@ -453,7 +455,8 @@ dq_status dq_norm_quantize_act(const void* X, dq_dtype xt, const void* residual,
   if (workspace && workspace_bytes < DQ_NORM_WORKSPACE_BYTES) return DQ_ERR_WORKSPACE;
   NormArgs p{};
   dq_status st = norm_args(X, xt, residual, residual_out, tokens, cols, weight, wt, eps, b, fmt,
-                           group, g, codes, inner_scales, &p);
+                           group, g, codes, inner_scales, {workspace, DQ_NORM_WORKSPACE_BYTES},
+                           &p);
   if (st != DQ_OK) return st;
   if ((uintptr_t)workspace & 255u) return DQ_ERR_ARG;
   void* ws = workspace;

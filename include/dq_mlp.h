@@ -13,9 +13,10 @@
  * The conventions are dq.h's: dense row-major device arrays owned by the caller, host-side
  * argument checks before anything is enqueued, no state between calls, deterministic results
  * (no floating-point atomics; the order of every sum depends on the shape alone). An output
- * overlaps neither an input nor another output (DQ_ERR_ARG) but where a call says so. The calls
- * allocate nothing and use no workspace unless they say so, so they can be captured into a
- * graph. `stream` belongs to the current device, where the arrays are.
+ * (a status word or a workspace too) overlaps neither an input nor another output (DQ_ERR_ARG)
+ * but where a call says so. The calls allocate nothing and use no workspace unless they say so,
+ * so they can be captured into a graph. `stream` belongs to the current device, where the arrays
+ * are.
  */
 #ifndef DQ_MLP_H
 #define DQ_MLP_H

@@ -201,7 +201,8 @@ def _bytes(entry, call):
         x = 4 * 256 * (2 if call["xt"] else 4)
         return dict(X=x, R=x, h=x, w=256 * (2 if call["wt"] else 4), b=1024,
                     codes=4 * (256 if call["fmt"] == 4 else 128),
-                    scales=4 * 8 * (2 if call["fmt"] == 0 else 1))
+                    scales=4 * 8 * (2 if call["fmt"] == 0 else 1),
+                    **({"ws": 256} if "ws" in call else {"status": 4}))
     n = dict(xc=4 * (512 if call["fmt"] == 4 else 256), xs=4 * 16)
     for k in ("wc", "gc", "uc"):
         n[k] = 64 * 256
@@ -218,7 +219,7 @@ def _bytes(entry, call):
 
 OUTPUTS = {"dq_gemm_mx_epilogue": ["y"], "dq_gated_mx": ["y"],
            "dq_gated_mx_quantized": ["codes", "scales"],
-           **{n: ["codes", "scales", "h"] for n in NORMS}}
+           NORMS[0]: ["codes", "scales", "h", "status"], NORMS[1]: ["codes", "scales", "h", "ws"]}
 
 
 @pytest.mark.parametrize("entry,change", [(e, {}) for e in CALLS] + [
@@ -233,12 +234,13 @@ def test_an_output_overlaps_no_other_array(status, entry, change):
         for other in size:
             if other == out:
                 continue
-            # 16-byte steps keep every array's alignment; sizes that are none reach over
-            up = lambda n: -(-n // 16) * 16  # noqa: E731
-            last = up(size[other]) - 16
+            # steps that keep the output's alignment; sizes that are no whole steps reach over
+            step = 256 if out == "ws" else 16
+            up = lambda n: -(-n // step) * step  # noqa: E731
+            last = up(size[other]) - step
             cases = [(call[other] + up(size[other]), ACCEPTED), (call[other] + last, ARG),
                      (call[other] - up(size[out]), ACCEPTED),
-                     (call[other] - up(size[out]) + 16, ARG if size[out] > 16 else None),
+                     (call[other] - up(size[out]) + step, ARG if size[out] > step else None),
                      (call[other], ARG)]
             if (out, other) in (("h", "X"), ("h", "R"), ("y", "res")):
                 cases[-1] = (call[other], ACCEPTED)  # in place
