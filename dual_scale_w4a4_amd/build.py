@@ -3,6 +3,9 @@ binding.
 
     python -m dual_scale_w4a4_amd.build
 
+The library needs hipcc alone. The binding is built against torch's headers; where torch is not
+installed there is nothing for it to bind to, and it is left out.
+
 Flags: IEEE fp32 arithmetic exactly as written (-ffp-contract=off: no fused multiply-add
 unless the source asks for one; subnormals kept), and packed-fp32 instruction selection
 disabled.
@@ -10,6 +13,7 @@ disabled.
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 
@@ -46,6 +50,13 @@ def _run(cmd, verbose):
         raise RuntimeError(f"{os.path.basename(cmd[0])} failed building libdq.so or _bind.so")
 
 
+def cxx() -> str:
+    """The host compiler: CXX, g++, or else the clang++ that hipcc itself runs."""
+    cand = os.environ.get("CXX") or shutil.which("g++")
+    rocm = os.path.dirname(os.path.dirname(shutil.which(hipcc()) or hipcc()))
+    return cand or os.path.join(rocm, "llvm", "bin", "clang++")
+
+
 def bind_cmd(out: str):
     """The compiler call for the Python binding of the MLP operators (host code only, against
     torch's headers and the libdq.so beside it)."""
@@ -57,7 +68,7 @@ def bind_cmd(out: str):
     tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
     inc = [f"-I{p}" for p in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
                               os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"))]
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    return [cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
             "-D__HIP_PLATFORM_AMD__",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
             os.path.join(CSRC, "dq_bind.cpp"), "-o", out, f"-L{tlib}", "-ltorch_python",
@@ -66,7 +77,7 @@ def bind_cmd(out: str):
 
 def build(verbose: bool = False) -> str:
     """Compile every source to an object in parallel (no device code crosses files), then
-    link the shared library and build the Python binding that calls it."""
+    link the shared library and build the Python binding that calls it, if there is a torch."""
     from concurrent.futures import ThreadPoolExecutor
 
     objdir = os.path.join(HERE, "_build")
@@ -82,6 +93,13 @@ def build(verbose: bool = False) -> str:
     _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", LIB_PATH + ".tmp"],
          verbose)
     os.replace(LIB_PATH + ".tmp", LIB_PATH)
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        print("torch is not installed: libdq.so without its Python binding", file=sys.stderr)
+        if os.path.exists(BIND_PATH):  # of an older library
+            os.remove(BIND_PATH)
+        return LIB_PATH
     _run(bind_cmd(BIND_PATH + ".tmp"), verbose)
     os.replace(BIND_PATH + ".tmp", BIND_PATH)
     return LIB_PATH
