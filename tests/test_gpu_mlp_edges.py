@@ -107,3 +107,36 @@ def test_gated_gelu_quantizes_groups_of_negative_gates(dq, fmt, tokens):
     codes, scales = q["codes"].cpu().numpy(), q["scales"].cpu().numpy()
     assert np.all(codes == codes[0]) and np.all(scales == scales[0])
     ref.check_quantized(codes[:1], scales[:1], want[None], dx[None], fmt)
+
+
+@pytest.mark.parametrize("tokens", [1, 60, 300, 700])  # each kernel of the selection
+@pytest.mark.parametrize("act_fmt", ["mxfp4", "mxfp8"])
+def test_products_repeat_themselves_bit_for_bit(dq, tokens, act_fmt):
+    # eager calls among others, on other outputs, and replays of a graph
+    import torch
+
+    K, channels = 2560, 4096
+    print(f"[repeat] tokens={tokens} {act_fmt}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    x = torch.randn(tokens, K, device="cuda", generator=g)
+    q = dq.norm_quantize_act(x, act_fmt, 32)
+    w = dq.quantize_act(torch.randn(channels, K, device="cuda", generator=g), "mxfp4", 32)
+    pk = dq.gemm_pack_weights(w["codes"], w["scales"])
+
+    def run():
+        kw = dict(act_fmt=act_fmt)
+        y = dq.gemm_mx_epilogue(q["codes"], q["scales"], pk, activation="gelu", **kw)
+        m = dq.gated_mx_quantized(q["codes"], q["scales"], pk, pk, "mxfp8", **kw)
+        return y, dq.gated_mx(q["codes"], q["scales"], pk, pk, **kw), m["codes"], m["scales"]
+
+    first = run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    for _ in range(4):
+        graph.replay()
+        again = run()
+        torch.cuda.synchronize()
+        for got in (captured, again):
+            assert all(torch.equal(a, b) for a, b in zip(first, got))
