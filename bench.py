@@ -644,7 +644,8 @@ def bench_gemm(args, dq) -> None:
                      "attainable": attainable, "frac_attainable": tf / attainable,
                      "attainable_note": "the same instruction streamed on register operands "
                                         "alone (dq_bench_fp4_mfma_rate): the chip's clock "
-                                        "drops under full matrix-core load",
+                                        "drops under full matrix-core load; most of its "
+                                        "4-bit codes are zero, so an upper bound",
                      "traffic_unit": "HBM bytes per step",
                      "timing": "back-to-back asynchronous calls between one pair of events"},
         "products": per,

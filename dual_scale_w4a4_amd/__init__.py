@@ -222,7 +222,7 @@ def bench_workspace_bytes(rows: int, cols: int, fmt: str, group: int, shape=None
 
 def bench_fp4_mfma_rate(iters: int = 20000, stream=None) -> float:
     """dq_bench_fp4_mfma_rate: the attainable dense-equivalent TFLOP/s of the scaled FP4 matrix
-    instruction (register operands only)."""
+    instruction (register operands only, mostly zero codes: an upper bound)."""
     out = ctypes.c_double(0.0)
     st = lib().dq_bench_fp4_mfma_rate(int(iters), _stream(stream), ctypes.byref(out))
     if st != 0:

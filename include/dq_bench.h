@@ -90,7 +90,9 @@ dq_status dq_solve_timed(const void* W, dq_dtype wt, int64_t rows, int64_t cols,
  * workgroups per CU, `iters` rounds of eight instructions per wave (1 .. 2^20), timed with HIP
  * events on `stream` after one untimed launch. *tflops receives the dense-equivalent TFLOP/s
  * (2 * 32 * 32 * 64 flops per instruction): what the chip sustains at the clock it holds under
- * such load, beside the published peak. Blocks until the timed launch ends. Returns DQ_ERR_ARG
+ * such load, beside the published peak. The operands are small numbers, most of whose 4-bit codes
+ * are zero, which costs less power than full ones: an upper bound (8.6 - 8.9 PFLOP/s, where
+ * random codes hold 6.3 - 6.4 and zeros 9.9). Blocks until the timed launch ends. Returns DQ_ERR_ARG
  * for iters out of range or a null tflops, DQ_ERR_HIP if a HIP call fails. */
 dq_status dq_bench_fp4_mfma_rate(int iters, hipStream_t stream, double* tflops);
 
