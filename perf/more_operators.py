@@ -33,41 +33,41 @@ def listed():
     H, I = 4096, 14336
     return [
         # between the attention and the MLP of one decoding sequence: latency
-        dict(name="norm, one token", op="norm", tokens=1, cols=H, dtype="bf16", post=True,
+        dict(name="norm one token", op="norm", tokens=1, cols=H, dtype="bf16", post=True,
              gate=False, token_gate=False, x_out=True),
         # the same for a prompt, with a gate per channel: memory bandwidth
-        dict(name="norm, prompt", op="norm", tokens=8192, cols=H, dtype="bf16", post=True,
+        dict(name="norm prompt", op="norm", tokens=8192, cols=H, dtype="bf16", post=True,
              gate=True, token_gate=False, x_out=True),
         # an fp32 stream, a gate per token, no post norm, a width that is no multiple of a tile
-        dict(name="norm, ragged fp32", op="norm", tokens=1003, cols=8160, dtype="f32", post=False,
+        dict(name="norm ragged fp32", op="norm", tokens=1003, cols=8160, dtype="f32", post=False,
              gate=False, token_gate=True, x_out=False),
         # the router of one decoding sequence: latency
-        dict(name="route, one token", op="route", tokens=1, cols=H, experts=64, top_k=8,
+        dict(name="route one token", op="route", tokens=1, cols=H, experts=64, top_k=8,
              dtype="bf16", score="softmax", bias=False),
         # the router of a prompt, with sigmoid scores and a balancing bias
-        dict(name="route, prompt", op="route", tokens=4096, cols=H, experts=128, top_k=8,
+        dict(name="route prompt", op="route", tokens=4096, cols=H, experts=128, top_k=8,
              dtype="bf16", score="sigmoid", bias=True),
         # a layer of small experts for one decoding sequence: reads 8 experts' weights
-        dict(name="moe, one token", op="moe", tokens=1, K=2048, inner=1024, experts=64, top_k=8,
+        dict(name="moe one token", op="moe", tokens=1, K=2048, inner=1024, experts=64, top_k=8,
              act_fmt="mxfp4", act="silu", residual=True),
         # 24 sequences decoding together: nearly every expert's weights, a few tokens each
-        dict(name="moe, 24 sequences", op="moe", tokens=24, K=H, inner=1536, experts=64, top_k=8,
+        dict(name="moe 24 sequences", op="moe", tokens=24, K=H, inner=1536, experts=64, top_k=8,
              act_fmt="mxfp4", act="silu", residual=True),
         # few large experts, 8-bit activations, an odd number of sequences
-        dict(name="moe, 8-bit, 5 sequences", op="moe", tokens=5, K=H, inner=I, experts=8, top_k=2,
+        dict(name="moe 8-bit 5 sequences", op="moe", tokens=5, K=H, inner=I, experts=8, top_k=2,
              act_fmt="mxfp8", act="silu", residual=False),
         # a chunk of a prompt: about 90 tokens an expert
-        dict(name="moe, chunk of a prompt", op="moe", tokens=700, K=H, inner=1536, experts=32,
+        dict(name="moe chunk of a prompt", op="moe", tokens=700, K=H, inner=1536, experts=32,
              top_k=4, act_fmt="mxfp4", act="gelu_tanh", residual=True),
         # the down projection of 32 sequences decoding together, nearly each with its own adapter
-        dict(name="adapter, 32 sequences", op="adapter", tokens=32, K=I, out=H, rank=16,
+        dict(name="adapter 32 sequences", op="adapter", tokens=32, K=I, out=H, rank=16,
              adapters=40, packed=False, act_fmt="mxfp4", dtype="bf16", bias=False, act="none",
              residual=True),
         # prompts of several requests packed into one batch
-        dict(name="adapter, prompts", op="adapter", tokens=4096, K=H, out=I, rank=64, adapters=6,
+        dict(name="adapter prompts", op="adapter", tokens=4096, K=H, out=I, rank=64, adapters=6,
              packed=True, act_fmt="mxfp4", dtype="bf16", bias=False, act="none", residual=False),
         # odd sizes, bias and activation, fp32 out
-        dict(name="adapter, ragged", op="adapter", tokens=515, K=2560, out=1733, rank=24,
+        dict(name="adapter ragged", op="adapter", tokens=515, K=2560, out=1733, rank=24,
              adapters=5, packed=True, act_fmt="mxfp4", dtype="f32", bias=True, act="gelu_tanh",
              residual=False),
     ]
