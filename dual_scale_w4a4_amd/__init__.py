@@ -531,6 +531,55 @@ def gated_mx_quantized(act_codes, act_scales, gate, up, fmt: str, a_gate=None, a
     return {"codes": codes, "scales": scales}
 
 
+# ------------------------------------------------ operators of other decoder layers
+# (include/dq_layer.h) By the same rules as the MLP operators'.
+
+
+def block_norm_quantize_act(X, fmt: str, group: int, residual=None, residual_out=None,
+                            post_norm: bool = True, post_weight=None, post_eps: float = 1e-5,
+                            gate=None, token_gate=None, residual_scale: float = 1.0, weight=None,
+                            eps: float = 1e-5, x_out=None, b=None, g: float = 0.0, workspace=None,
+                            stream=None) -> Dict[str, object]:
+    """dq_block_norm_quantize_act: from a block's output X to the next block's quantized input.
+    m = X, normed with ``post_weight`` (unless ``post_norm`` is false), times ``gate`` (per
+    channel) and ``token_gate`` (per token); h = residual_scale * residual + m; its norm with
+    ``weight`` (stored in ``x_out`` where given), times ``b``, quantized as norm_quantize_act does.
+    Returns codes, scales, "residual": h in ``residual_out`` (``residual`` itself updates it in
+    place) or a new tensor, and "x": x_out where given."""
+    m = _calls()
+    if stream is None:
+        codes, scales = m.act_outputs(X, fmt, group)
+        if residual_out is None:
+            residual_out = _torch().empty_like(X)
+    else:
+        with _torch().cuda.stream(stream):  # the outputs belong to the stream that writes them
+            codes, scales = m.act_outputs(X, fmt, group)
+            if residual_out is None:
+                residual_out = _torch().empty_like(X)
+    m.block_norm(X, fmt, group, codes, scales, None, post_norm, post_weight, post_eps, gate,
+                 token_gate, residual, residual_scale, residual_out, weight, eps, x_out, b, g,
+                 workspace, stream)
+    out = {"codes": codes, "scales": scales, "residual": residual_out}
+    if x_out is not None:
+        out["x"] = x_out
+    return out
+
+
+def block_norm_quantize_act_async(X, fmt: str, group: int, codes, scales, status, residual=None,
+                                  residual_out=None, post_norm: bool = True, post_weight=None,
+                                  post_eps: float = 1e-5, gate=None, token_gate=None,
+                                  residual_scale: float = 1.0, weight=None, eps: float = 1e-5,
+                                  x_out=None, b=None, g: float = 0.0, stream=None) -> None:
+    """dq_block_norm_quantize_act_async into caller-allocated outputs (codes, scales from
+    act_outputs, ``residual_out``, ``x_out`` where wanted): enqueued on the stream, no wait;
+    device errors are OR-ed into ``status`` (an int32 CUDA tensor the caller clears)."""
+    if status is None:
+        raise ValueError("status must be an int32 tensor on X's device")
+    _calls().block_norm(X, fmt, group, codes, scales, status, post_norm, post_weight, post_eps,
+                        gate, token_gate, residual, residual_scale, residual_out, weight, eps,
+                        x_out, b, g, None, stream)
+
+
 class _BatchItem(ctypes.Structure):
     _fields_ = [("W", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("a0", ctypes.c_void_p), ("b0", ctypes.c_void_p), ("g0", ctypes.c_float),

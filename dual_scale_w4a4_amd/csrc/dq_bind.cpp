@@ -1,5 +1,5 @@
-// dq_bind.cpp -- the Python binding's calls of the MLP operators (include/dq_mlp.h): argument
-// checks, output tensors, the stream, and the call of the C entry point. A single token's
+// dq_bind.cpp -- the Python binding's calls of the MLP operators (include/dq_mlp.h) and of those
+// of other decoder layers (include/dq_layer.h): argument checks, output tensors, the stream, and the call of the C entry point. A single token's
 // operator is a few microseconds on the GPU, less than the same checks took in Python: on one
 // box gemm_mx_epilogue cost the host 10 us a call there and 5 here.
 //
@@ -19,7 +19,7 @@
 #include <optional>
 #include <string>
 
-#include "../../include/dq_mlp.h"
+#include "../../include/dq_layer.h"
 
 namespace {
 
@@ -220,6 +220,84 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t) {
   END_HANDLE_TH_ERRORS
 }
 
+// block_norm(X, fmt, group, codes, scales, status, post_norm, post_weight, post_eps, gate,
+//            token_gate, residual, residual_scale, residual_out, weight, eps, x_out, b, g,
+//            workspace, stream): asynchronous with a status tensor, else blocking
+PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  const at::Tensor& X = tensor(a[0], "X");
+  const Arr arr{device_of(X, "X")};
+  const at::ScalarType xt = X.scalar_type();
+  if ((xt != at::kFloat && xt != at::kBFloat16) || !X.is_contiguous())
+    refuse("X must be a contiguous 2-D float32 or bfloat16 tensor");
+  const QuantShape q(X, a[1], a[2]);
+  const auto cs = q.codes(), ss = q.scales();
+  void* codes = arr.need(a[3], "codes", at::kByte, cs);
+  void* scales = arr.need(a[4], "scales", q.scale_type, ss);
+  const int post_norm = PyObject_IsTrue(a[6]);
+  if (post_norm < 0) throw python_error();
+  at::ScalarType wt = at::kFloat;  // of both weights
+  auto weight = [&](PyObject* o, const char* name, bool first) -> const void* {
+    if (o == Py_None) return nullptr;
+    const at::ScalarType t = tensor(o, name).scalar_type();
+    if (t != at::kFloat && t != at::kBFloat16) refuse("%s must be float32 or bfloat16", name);
+    if (!first && t != wt) refuse("weight and post_weight must have one type");
+    wt = t;
+    return arr.need(o, name, t, {q.cols});
+  };
+  const void* post = weight(a[7], "post_weight", true);
+  if (post && !post_norm) refuse("post_weight without post_norm");
+  const void* w = weight(a[14], "weight", !post);
+  const double post_eps = number(a[8]), eps = number(a[15]);
+  const float* gate = arr.floats(a[9], "gate", q.cols);
+  const float* token_gate = arr.floats(a[10], "token_gate", q.tokens);
+  const void* residual = arr.option(a[11], "residual", xt, X.sizes());
+  const float rs = (float)number(a[12]);
+  void* residual_out = arr.need(a[13], "residual_out", xt, X.sizes());
+  void* x_out = nullptr;
+  at::ScalarType xot = xt;
+  if (a[16] != Py_None) {
+    xot = tensor(a[16], "x_out").scalar_type();
+    if (xot != at::kFloat && xot != at::kBFloat16) refuse("x_out must be float32 or bfloat16");
+    x_out = arr.need(a[16], "x_out", xot, X.sizes());
+  }
+  const float* b = arr.floats(a[17], "b", q.cols);
+  const float g = (float)number(a[18]);
+  auto type = [](at::ScalarType t) { return t == at::kBFloat16 ? DQ_BF16 : DQ_F32; };
+  if (a[5] != Py_None) {
+    const at::Tensor& st = tensor(a[5], "status");
+    if (st.scalar_type() != at::kInt || st.device() != arr.dev || st.numel() < 1)
+      refuse("status must be an int32 tensor on X's device");
+    const Place place(arr.dev, a[20]);
+    check(dq_block_norm_quantize_act_async(
+              X.data_ptr(), type(xt), post_norm, post, post_eps, gate, token_gate, residual, rs,
+              residual_out, q.tokens, q.cols, w, type(wt), eps, x_out, type(xot), b,
+              (dq_format)q.fmt, (int)q.group, g, static_cast<uint8_t*>(codes), scales,
+              static_cast<int*>(st.data_ptr()), place.stream),
+          "dq_block_norm_quantize_act_async");
+  } else {
+    void* ws = nullptr;
+    size_t bytes = 0;
+    if (a[19] != Py_None) {
+      const at::Tensor& t = tensor(a[19], "workspace");
+      if (t.device() != arr.dev) refuse("workspace must lie on X's device");
+      ws = t.data_ptr();
+      bytes = t.nbytes();
+    }
+    const Place place(arr.dev, a[20]);
+    dq_status st;
+    Py_BEGIN_ALLOW_THREADS  // it waits for the stream
+    st = dq_block_norm_quantize_act(
+        X.data_ptr(), type(xt), post_norm, post, post_eps, gate, token_gate, residual, rs,
+        residual_out, q.tokens, q.cols, w, type(wt), eps, x_out, type(xot), b, (dq_format)q.fmt,
+        (int)q.group, g, static_cast<uint8_t*>(codes), scales, ws, bytes, place.stream);
+    Py_END_ALLOW_THREADS
+    check(st, "dq_block_norm_quantize_act");
+  }
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 // ------------------------------------------------------------------------------ products
 
 // Packed weights: {"codes", "scales", "out", "K"}
@@ -410,6 +488,7 @@ PyObject* counted(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef kMethods[] = {DQ_METHOD(bind, 2),      DQ_METHOD(act_outputs, 3),
                           DQ_METHOD(norm, 14),     DQ_METHOD(epilogue, 11),
                           DQ_METHOD(gated, 11),    DQ_METHOD(gated_quantized, 13),
+                          DQ_METHOD(block_norm, 21),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

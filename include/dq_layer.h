@@ -1,0 +1,69 @@
+/*
+ * dq_layer.h -- C ABI of libdq.so's operators for decoder layers beyond the dense MLP of
+ * dq_mlp.h: norms on both sides of a block, a projection that many requests share with a low-rank
+ * adapter of each request beside it, and a layer of experts with its router.
+ *
+ *   dq_block_norm_quantize_act  norm after a block, its gate, the scaled residual, norm before the
+ *                               next block, column scales, quantizer
+ *   dq_gemm_mx_adapters         dq_gemm_mx_epilogue with each token's own low-rank adapter
+ *   dq_moe_route                scores of the experts, the top k of them and their weights
+ *   dq_moe_mx                   gated products, quantizer, down products and weighted sum of every
+ *                               token's experts
+ *
+ * The conventions are dq_mlp.h's: dense row-major device arrays owned by the caller, host-side
+ * argument checks before anything is enqueued, no state between calls, deterministic results (no
+ * floating-point atomics), outputs that overlap nothing but where a call says so (DQ_ERR_ARG), no
+ * allocation. The calls only enqueue (except dq_block_norm_quantize_act) and can be captured into
+ * a graph. A workspace is scratch memory of one call at a time: calls (and replays of graphs) that
+ * share one have to follow each other on the device. `stream` belongs to the current device, where
+ * the arrays are.
+ */
+#ifndef DQ_LAYER_H
+#define DQ_LAYER_H
+
+#include "dq_mlp.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* What lies between a block (attention, MLP, experts) and the next one's quantized product:
+ *     m  = X, or with post_norm fl32(fl32(X r1) post_weight_j), r1 = fl32(1 / sqrt(mean_j X_tj^2
+ *          + post_eps))
+ *     m  = fl32(fl32(m gate_j) token_gate_t)
+ *     h  = fl32(fl32(residual_scale residual) + m), rounded to X's type and stored
+ *     n  = fl32(fl32(h r2) weight_j),  r2 = fl32(1 / sqrt(mean_j h_tj^2 + eps))
+ *     x  = fl32(n b_j)
+ * (sums of squares and roots in fp64) and then the group quantizer of dq_quantize_act on x, bit
+ * for bit.
+ *  X:            the block's output, tokens x cols, fp32 or bf16 (xt), 16-byte aligned.
+ *  post_norm:    0 or 1.  post_weight: cols values of type wt, or NULL for ones; NULL without
+ *                post_norm.  post_eps: > 0, finite (ignored without post_norm).
+ *  gate:         cols floats, or NULL for ones.  token_gate: tokens floats (4-byte aligned), or
+ *                NULL for ones.
+ *  residual:     as X, or NULL for zeros.  residual_scale: finite.
+ *  residual_out: out, h, as X; may equal residual or X (updated in place).
+ *  weight:       cols values of type wt (fp32 or bf16), or NULL for ones.  eps: > 0, finite.
+ *  x_out:        out, n rounded to type xot (fp32 or bf16), tokens x cols, or NULL: what a router
+ *                or an adapter reads.
+ *  b, fmt, group, g, codes, inner_scales, status, workspace: as for dq_norm_quantize_act.
+ * All arrays of cols or tokens x cols values 16-byte aligned. Status bits: 1 a NaN / Inf in X or
+ * residual, 2 a value of h, n (as x_out holds it) or x that is not finite in a row whose X and
+ * residual are. A row with an error has unspecified outputs; other rows are not affected. */
+dq_status dq_block_norm_quantize_act_async(
+    const void* X, dq_dtype xt, int post_norm, const void* post_weight, double post_eps,
+    const float* gate, const float* token_gate, const void* residual, float residual_scale,
+    void* residual_out, int64_t tokens, int64_t cols, const void* weight, dq_dtype wt, double eps,
+    void* x_out, dq_dtype xot, const float* b, dq_format fmt, int group, float g, uint8_t* codes,
+    void* inner_scales, int* status, hipStream_t stream);
+dq_status dq_block_norm_quantize_act(
+    const void* X, dq_dtype xt, int post_norm, const void* post_weight, double post_eps,
+    const float* gate, const float* token_gate, const void* residual, float residual_scale,
+    void* residual_out, int64_t tokens, int64_t cols, const void* weight, dq_dtype wt, double eps,
+    void* x_out, dq_dtype xot, const float* b, dq_format fmt, int group, float g, uint8_t* codes,
+    void* inner_scales, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* DQ_LAYER_H */
