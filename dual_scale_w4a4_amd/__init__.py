@@ -104,6 +104,8 @@ def lib() -> ctypes.CDLL:
         L.dq_gemm_pack_weights.restype = I
         L.dq_gemm_mx_packed.argtypes = [P, P, I64, I64, P, P, P, I64, I, P, P]
         L.dq_gemm_mx_packed.restype = I
+        L.dq_moe_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I, ctypes.POINTER(SZ)]
+        L.dq_moe_workspace_bytes.restype = I
         L.dq_status_str.argtypes = [I]
         L.dq_status_str.restype = ctypes.c_char_p
         _lib = L
@@ -578,6 +580,32 @@ def block_norm_quantize_act_async(X, fmt: str, group: int, codes, scales, status
     _calls().block_norm(X, fmt, group, codes, scales, status, post_norm, post_weight, post_eps,
                         gate, token_gate, residual, residual_scale, residual_out, weight, eps,
                         x_out, b, g, None, stream)
+
+
+def moe_workspace_bytes(tokens: int, K: int, inner: int, out: int, experts: int, top_k: int) -> int:
+    """dq_moe_workspace_bytes: bytes of moe_mx's workspace."""
+    n = ctypes.c_size_t(0)
+    st = lib().dq_moe_workspace_bytes(int(tokens), int(K), int(inner), int(out), int(experts),
+                                      int(top_k), ctypes.byref(n))
+    if st != 0:
+        raise DQError(st, "dq_moe_workspace_bytes")
+    return n.value
+
+
+def moe_mx(act_codes, act_scales, ids, weights, gate, up, down, experts: int, a_gate=None,
+           a_up=None, a_down=None, activation: str = "silu", b_inner=None, residual=None,
+           act_fmt: str = "mxfp4", inner_fmt: str = "mxfp8", out_dtype: str = "bf16", y=None,
+           workspace=None, stream=None):
+    """dq_moe_mx: Y = residual + sum_s weights[t, s] * the gated MLP of expert ids[t, s] (int32 and
+    float32, tokens x top_k, as moe_route returns them). ``gate``, ``up`` and ``down`` come from
+    gemm_pack_weights on the experts' rows one expert after the other, (experts inner) x K and
+    (experts out) x inner; ``a_*`` and ``b_inner`` are laid out likewise. Between the products the
+    values are quantized to ``inner_fmt`` ("mxfp4" or "mxfp8"). Returns Y (tokens x out, bfloat16, or
+    float32 where both formats are "mxfp4"), into ``y`` when given. ``workspace``: a uint8 tensor
+    of moe_workspace_bytes bytes, else it is allocated."""
+    return _calls().moe(act_codes, act_scales, ids, weights, gate, up, down, experts, a_gate, a_up,
+                        a_down, activation, b_inner, residual, act_fmt, inner_fmt, out_dtype, y,
+                        workspace, stream)
 
 
 class _BatchItem(ctypes.Structure):

@@ -15,6 +15,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
+#include <algorithm>
 #include <array>
 #include <optional>
 #include <string>
@@ -463,6 +464,80 @@ PyObject* gated_quantized(PyObject*, PyObject* const* a, Py_ssize_t) {
   END_HANDLE_TH_ERRORS
 }
 
+// A call's workspace: the caller's (uint8, on the device), or one that belongs to its stream
+struct Space {
+  at::Tensor made;
+  void* ptr;
+  size_t bytes;
+
+  Space(PyObject* o, size_t need, const Arr& arr) {
+    if (o == Py_None) {
+      made = make({(int64_t)need}, at::kByte, arr.dev);
+      ptr = made.data_ptr();
+      bytes = need;
+      return;
+    }
+    const at::Tensor& t = tensor(o, "workspace");
+    if (t.device() != arr.dev || !t.is_contiguous())
+      refuse("workspace must be a contiguous tensor on the arguments' device");
+    ptr = t.data_ptr();
+    bytes = t.nbytes();
+  }
+};
+
+// moe(act_codes, act_scales, ids, weights, gate, up, down, experts, a_gate, a_up, a_down,
+//     activation, b_inner, residual, act_fmt, inner_fmt, out_dtype, y, workspace, stream) -> y
+PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  const Packed gate(a[4], "gate"), up(a[5], "up"), down(a[6], "down");
+  const int64_t experts = integer(a[7]);
+  if (experts < 1 || gate.out % experts || down.out % experts)
+    refuse("experts must be positive and divide the rows of the packed weights");
+  const int64_t inner = gate.out / experts, out = down.out / experts;
+  if (up.out != gate.out || up.K != gate.K || down.K != inner)
+    refuse("gate, up and down weights disagree on their channels");
+  if (out % 32) refuse("an expert's rows must be a multiple of 32");
+  const Acts x(a[0], a[1], a[14], gate.K);
+  const Arr& arr = x.arr;
+  const int64_t tokens = x.tokens;
+  const at::Tensor& idt = tensor(a[2], "ids");
+  if (idt.dim() != 2) refuse("ids must be a tokens x top_k tensor");
+  const int64_t top_k = idt.size(1);
+  const std::array<int64_t, 2> chosen{tokens, top_k}, shape{tokens, out};
+  const int* ids = static_cast<const int*>(arr.need(a[2], "ids", at::kInt, chosen));
+  const float* weights = static_cast<const float*>(arr.need(a[3], "weights", at::kFloat, chosen));
+  const uint8_t *gc = gate.code_ptr(arr, "gate codes"), *gs = gate.scale_ptr(arr, "gate scales"),
+                *uc = up.code_ptr(arr, "up codes"), *us = up.scale_ptr(arr, "up scales"),
+                *dc = down.code_ptr(arr, "down codes"), *ds = down.scale_ptr(arr, "down scales");
+  const float *ag = arr.floats(a[8], "a_gate", gate.out), *au = arr.floats(a[9], "a_up", gate.out),
+              *ad = arr.floats(a[10], "a_down", down.out),
+              *b = arr.floats(a[12], "b_inner", gate.out);
+  const int act = choice(a[11], kActs, "activation"), mid = choice(a[15], kFmts, "format");
+  const at::ScalarType type = out_type(a[16]);
+  const void* residual = arr.option(a[13], "residual", type, shape);
+  void* y = arr.option(a[17], "y", type, shape);
+  size_t need = 0;
+  check(dq_moe_workspace_bytes(tokens, gate.K, inner, out, experts, (int)std::min<int64_t>(top_k, INT32_MAX),
+                               &need),
+        "dq_moe_workspace_bytes");
+  const Place place(arr.dev, a[19]);
+  at::Tensor made;
+  if (!y) {
+    made = make(shape, type, arr.dev);
+    y = made.data_ptr();
+  }
+  const Space space(a[18], need, arr);
+  check(dq_moe_mx(x.codes, x.scales, x.fmt, tokens, gate.K, ids, weights, (int)top_k, experts, gc, gs,
+                  ag, uc, us, au, (dq_activation)act, inner, b, (dq_format)mid, dc, ds, ad, residual,
+                  out, type == at::kBFloat16 ? DQ_BF16 : DQ_F32, y, space.ptr, space.bytes,
+                  place.stream),
+        "dq_moe_mx");
+  if (made.defined()) return THPVariable_Wrap(std::move(made));
+  Py_INCREF(a[17]);
+  return a[17];
+  END_HANDLE_TH_ERRORS
+}
+
 // bind(DQError, raw_stream)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t) {
   Py_INCREF(a[0]);
@@ -488,7 +563,7 @@ PyObject* counted(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef kMethods[] = {DQ_METHOD(bind, 2),      DQ_METHOD(act_outputs, 3),
                           DQ_METHOD(norm, 14),     DQ_METHOD(epilogue, 11),
                           DQ_METHOD(gated, 11),    DQ_METHOD(gated_quantized, 13),
-                          DQ_METHOD(block_norm, 21),
+                          DQ_METHOD(block_norm, 21), DQ_METHOD(moe, 20),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -63,6 +63,40 @@ dq_status dq_block_norm_quantize_act(
     void* x_out, dq_dtype xot, const float* b, dq_format fmt, int group, float g, uint8_t* codes,
     void* inner_scales, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* A layer of experts: for each token its top_k experts' gated MLPs, summed with the token's weights:
+ *     H  = act(a_gate_ei * sum_k x^ Qgate_e) * (a_up_ei * sum_k x^ Qup_e),  e = ids[t][s]
+ *     q  = the quantizer's values of fl32(H * b_e) in groups of 32 channels (inner_fmt)
+ *     Y[t][i] = residual[t][i] + sum_s weights[t][s] * (a_down_ei * sum_j q_j Qdown_e)
+ * products as dq_gated_mx_quantized and dq_gemm_mx_epilogue compute them, the sum over s in fp32 in
+ * ascending order, residual last, one rounding to Y's type.
+ *  act_codes, act_scales, act_fmt, K: the activations, as for dq_gated_mx.
+ *  ids:          tokens x top_k experts (4-byte aligned), in any order; a value outside
+ *                0 .. experts - 1 contributes nothing; an expert named twice counts twice.
+ *  weights:      tokens x top_k floats (4-byte aligned).   1 <= top_k <= 32.
+ *  gate, up, down codes and scales: one packed matrix each (dq_gemm_pack_weights), the experts'
+ *                rows one expert after the other: (experts inner) x K, and (experts out) x inner.
+ *                1 <= experts <= 1024; K and inner multiples of 512, out of 32; each at most 2^22.
+ *  a_gate, a_up, a_down: experts x inner (x out) floats, 16-byte aligned, or NULL.
+ *  b_inner:      experts x inner floats > 0, 16-byte aligned, or NULL.
+ *  inner_fmt:    DQ_FMT_MXFP4 or DQ_FMT_MXFP8.
+ *  residual:     tokens x out of Y's type, or NULL; may equal Y.
+ *  Y:            out, tokens x out, fp32 or bf16 (yt), 16-byte aligned; likewise residual. fp32 where
+ *                act_fmt and inner_fmt are MXFP4, for dq_gemm_mx_epilogue's reason.
+ *  workspace:    dq_moe_workspace_bytes, 256-byte aligned.
+ * A token's result can depend in its last bits on the batch it is in (which kernel, and so which
+ * order of the fp32 sums over k, goes by the number of tokens). */
+dq_status dq_moe_workspace_bytes(int64_t tokens, int64_t K, int64_t inner, int64_t out,
+                                 int64_t experts, int top_k, size_t* bytes);
+dq_status dq_moe_mx(const uint8_t* act_codes, const uint8_t* act_scales, dq_format act_fmt,
+                    int64_t tokens, int64_t K, const int32_t* ids, const float* weights, int top_k,
+                    int64_t experts, const uint8_t* gate_codes, const uint8_t* gate_scales,
+                    const float* a_gate, const uint8_t* up_codes, const uint8_t* up_scales,
+                    const float* a_up, dq_activation activation, int64_t inner,
+                    const float* b_inner, dq_format inner_fmt, const uint8_t* down_codes,
+                    const uint8_t* down_scales, const float* a_down, const void* residual,
+                    int64_t out, dq_dtype yt, void* Y, void* workspace, size_t workspace_bytes,
+                    hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

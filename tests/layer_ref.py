@@ -41,3 +41,65 @@ def block_norm(X, R, post, gate, tgate, rs, w, b, dtype, post_norm=True, post_ep
     x = n if b is None else n * b.astype(F32)
     assert m.dtype == h.dtype == n.dtype == x.dtype == F32
     return h, n, x
+
+
+# ---------------------------------------------------------------------------------- experts
+
+
+def _grid(v, e, fmt):
+    """Values of float64 v quantized with the group exponents e (one per value)."""
+    top, bits, emin = (6.0, 1, 0) if fmt == "mxfp4" else (448.0, 3, -6)
+    u = np.clip(v / np.exp2(e), -top, top)
+    b = np.maximum(np.floor(np.log2(np.maximum(np.abs(u), 2.0 ** -100))), emin)
+    step = np.exp2(b - bits)
+    return np.rint(u / step) * step * np.exp2(e)
+
+
+def quantized(x, dx, fmt):
+    """(q, dq): the quantizer's values for rows x, and how far those of any values within dx of
+    x can be from them: rounding is monotone, so for each scale that a group's largest magnitude
+    within reach can give, the ends of each interval are the furthest."""
+    emax = 2 if fmt == "mxfp4" else 8
+    n = x.shape[0]
+    g, d = np.abs(x).reshape(n, -1, 32), dx.reshape(n, -1, 32)
+    at = lambda m: np.repeat(ref.mx_exponent(m.max(2), emax), 32, 1).astype(float)  # noqa: E731
+    q = _grid(x, at(g), fmt)
+    # at most one power of two apart: every test's dx is far below its group's largest value, or
+    # the group is all zeros within reach (then every candidate is zero or below dx)
+    ends = [_grid(v, at(m), fmt) for v in (x - dx, x + dx) for m in (np.maximum(g - d, 0), g + d)]
+    return q, np.max([np.abs(v - q) for v in ends], 0)
+
+
+def moe(xc, xs, act_fmt, ids, weights, gate, up, down, kind, b, mid, residual):
+    """(y, dy) before the rounding to the output type; gate, up, down: (codes, scales, a) with
+    experts as a first axis, b experts x inner or None."""
+    tokens, out = ids.shape[0], down[0].shape[1]
+    y, dy, size = np.zeros((tokens, out)), np.zeros((tokens, out)), np.zeros((tokens, out))
+    for e in range(gate[0].shape[0]):
+        t, s = np.nonzero(ids == e)
+        if not len(t):
+            continue
+        one = lambda w: (w[0][e], w[1][e], None if w[2] is None else w[2][e])  # noqa: E731
+        h, dh = ref.gated(xc[t], xs[t], act_fmt, one(gate), one(up), kind)
+        if b is not None:
+            h, dh = h * b[e], dh * b[e] + np.abs(h * b[e]) * ref.U24
+        q, dq = quantized(h, dh, mid)
+        w = ref.decode(down[0][e], down[1][e], "mxfp4")
+        K = q.shape[1]
+        z, S = q @ w.T, np.abs(q) @ np.abs(w).T
+        dz = (K / 64 + 2) * 2 * ref.U24 * S + dq @ np.abs(w).T
+        if mid == "mxfp8":  # the matrix instruction aligns 16 products to 2^-13 of the largest
+            qa, wa = np.abs(q).reshape(len(q), -1, 16), np.abs(w).reshape(len(w), -1, 16)
+            for k in range(K // 16):
+                dz += 16 * 2.0 ** -13 * (qa[:, None, k] * wa[None, :, k]).max(-1)
+        if down[2] is not None:
+            z, dz = z * down[2][e], dz * np.abs(down[2][e])
+        v = weights[t, s].astype(np.float64)[:, None]
+        np.add.at(y, t, z * v)
+        np.add.at(dy, t, dz * np.abs(v))
+        np.add.at(size, t, np.abs(z * v))
+    dy += size * (ids.shape[1] + 1) * ref.U24
+    if residual is not None:
+        y = y + residual.astype(np.float64)
+        dy += np.abs(y) * ref.U24
+    return y, dy
