@@ -104,6 +104,8 @@ def lib() -> ctypes.CDLL:
         L.dq_gemm_pack_weights.restype = I
         L.dq_gemm_mx_packed.argtypes = [P, P, I64, I64, P, P, P, I64, I, P, P]
         L.dq_gemm_mx_packed.restype = I
+        L.dq_moe_route_workspace_bytes.argtypes = [I64, I64, ctypes.POINTER(SZ)]
+        L.dq_moe_route_workspace_bytes.restype = I
         L.dq_moe_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I, ctypes.POINTER(SZ)]
         L.dq_moe_workspace_bytes.restype = I
         L.dq_status_str.argtypes = [I]
@@ -580,6 +582,26 @@ def block_norm_quantize_act_async(X, fmt: str, group: int, codes, scales, status
     _calls().block_norm(X, fmt, group, codes, scales, status, post_norm, post_weight, post_eps,
                         gate, token_gate, residual, residual_scale, residual_out, weight, eps,
                         x_out, b, g, None, stream)
+
+
+def moe_route_workspace_bytes(tokens: int, experts: int) -> int:
+    """dq_moe_route_workspace_bytes: bytes of moe_route's workspace."""
+    n = ctypes.c_size_t(0)
+    st = lib().dq_moe_route_workspace_bytes(int(tokens), int(experts), ctypes.byref(n))
+    if st != 0:
+        raise DQError(st, "dq_moe_route_workspace_bytes")
+    return n.value
+
+
+def moe_route(X, W, top_k: int, score: str = "softmax", bias=None, renormalize: bool = True,
+              scale: float = 1.0, ids=None, weights=None, workspace=None, stream=None):
+    """dq_moe_route: the ``top_k`` experts of each token (X: tokens x cols, W: experts x cols) by
+    their "softmax" or "sigmoid" score plus ``bias``, largest first and ties to the lower index, and
+    their scores, divided by their sum where ``renormalize``, times ``scale``. Returns (ids, weights),
+    int32 and float32 tokens x top_k (into the given tensors). ``workspace``: a uint8 tensor of
+    moe_route_workspace_bytes bytes, else it is allocated."""
+    return _calls().route(X, W, top_k, score, bias, renormalize, scale, ids, weights, workspace,
+                          stream)
 
 
 def moe_workspace_bytes(tokens: int, K: int, inner: int, out: int, experts: int, top_k: int) -> int:

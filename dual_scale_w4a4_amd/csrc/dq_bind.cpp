@@ -485,6 +485,56 @@ struct Space {
   }
 };
 
+// route(X, W, top_k, score, bias, renormalize, scale, ids, weights, workspace, stream)
+//   -> (ids, weights)
+PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  const at::Tensor &X = tensor(a[0], "X"), &W = tensor(a[1], "W");
+  const Arr arr{device_of(X, "X")};
+  auto type = [](const at::Tensor& t, const char* name) {
+    const at::ScalarType s = t.scalar_type();
+    if ((s != at::kFloat && s != at::kBFloat16) || t.dim() != 2 || !t.is_contiguous())
+      refuse("%s must be a contiguous 2-D float32 or bfloat16 tensor", name);
+    return s == at::kBFloat16 ? DQ_BF16 : DQ_F32;
+  };
+  const dq_dtype xt = type(X, "X"), wt = type(W, "W");
+  const int64_t tokens = X.size(0), cols = X.size(1), experts = W.size(0);
+  const void* w = arr.need(a[1], "W", W.scalar_type(), {experts, cols});
+  const int64_t top_k = integer(a[2]);
+  if (top_k < 1 || top_k > experts || top_k > 32) refuse("top_k is 1 .. 32, at most the experts");
+  constexpr const char* kScores[] = {"softmax", "sigmoid"};
+  const int score = choice(a[3], kScores, "score");
+  const float* bias = arr.floats(a[4], "bias", experts);
+  const int renormalize = PyObject_IsTrue(a[5]);
+  if (renormalize < 0) throw python_error();
+  const float scale = (float)number(a[6]);
+  const std::array<int64_t, 2> shape{tokens, top_k};
+  void *ids = arr.option(a[7], "ids", at::kInt, shape),
+       *weights = arr.option(a[8], "weights", at::kFloat, shape);
+  size_t need = 0;
+  check(dq_moe_route_workspace_bytes(tokens, experts, &need), "dq_moe_route_workspace_bytes");
+  const Place place(arr.dev, a[10]);
+  THPObjectPtr io(a[7]), wo(a[8]);
+  Py_INCREF(a[7]);
+  Py_INCREF(a[8]);
+  auto fill = [&](void*& ptr, THPObjectPtr& o, at::ScalarType t) {
+    if (ptr) return;
+    at::Tensor made = make(shape, t, arr.dev);
+    ptr = made.data_ptr();
+    o = THPVariable_Wrap(std::move(made));
+    if (!o) throw python_error();
+  };
+  fill(ids, io, at::kInt);
+  fill(weights, wo, at::kFloat);
+  const Space space(a[9], need, arr);
+  check(dq_moe_route(X.data_ptr(), xt, tokens, cols, w, wt, experts, bias, (dq_score)score, (int)top_k,
+                     renormalize, scale, static_cast<int32_t*>(ids), static_cast<float*>(weights),
+                     space.ptr, space.bytes, place.stream),
+        "dq_moe_route");
+  return PyTuple_Pack(2, io.get(), wo.get());
+  END_HANDLE_TH_ERRORS
+}
+
 // moe(act_codes, act_scales, ids, weights, gate, up, down, experts, a_gate, a_up, a_down,
 //     activation, b_inner, residual, act_fmt, inner_fmt, out_dtype, y, workspace, stream) -> y
 PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t) {
@@ -564,6 +614,7 @@ PyMethodDef kMethods[] = {DQ_METHOD(bind, 2),      DQ_METHOD(act_outputs, 3),
                           DQ_METHOD(norm, 14),     DQ_METHOD(epilogue, 11),
                           DQ_METHOD(gated, 11),    DQ_METHOD(gated_quantized, 13),
                           DQ_METHOD(block_norm, 21), DQ_METHOD(moe, 20),
+                          DQ_METHOD(route, 11),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

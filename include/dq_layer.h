@@ -63,6 +63,29 @@ dq_status dq_block_norm_quantize_act(
     void* x_out, dq_dtype xot, const float* b, dq_format fmt, int group, float g, uint8_t* codes,
     void* inner_scales, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* How a router turns a logit into a score: the softmax over all experts, or 1 / (1 + exp(-l)). */
+typedef enum { DQ_SCORE_SOFTMAX = 0, DQ_SCORE_SIGMOID = 1 } dq_score;
+
+/* The router of a layer of experts:
+ *     l_te = fl32(sum_k X_tk W_ek)  (the sum in fp64, so that its order does not matter)
+ *     s_te = the score of l_te, in fp64
+ *     ids[t] = the top_k experts with the largest s_te + bias_e (fp64), largest first, ties to the
+ *              lower index
+ *     weights[t] = fl32(scale * s_te) of those, or with renormalize fl32(scale * s_te / their sum)
+ *              (zeros where the sum is zero)
+ *  X:            tokens x cols, fp32 or bf16 (xt).  W: experts x cols, fp32 or bf16 (wt). Both 16-byte
+ *                aligned, cols a multiple of 8, at most 2^22.  1 <= experts <= 1024.
+ *  bias:         experts floats (4-byte aligned), or NULL for zeros.
+ *  top_k:        1 .. min(32, experts).  renormalize: 0 or 1.  scale: finite.
+ *  ids, weights: out, tokens x top_k (4-byte aligned).
+ *  workspace:    dq_moe_route_workspace_bytes, 256-byte aligned.
+ * A NaN s_te + bias_e ranks as -infinity, so ids are always top_k different experts. */
+dq_status dq_moe_route_workspace_bytes(int64_t tokens, int64_t experts, size_t* bytes);
+dq_status dq_moe_route(const void* X, dq_dtype xt, int64_t tokens, int64_t cols, const void* W,
+                       dq_dtype wt, int64_t experts, const float* bias, dq_score score, int top_k,
+                       int renormalize, float scale, int32_t* ids, float* weights, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
 /* A layer of experts: for each token its top_k experts' gated MLPs, summed with the token's weights:
  *     H  = act(a_gate_ei * sum_k x^ Qgate_e) * (a_up_ei * sum_k x^ Qup_e),  e = ids[t][s]
  *     q  = the quantizer's values of fl32(H * b_e) in groups of 32 channels (inner_fmt)

@@ -103,3 +103,29 @@ def moe(xc, xs, act_fmt, ids, weights, gate, up, down, kind, b, mid, residual):
         y = y + residual.astype(np.float64)
         dy += np.abs(y) * ref.U24
     return y, dy
+
+
+# ---------------------------------------------------------------------------------- router
+
+
+def logits(X, W):
+    return (X.astype(np.float64) @ W.astype(np.float64).T).astype(F32)
+
+
+def route(l, top_k, score, bias, renormalize, scale):
+    """(ids, weights float64) of float32 logits by the definition."""
+    l = l.astype(np.float64)
+    with np.errstate(all="ignore"):
+        if score == "softmax":
+            s = np.exp(l - l.max(1, keepdims=True))
+            s = s / s.sum(1, keepdims=True)
+        else:
+            s = 1.0 / (1.0 + np.exp(-l))
+        key = s if bias is None else s + bias.astype(np.float64)
+    key = np.where(np.isnan(key), -np.inf, key)
+    ids = np.argsort(-key, 1, kind="stable")[:, :top_k]
+    w = np.take_along_axis(s, ids, 1)
+    if renormalize:
+        d = w.sum(1, keepdims=True)
+        w = np.where(d == 0, 0.0, w / np.where(d == 0, 1.0, d))
+    return ids.astype(np.int32), w * scale
