@@ -104,6 +104,8 @@ def lib() -> ctypes.CDLL:
         L.dq_gemm_pack_weights.restype = I
         L.dq_gemm_mx_packed.argtypes = [P, P, I64, I64, P, P, P, I64, I, P, P]
         L.dq_gemm_mx_packed.restype = I
+        L.dq_adapter_workspace_bytes.argtypes = [I64, I64, I, ctypes.POINTER(SZ)]
+        L.dq_adapter_workspace_bytes.restype = I
         L.dq_moe_route_workspace_bytes.argtypes = [I64, I64, ctypes.POINTER(SZ)]
         L.dq_moe_route_workspace_bytes.restype = I
         L.dq_moe_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I, ctypes.POINTER(SZ)]
@@ -582,6 +584,27 @@ def block_norm_quantize_act_async(X, fmt: str, group: int, codes, scales, status
     _calls().block_norm(X, fmt, group, codes, scales, status, post_norm, post_weight, post_eps,
                         gate, token_gate, residual, residual_scale, residual_out, weight, eps,
                         x_out, b, g, None, stream)
+
+
+def adapter_workspace_bytes(tokens: int, K: int, rank: int) -> int:
+    """dq_adapter_workspace_bytes: bytes of gemm_mx_adapters' workspace."""
+    n = ctypes.c_size_t(0)
+    st = lib().dq_adapter_workspace_bytes(int(tokens), int(K), int(rank), ctypes.byref(n))
+    if st != 0:
+        raise DQError(st, "dq_adapter_workspace_bytes")
+    return n.value
+
+
+def gemm_mx_adapters(act_codes, act_scales, packed, X, adapter, A, B, scale=None, a=None,
+                     bias=None, activation: str = "none", residual=None, act_fmt: str = "mxfp4",
+                     out_dtype: str = "bf16", y=None, workspace=None, stream=None):
+    """dq_gemm_mx_adapters: gemm_mx_epilogue with each token's low-rank adapter,
+    Y = residual + act((xhat Qhat^T) D_a + bias + scale_r (X A_r^T) B_r^T), r = adapter[t]
+    (int32, -1 for none). ``X``: the activations before the quantizer (tokens x K, bfloat16); ``A``:
+    adapters x rank x K and ``B``: adapters x out x rank, bfloat16. Returns Y as gemm_mx_epilogue
+    does. ``workspace``: a uint8 tensor of adapter_workspace_bytes bytes, else it is allocated."""
+    return _calls().adapters(act_codes, act_scales, packed, X, adapter, A, B, scale, a, bias,
+                             activation, residual, act_fmt, out_dtype, y, workspace, stream)
 
 
 def moe_route_workspace_bytes(tokens: int, experts: int) -> int:

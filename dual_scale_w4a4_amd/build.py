@@ -22,7 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libdq.so")
 BIND_PATH = os.path.join(HERE, "_bind.so")
 SOURCES = ["dq_kernels.hip", "dq_pass.hip", "dq_rowres.hip", "dq_act.hip", "dq_gemm.hip",
-           "dq_norm.hip", "dq_block_norm.hip", "dq_mlp.hip", "dq_moe.hip", "dq_route.hip",
+           "dq_norm.hip", "dq_block_norm.hip", "dq_mlp.hip", "dq_adapter.hip", "dq_moe.hip",
+           "dq_route.hip",
            "dq_api.hip"]
 ARCH = os.environ.get("DQ_OFFLOAD_ARCH", "gfx950")
 

@@ -485,6 +485,49 @@ struct Space {
   }
 };
 
+// adapters(act_codes, act_scales, packed, X, adapter, A, B, scale, a, bias, activation, residual,
+//          act_fmt, out_dtype, y, workspace, stream) -> y
+PyObject* adapters(PyObject*, PyObject* const* a, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  const Packed w(a[2], "packed");
+  const Acts x(a[0], a[1], a[12], w.K);
+  const Arr& arr = x.arr;
+  const at::ScalarType type = out_type(a[13]);
+  const std::array<int64_t, 2> shape{x.tokens, w.out};
+  const uint8_t *wc = w.code_ptr(arr, "packed codes"), *ws = w.scale_ptr(arr, "packed scales");
+  const void* X = arr.need(a[3], "X", at::kBFloat16, {x.tokens, w.K});
+  const int* adapter = static_cast<const int*>(arr.need(a[4], "adapter", at::kInt, {x.tokens}));
+  const at::Tensor& At = tensor(a[5], "A");
+  if (At.dim() != 3) refuse("A must be an adapters x rank x K tensor");
+  const int64_t n = At.size(0), rank = At.size(1);
+  const void* A = arr.need(a[5], "A", at::kBFloat16, {n, rank, w.K});
+  const void* B = arr.need(a[6], "B", at::kBFloat16, {n, w.out, rank});
+  if (rank < 8 || rank > 256 || rank % 8) refuse("the rank is a multiple of 8, 8 .. 256");
+  const float* scale = arr.floats(a[7], "scale", n);
+  const float *av = arr.floats(a[8], "a", w.out), *bias = arr.floats(a[9], "bias", w.out);
+  const int act = choice(a[10], kActs, "activation");
+  const void* residual = arr.option(a[11], "residual", type, shape);
+  void* y = arr.option(a[14], "y", type, shape);
+  size_t need = 0;
+  check(dq_adapter_workspace_bytes(x.tokens, w.K, (int)rank, &need), "dq_adapter_workspace_bytes");
+  const Place place(arr.dev, a[16]);
+  at::Tensor made;
+  if (!y) {
+    made = make(shape, type, arr.dev);
+    y = made.data_ptr();
+  }
+  const Space space(a[15], need, arr);
+  check(dq_gemm_mx_adapters(x.codes, x.scales, x.fmt, x.tokens, w.K, wc, ws, av, bias, X, adapter, n,
+                            (int)rank, A, B, scale, (dq_activation)act, residual, w.out,
+                            type == at::kBFloat16 ? DQ_BF16 : DQ_F32, y, space.ptr, space.bytes,
+                            place.stream),
+        "dq_gemm_mx_adapters");
+  if (made.defined()) return THPVariable_Wrap(std::move(made));
+  Py_INCREF(a[14]);
+  return a[14];
+  END_HANDLE_TH_ERRORS
+}
+
 // route(X, W, top_k, score, bias, renormalize, scale, ids, weights, workspace, stream)
 //   -> (ids, weights)
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t) {
@@ -614,7 +657,7 @@ PyMethodDef kMethods[] = {DQ_METHOD(bind, 2),      DQ_METHOD(act_outputs, 3),
                           DQ_METHOD(norm, 14),     DQ_METHOD(epilogue, 11),
                           DQ_METHOD(gated, 11),    DQ_METHOD(gated_quantized, 13),
                           DQ_METHOD(block_norm, 21), DQ_METHOD(moe, 20),
-                          DQ_METHOD(route, 11),
+                          DQ_METHOD(route, 11),    DQ_METHOD(adapters, 17),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

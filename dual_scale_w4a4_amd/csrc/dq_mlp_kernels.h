@@ -438,7 +438,8 @@ __device__ __forceinline__ v16f adapter_block(const Adapters& x, int t0, int tok
 #pragma unroll
             for (int k = 0; k < NP; k++) {
               part[k][e] = (__bf16)w;
-              w = w - (float)part[k][e];
+              const float rest = w - (float)part[k][e];
+              w = rest == rest ? rest : 0.0f;  // nothing is left of an infinity (a NaN is in part 0)
             }
           }
         }

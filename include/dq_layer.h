@@ -63,6 +63,34 @@ dq_status dq_block_norm_quantize_act(
     void* x_out, dq_dtype xot, const float* b, dq_format fmt, int group, float g, uint8_t* codes,
     void* inner_scales, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* dq_gemm_mx_epilogue with a low-rank adapter of each token beside the shared weights:
+ *     Y[t][i] = residual[t][i] + act(a_i * sum_k x^[t][k] Qhat[i][k] + bias_i
+ *                                    + scale_r * sum_j u[t][j] B_r[i][j])
+ *     u[t][j] = sum_k X[t][k] A_r[j][k],  r = adapter[t]
+ * both sums in fp32 on the matrix cores, of exact products of bf16 values in u; for B u is split
+ * into bf16 values that hold 16 bits of it, or all 24 where Y is fp32.
+ *  X:            the activations before column scales and quantizer, tokens x K, bf16 (A is the
+ *                adapter as trained: no column scale is in it).
+ *  adapter:      tokens values (4-byte aligned); a token with one outside 0 .. adapters - 1 has no
+ *                adapter. Tokens of one adapter need not be neighbours, but blocks of 32 tokens with
+ *                few adapters are faster.
+ *  A:            adapters x rank x K, bf16.  B: adapters x out x rank, bf16.  X, A, B 16-byte
+ *                aligned.  1 <= adapters <= 2^20; rank a multiple of 8, 8 .. 256 (shorter adapters
+ *                padded with zeros).
+ *  scale:        adapters floats (4-byte aligned), or NULL for ones.
+ *  workspace:    dq_adapter_workspace_bytes, 256-byte aligned.
+ * A NaN or an infinity in an adapter reaches its own tokens only. The other arguments as for
+ * dq_gemm_mx_epilogue. */
+dq_status dq_adapter_workspace_bytes(int64_t tokens, int64_t K, int rank, size_t* bytes);
+dq_status dq_gemm_mx_adapters(const uint8_t* act_codes, const uint8_t* act_scales, dq_format act_fmt,
+                              int64_t tokens, int64_t K, const uint8_t* packed_codes,
+                              const uint8_t* packed_scales, const float* a, const float* bias,
+                              const void* X, const int32_t* adapter, int64_t adapters, int rank,
+                              const void* A, const void* B, const float* scale,
+                              dq_activation activation, const void* residual, int64_t out,
+                              dq_dtype yt, void* Y, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
 /* How a router turns a logit into a score: the softmax over all experts, or 1 / (1 + exp(-l)). */
 typedef enum { DQ_SCORE_SOFTMAX = 0, DQ_SCORE_SIGMOID = 1 } dq_score;
 

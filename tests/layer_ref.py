@@ -129,3 +129,33 @@ def route(l, top_k, score, bias, renormalize, scale):
         d = w.sum(1, keepdims=True)
         w = np.where(d == 0, 0.0, w / np.where(d == 0, 1.0, d))
     return ids.astype(np.int32), w * scale
+
+
+# --------------------------------------------------------------------------------- adapters
+
+
+def adapters(xc, xs, act_fmt, wc, ws, a, bias, kind, res, X, adapter, A, B, scale, dtype):
+    """(y, dy) before the rounding to the output type. u is a sum of K exact products in fp32 in
+    some order: K roundings of at most 2^-23 of the magnitudes' sum each. Its split into bf16 values
+    leaves 2^-18 of it (nearest, twice 9 bits) for bf16 outputs and nothing over 2^-24 for fp32; the
+    sum over the rank (three parts at most) rounds like u's."""
+    z, dz = ref.product(xc, xs, act_fmt, wc, ws, a)
+    for r in range(A.shape[0]):
+        t = np.nonzero(adapter == r)[0]
+        if not len(t):
+            continue
+        x, Ar, Br = X[t].astype(np.float64), A[r].astype(np.float64), B[r].astype(np.float64)
+        s = 1.0 if scale is None else float(scale[r])
+        u, S = x @ Ar.T * s, np.abs(x) @ np.abs(Ar).T * abs(s)
+        du = S * (x.shape[1] + 2) * 2.0 ** -23 + np.abs(u) * (2.0 ** -18 if dtype == "bf16" else ref.U24)
+        d, D = u @ Br.T, np.abs(u) @ np.abs(Br).T
+        z[t] += d
+        dz[t] += du @ np.abs(Br).T + D * (3 * Br.shape[1] + 2) * 2.0 ** -23 + np.abs(z[t]) * ref.U24
+    if bias is not None:
+        z = z + bias.astype(np.float64)
+        dz = dz + np.abs(z) * ref.U24
+    y, dy = ref.act(z, kind), ref.act_error(z, dz, kind)
+    if res is not None:
+        y = y + res.astype(np.float64)
+        dy = dy + np.abs(y) * ref.U24
+    return y, dy
