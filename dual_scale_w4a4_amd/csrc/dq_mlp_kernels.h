@@ -272,14 +272,17 @@ __device__ __forceinline__ v16f mfma(const u32x4& a, const u32x4* b, v16f c, uin
 struct Plain {};
 
 // Low-rank adapters beside the product: adds scale_r sum_j u[t][j] B_r[i][j] to a_i s[t][i], r the
-// token's adapter and u its rank values, stored as `slices` partial sums (dq_adapter.hip).
+// token's adapter and u its rank values (dq_adapter.hip): scaled and split into bf16 values that
+// add up to u, or, with few tokens, `slices` partial sums over k.
 struct Adapters {
-  const float* u;        // slices x tokens x rank
-  const int* adapter;    // tokens; none where out of range
-  const uint16_t* B;     // adapters x out x rank, bf16
-  const float* scale;    // adapters, or null
+  const uint16_t* parts;  // or null: the parts as matrix operands, 1 KiB blocks (32 tokens, step of 16
+                          // rank values, part), lane 16 bytes
+  const float* u;         // else slices x tokens x rank
+  const int* adapter;     // tokens; none where out of range
+  const uint16_t* B;      // adapters x out x rank, bf16
+  const float* scale;     // adapters, or null (in the parts already)
   int adapters, rank, slices;
-  int64_t stride;        // from a slice of u to the next
+  int64_t stride;         // from a slice of u to the next
 };
 
 // Weights of one expert per row: row p of the output (a pair of a token and one of its experts) is
@@ -395,62 +398,268 @@ constexpr bool kAdapters = std::is_same<X, Adapters>::value;
 
 __device__ __forceinline__ const float* shifted(const float* p, int64_t by) { return p ? p + by : p; }
 
-// The adapters' part of 32 channels (row block rb) of the 32 tokens from t0 on, laid out as a matrix
-// result (lane: token lane % 32). The tokens' distinct adapters are taken in order of their first
-// token, those numbered first, first + step, ..; each is a product of B's rows with the rank values of
-// all 32 tokens, of which its own tokens keep theirs (so that a NaN or an infinity in one adapter
-// reaches no other's tokens). u is split into two bf16 values (2^-17 of u is lost, nothing next to a
-// bf16 result's rounding), or three where the result is fp32.
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+// u is split into two bf16 values (2^-18 of it is lost, nothing next to a bf16 result's rounding), or
+// three where the result is fp32.
+constexpr int kMaxSlices = 8, kSliceTokens = 32;
+
 template <int OUT>
-__device__ __forceinline__ v16f adapter_block(const Adapters& x, int t0, int tokens, int rb, int out,
-                                              int first, int step) {
-  constexpr int NP = OUT == kOutF32 ? 3 : 2;
-  const int lane = threadIdx.x & 63, rl = lane & 31, h = lane >> 5;
-  const int t = t0 + rl, ch = rb * 32 + rl;
-  int id = t < tokens ? x.adapter[t] : -1;
-  if ((unsigned)id >= (unsigned)x.adapters) id = -1;
-  v16f sum = {};
-  uint32_t left = (uint32_t)__ballot(id >= 0);  // the halves agree
-  for (int q = 0; left; q++) {
-    const int r = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-    left &= ~(uint32_t)__ballot(id == r);
-    if (q % step != first) continue;
-    const float scale = x.scale ? x.scale[r] : 1.0f;
-    v16f d = {};
-    for (int j = 8 * h; j - 8 * h < x.rank; j += 16) {
-      bf16x8 b = {}, part[NP] = {};
-      if (j < x.rank) {
-        if (ch < out)
-          b = *reinterpret_cast<const bf16x8*>(x.B + ((int64_t)r * out + ch) * x.rank + j);
-        if (id == r) {
-          const float* u = x.u + (int64_t)t * x.rank + j;
-          f32x4 v[2] = {*reinterpret_cast<const f32x4*>(u), *reinterpret_cast<const f32x4*>(u + 4)};
-          for (int s = 1; s < x.slices; s++) {
-            u += x.stride;
-            v[0] += *reinterpret_cast<const f32x4*>(u);
-            v[1] += *reinterpret_cast<const f32x4*>(u + 4);
-          }
+constexpr int kParts = OUT == kOutF32 ? 3 : 2;
+
+// w as the sum of NP bf16 values; nothing is left of an infinity (a NaN is in the first)
+template <int NP>
+__device__ __forceinline__ void split_bf16(float w, __bf16 (&v)[NP]) {
 #pragma unroll
-          for (int e = 0; e < 8; e++) {
-            float w = v[e / 4][e % 4] * scale;
+  for (int k = 0; k < NP; k++) {
+    v[k] = (__bf16)w;
+    const float rest = w - (float)v[k];
+    w = rest == rest ? rest : 0.0f;
+  }
+}
+
+__device__ __forceinline__ int adapter_of(const Adapters& x, int t, int tokens) {
+  const int id = t < tokens ? x.adapter[t] : -1;
+  return (unsigned)id < (unsigned)x.adapters ? id : -1;
+}
+
+// 8 of B's values of adapter r: rank values j .. j + 7 of a channel, zeros past either's end
+__device__ __forceinline__ bf16x8 load_b(const Adapters& x, int r, int ch, int out, int j) {
+  bf16x8 b = {};
+  if (ch < out && j < x.rank)
+    b = *reinterpret_cast<const bf16x8*>(x.B + ((int64_t)r * out + ch) * x.rank + j);
+  return b;
+}
+
+// where the parts of a block of tokens begin
+template <int NP>
+__device__ __forceinline__ const uint16_t* parts_of(const Adapters& x, int t0) {
+  return x.parts + (int64_t)(t0 / 32) * ((x.rank + 15) / 16) * (NP * 512);
+}
+
+// The rank values j0 .. j0 + 15 of the 32 tokens from t0 on, split; SUM: they may lie in partial sums
+// (up to kSliceTokens tokens, which no tile kernel takes). Columns of tokens without an adapter
+// hold anything.
+template <int NP, bool SUM>
+__device__ __forceinline__ void load_u(const Adapters& x, int t0, int tokens, float scale, int j0,
+                                       bf16x8 (&part)[NP]) {
+  const int lane = threadIdx.x & 63;
+  if (!SUM || x.parts) {
+    const uint16_t* at = parts_of<NP>(x, t0) + (int64_t)(j0 / 16) * (NP * 512) + lane * 8;
 #pragma unroll
-            for (int k = 0; k < NP; k++) {
-              part[k][e] = (__bf16)w;
-              const float rest = w - (float)part[k][e];
-              w = rest == rest ? rest : 0.0f;  // nothing is left of an infinity (a NaN is in part 0)
-            }
-          }
-        }
+    for (int k = 0; k < NP; k++) part[k] = *reinterpret_cast<const bf16x8*>(at + k * 512);
+    return;
+  }
+  const int t = min(t0 + (lane & 31), tokens - 1), j = j0 + 8 * (lane >> 5);
+  const float* at = x.u + (int64_t)t * x.rank + j;
+  f32x4 w[kMaxSlices][2], v[2] = {};
+#pragma unroll
+  for (int s = 0; s < kMaxSlices; s++)
+#pragma unroll
+    for (int e = 0; e < 2; e++)
+      w[s][e] = s < x.slices && j < x.rank
+                    ? *reinterpret_cast<const f32x4*>(at + s * x.stride + 4 * e) : f32x4{};
+#pragma unroll
+  for (int s = 0; s < kMaxSlices; s++)
+#pragma unroll
+    for (int e = 0; e < 2; e++) v[e] += w[s][e];
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    __bf16 y[NP];
+    split_bf16<NP>(v[e / 4][e % 4] * scale, y);
+#pragma unroll
+    for (int k = 0; k < NP; k++) part[k][e] = y[k];
+  }
+}
+
+// The distinct adapters of 32 tokens in order of their first token, those numbered first, first +
+// step, .., up to T at a time with their rows of B (M blocks of 32 channels, 16 rank values).
+template <int M, int T>
+struct AdapterWalk {
+  int id;              // this lane's token's adapter
+  uint32_t all, left;  // tokens with an adapter; with one not taken yet
+  int q, r[T];
+  bf16x8 b[T][M];
+
+  __device__ __forceinline__ void start(const Adapters& x, int t0, int tokens) {
+    id = adapter_of(x, t0 + (threadIdx.x & 31), tokens);
+    all = (uint32_t)__ballot(id >= 0);  // the halves agree
+    again();
+  }
+  __device__ __forceinline__ void again() {
+    left = all;
+    q = 0;
+  }
+  __device__ __forceinline__ void next(const Adapters& x, int rb0, int out, int j0, int first, int step) {
+    const int rl = threadIdx.x & 31, j = j0 + 8 * ((threadIdx.x & 63) >> 5);
+#pragma unroll
+    for (int g = 0; g < T; g++) {
+      r[g] = -1;
+      while (left && r[g] < 0) {
+        const int one = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+        left &= ~(uint32_t)__ballot(id == one);
+        if (q % step == first) r[g] = one;
+        q++;
       }
-#pragma unroll
-      for (int k = 0; k < NP; k++) d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, part[k], d, 0, 0, 0);
     }
 #pragma unroll
-    for (int v = 0; v < 16; v++) sum[v] = id == r ? d[v] : sum[v];
+    for (int g = 0; g < T; g++)
+      if (r[g] >= 0)
+#pragma unroll
+        for (int m = 0; m < M; m++) b[g][m] = load_b(x, r[g], (rb0 + m) * 32 + rl, out, j);
   }
-  return sum;
+};
+
+// Adds the adapters' part to the sums of M blocks of 32 channels (from row block rb0 on) of the 32
+// tokens from t0 on (matrix results; lane: token lane % 32), adapter by adapter of `walk`, whose first
+// step has been taken. Each is a product of B's rows with the rank values of all 32 tokens, of which
+// its own tokens keep theirs: columns do not mix, so a NaN or an infinity in one adapter reaches no
+// other's tokens. B's rows of the next T adapters are loaded meanwhile.
+template <int OUT, int M, bool SUM, int T>
+__device__ __forceinline__ void adapter_blocks(const Adapters& x, AdapterWalk<M, T>& walk, int t0,
+                                               int tokens, int rb0, int out, int first, int step,
+                                               v16f (&sum)[M]) {
+  constexpr int NP = kParts<OUT>;
+  if (!walk.all) return;
+  const int id = walk.id;
+  const float scale = SUM && !x.parts && x.scale && id >= 0 ? x.scale[id] : 1.0f;
+  for (int j0 = 0; j0 < x.rank; j0 += 16) {
+    bf16x8 part[NP];
+    load_u<NP, SUM>(x, t0, tokens, scale, j0, part);
+    if (j0) {
+      walk.again();
+      walk.next(x, rb0, out, j0, first, step);
+    }
+    while (walk.r[0] >= 0) {
+      AdapterWalk<M, T> now = walk;
+      walk.next(x, rb0, out, j0, first, step);
+#pragma unroll
+      for (int g = 0; g < T; g++)
+        if (now.r[g] >= 0)
+#pragma unroll
+          for (int m = 0; m < M; m++) {
+            v16f d = sum[m];
+#pragma unroll
+            for (int k = 0; k < NP; k++)
+              d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now.b[g][m], part[k], d, 0, 0, 0);
+#pragma unroll
+            for (int v = 0; v < 16; v++) sum[m][v] = id == now.r[g] ? d[v] : sum[m][v];
+          }
+    }
+  }
+}
+
+// acc times a_i for a wave's M row blocks and NB blocks of 32 tokens
+template <int M, int NB>
+__device__ __forceinline__ void times_a(const MlpArgs& p, int rb0, v16f (&acc)[M][NB]) {
+  if (!p.a[0]) return;
+  const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int m = 0; m < M; m++) {
+    f32x4 a[4];
+#pragma unroll
+    for (int g = 0; g < 4; g++)
+      a[g] = load_channels(p.a[0], (rb0 + m) * 32 + g * 8 + h * 4, p.out, 1.0f);
+#pragma unroll
+    for (int n = 0; n < NB; n++)
+#pragma unroll
+      for (int v = 0; v < 16; v++) acc[m][n][v] = acc[m][n][v] * a[v / 4][v % 4];
+  }
+}
+
+// The tile kernel's sums become a_i s plus the adapters' part. A block of 32 tokens with one adapter
+// takes its products straight onto the sums: B's rows go through LDS (`region`, 8 KiB of the wave's own),
+// eight lanes to a row of 64 rank values as the tokens of the main loop do, once for neighbouring
+// blocks of one adapter, and the rank values are loaded a block ahead. Loaded straight into operands
+// both would touch a cache line a lane (4096 tokens, rank 64, 4096 -> 14336: 181 us). Other blocks go by
+// adapter_blocks.
+template <int OUT, int NB>
+__device__ __forceinline__ void adapter_tile(const MlpArgs& p, const Adapters& x, int rb0, int t0,
+                                             int rows, uint8_t* region, v16f (&acc)[2][NB]) {
+  constexpr int NP = kParts<OUT>;
+  const int lane = threadIdx.x & 63, rl = lane & 31, h = lane >> 5;
+  __builtin_amdgcn_sched_barrier(0);
+  times_a<2, NB>(p, rb0, acc);
+  __builtin_amdgcn_sched_barrier(0);
+  constexpr int kMixed = -2;
+  int one[NB];  // each block's adapter, -1 for none
+#pragma unroll
+  for (int n = 0; n < NB; n++) {
+    const int id = adapter_of(x, t0 + n * 32 + rl, p.tokens);
+    one[n] = __builtin_amdgcn_readfirstlane(id);
+    if (!__all(id == one[n] || n * 32 + rl >= rows)) one[n] = kMixed;
+  }
+  // the wave's channels as rows of LDS, 8 j + lane / 8 this lane's to load; rows and rank values past
+  // the end read zeros
+  const int nch = min(64, p.out - rb0 * 32);
+  const uint32_t pitch = (uint32_t)x.rank * 2u;
+  uint32_t vo[8];
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    const int r = 8 * j + (lane >> 3);
+    vo[j] = r < nch ? (uint32_t)r * pitch : kOob;
+  }
+  const int xt = (rl & 7) ^ ((rl >> 3) & 1);
+  for (int j0 = 0; j0 < x.rank; j0 += 64) {
+    const int steps = min(4, (x.rank - j0 + 15) / 16);
+    bf16x8 u[2][4][NP];
+    auto load = [&](int n, bf16x8 (&f)[4][NP]) {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (i < steps) load_u<NP, false>(x, t0 + n * 32, p.tokens, 1.0f, j0 + 16 * i, f[i]);
+    };
+    int staged = -1;
+    if (one[0] >= 0) load(0, u[0]);
+#pragma unroll
+    for (int n = 0; n < NB; n++) {
+      if (n + 1 < NB && one[n + 1 < NB ? n + 1 : n] >= 0) load(n + 1, u[(n + 1) & 1]);
+      const int r = one[n];
+      if (r < 0) continue;
+      if (r != staged) {
+        staged = r;
+        const __amdgpu_buffer_rsrc_t rb =
+            rsrc(x.B + ((int64_t)r * p.out + rb0 * 32) * x.rank, (uint32_t)max(nch, 0) * pitch);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // the rows before are read
+        wave_lds_order();
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          const int row = 8 * j + (lane >> 3);
+          const int pc = (lane & 7) ^ (row & 7) ^ ((row >> 3) & 1);
+          const bool in = vo[j] != kOob && j0 + pc * 8 < x.rank;
+          load_lds(rb, region + j * 1024, in ? vo[j] + (uint32_t)(j0 + pc * 8) * 2u : kOob, 0);
+        }
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        wave_lds_order();
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        if (i >= steps) continue;
+        const uint8_t* at = region + rl * kRowB + ((2 * i + h) ^ xt) * 16;
+        bf16x8 b[2];
+#pragma unroll
+        for (int m = 0; m < 2; m++) b[m] = *reinterpret_cast<const bf16x8*>(at + m * 32 * kRowB);
+#pragma unroll
+        for (int k = 0; k < NP; k++)
+#pragma unroll
+          for (int m = 0; m < 2; m++)
+            acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[m], u[n & 1][i][k], acc[m][n], 0, 0, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NB; n++) {
+    if (one[n] != kMixed) continue;
+#pragma unroll
+    for (int m = 0; m < 2; m++) {
+      AdapterWalk<1, 2> walk;
+      walk.start(x, t0 + n * 32, p.tokens);
+      walk.next(x, rb0 + m, p.out, 0, 0, 1);
+      v16f d[1] = {acc[m][n]};
+      adapter_blocks<OUT, 1, false, 2>(x, walk, t0 + n * 32, p.tokens, rb0 + m, p.out, 0, 1, d);
+      acc[m][n] = d[0];
+      __builtin_amdgcn_sched_barrier(0);  // one block's registers at a time
+    }
+  }
 }
 
 // ------------------------------------------------------------------- split-k kernel
@@ -633,9 +842,13 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p, X x) {
       load(std::integral_constant<int, J + 2 - PER>{}, q + W, par ^ 1, f);
     __builtin_amdgcn_sched_barrier(0);
   };
+  // the first adapters of the first tokens are found, and their rows of B loaded, before the loop
+  AdapterWalk<M, 4> walk;
+  if constexpr (kAdapters<X>) walk.start(x, t0, p.tokens);
   load(std::integral_constant<int, 0>{}, wave, 0, f0);
   __builtin_amdgcn_sched_barrier(0);
   load(std::integral_constant<int, 1>{}, wave, 0, f1);
+  if constexpr (kAdapters<X>) walk.next(x, rb0, p.out, 0, wave, W);
   for (int q = wave, par = 0; q < nper; q += W, par ^= 1) {
     stage(std::integral_constant<int, 0>{}, q, par);
     stage(std::integral_constant<int, 1>{}, q, par);
@@ -648,20 +861,21 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p, X x) {
   // reuses that memory
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
 
-  // adapters: this wave's share of every token's, joined with its share of k
+  // adapters: this wave's share of them, joined with its share of k
   if constexpr (kAdapters<X>) {
+    times_a<M, NB>(p, rb0, acc);
 #pragma unroll
-    for (int m = 0; m < M; m++) {
-      f32x4 a[4];
+    for (int n = 0; n < NB; n++) {
+      v16f d[M];
 #pragma unroll
-      for (int g = 0; g < 4; g++)
-        a[g] = load_channels(p.a[0], (rb0 + m) * 32 + g * 8 + h * 4, p.out, 1.0f);
-#pragma unroll
-      for (int n = 0; n < NB; n++) {
-        const v16f d = adapter_block<OUT>(x, t0 + n * 32, p.tokens, rb0 + m, p.out, wave, W);
-#pragma unroll
-        for (int v = 0; v < 16; v++) acc[m][n][v] = acc[m][n][v] * a[v / 4][v % 4] + d[v];
+      for (int m = 0; m < M; m++) d[m] = acc[m][n];
+      if (n) {
+        walk.start(x, t0 + n * 32, p.tokens);
+        walk.next(x, rb0, p.out, 0, wave, W);
       }
+      adapter_blocks<OUT, M, NB == 1>(x, walk, t0 + n * 32, p.tokens, rb0, p.out, wave, W, d);
+#pragma unroll
+      for (int m = 0; m < M; m++) acc[m][n] = d[m];
     }
   }
 
@@ -887,7 +1101,7 @@ template <bool GATED>
 constexpr int kWaveStaging = 2 * 32 * (128 * (GATED ? 1 : 2) + 16);  // LDS bytes of a wave
 
 template <bool GATED, int NB, int OUT, class X>
-__device__ __forceinline__ void tile_store(const MlpArgs& p, const X& x, const int* list, int expert,
+__device__ __forceinline__ void tile_store(const MlpArgs& p, const int* list, int expert,
                                            const v16f (&acc)[2][NB], int rb0, int t0, int rows,
                                            uint8_t* region) {
   constexpr int ME = GATED ? 1 : 2;       // row blocks of results
@@ -969,21 +1183,11 @@ __device__ __forceinline__ void tile_store(const MlpArgs& p, const X& x, const i
       });
     } else {
 #pragma unroll
-      for (int m = 0; m < ME; m++) {
+      for (int m = 0; m < ME; m++)
 #pragma unroll
         for (int g = 0; g < 4; g++)
           y[m][g] = f32x4{acc[m][n][4 * g], acc[m][n][4 * g + 1], acc[m][n][4 * g + 2],
                           acc[m][n][4 * g + 3]};
-        if constexpr (kAdapters<X>) {
-          const v16f d = adapter_block<OUT>(x, t0 + n * 32, p.tokens, rb0 + m, p.out, 0, 1);
-#pragma unroll
-          for (int g = 0; g < 4; g++) {
-            const f32x4 a = load_channels(p.a[0], (rb0 + m) * 32 + 8 * g + 4 * h, p.out, 1.0f);
-#pragma unroll
-            for (int e = 0; e < 4; e++) y[m][g][e] = y[m][g][e] * a[e] + d[4 * g + e];
-          }
-        }
-      }
     }
     if constexpr (OUT >= kOutFp4) {
 #pragma unroll
@@ -1213,8 +1417,14 @@ __global__ __launch_bounds__(256, 2) void k_mlp_tile(MlpArgs p, int nti, int ntt
   // epilogue reuses that memory
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
   __syncthreads();  // every wave is done with the main loop's LDS
+  if constexpr (kAdapters<X>) {
+    static_assert(OUT < kOutFp4, "kWaveStaging bytes of a wave's own");
+    adapter_tile<OUT, NB>(p, x, rb0, t0, rows, lds + wave * kWaveStaging<GATED>, acc);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // read before the epilogue stages rows there
+    wave_lds_order();
+  }
   uint8_t* region = lds + (OUT >= kOutFp4 ? 0 : wave * kWaveStaging<GATED>);
-  tile_store<GATED, NB, OUT>(p, x, list, expert, acc, rb0, t0, rows, region);
+  tile_store<GATED, NB, OUT, X>(p, list, expert, acc, rb0, t0, rows, region);
 }
 
 // ---------------------------------------------------------------------------------- host
@@ -1312,7 +1522,8 @@ hipError_t launch_o(const MlpArgs& whole, const X& whole_x, bool act8, hipStream
     p.xs += t * (p.K / 32);
     X x = whole_x;
     if constexpr (kAdapters<X>) {
-      x.u += t * x.rank;
+      if (x.parts) x.parts += t / 32 * ((x.rank + 15) / 16) * (kParts<OUT> * 512);
+      else x.u += t * x.rank;
       x.adapter += t;
     }
     const size_t off = out_bytes(OUT, t * p.out);
