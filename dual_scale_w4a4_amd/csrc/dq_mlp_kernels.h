@@ -304,11 +304,39 @@ constexpr int kInlinePairs = 1024;  // the most that a workgroup counts by itsel
 // of LDS that nothing else uses until the next barrier after the call.
 __device__ __forceinline__ bool find_tile(const Experts& x, int slot, int tile, int* scratch,
                                           int* out) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  auto before = [](uint64_t m) {  // lanes of m below this one
+    return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+  };
+  if (x.pairs <= 64) {  // a lane per row, experts in order of their first: no counts, one barrier
+    const int id = lane < x.pairs ? x.ids[lane] : -1;
+    uint64_t left = __ballot((unsigned)id < (unsigned)x.experts);
+    for (int t = 0; left;) {
+      const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+      const uint64_t m = __ballot(id == e);
+      left &= ~m;
+      const int rows = __popcll(m), n = (rows + tile - 1) / tile;
+      if (slot < t + n) {
+        const int from = (slot - t) * tile, at = before(m) - from;
+        const int count = min(rows - from, tile);
+        if (wave == 0) {
+          if (id == e && at >= 0 && at < count) out[2 + at] = lane;
+          if (lane == 0) {
+            out[0] = e;
+            out[1] = count;
+          }
+        }
+        __syncthreads();
+        return true;
+      }
+      t += n;
+    }
+    return false;
+  }
   int* cnt = scratch;
   int* wsum = scratch + kMaxExperts;       // 4 waves' tiles, then their rows
   int* found = scratch + kMaxExperts + 8;  // expert, tile of it, its rows, its first row in order
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int e = tid; e < kMaxExperts; e += 256) cnt[e] = x.counts && e < x.experts ? x.counts[e] : 0;
   if (tid == 0) found[0] = -1;
   __syncthreads();
@@ -370,8 +398,7 @@ __device__ __forceinline__ bool find_tile(const Experts& x, int slot, int tile, 
     for (int i = 0; i < x.pairs; i += 64) {
       const bool mine = i + lane < x.pairs && x.ids[i + lane] == e;
       const uint64_t m = __ballot(mine);
-      const int at = seen - from + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
-                                                             __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+      const int at = seen - from + before(m);
       if (mine && at >= 0 && at < n) out[2 + at] = i + lane;
       seen += __popcll(m);
     }
@@ -1280,7 +1307,12 @@ __global__ __launch_bounds__(256, 2) void k_mlp_tile(MlpArgs p, int nti, int ntt
   constexpr int NK = steps(ACT8);
   constexpr int PER = ACT8 ? 4 : 2;  // stages per period (512 k)
   int ti, tt;
-  tile_origin(nti, ntt, ti, tt);
+  if constexpr (kExperts<X>) {  // tiles that do not exist come last, on every XCD alike
+    ti = blockIdx.x % nti;
+    tt = blockIdx.x / nti;
+  } else {
+    tile_origin(nti, ntt, ti, tt);
+  }
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   TileLds<NB>& L = *reinterpret_cast<TileLds<NB>*>(lds);

@@ -24,10 +24,15 @@ __global__ __launch_bounds__(1024) void k_moe_plan(const int* ids, int pairs, in
   const int share = ((pairs + 1023) / 1024) * 64;
   const int from = min(wave * share, pairs), to = min(from + share, pairs);
   int mine = 0, less = 0;
-  for (int i = from; i < to; i += 64) {
-    const int id = i + lane < to ? ids[i + lane] : -1;
-    mine += __popcll(__ballot(id == e));
-    less += __popcll(__ballot(id >= 0 && id < e));
+  for (int i = from; i < to; i += 256) {  // four loads in flight
+    int id[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) id[k] = i + 64 * k + lane < to ? ids[i + 64 * k + lane] : -1;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      mine += __popcll(__ballot(id[k] == e));
+      less += __popcll(__ballot(id[k] >= 0 && id[k] < e));
+    }
   }
   if (lane == 0) {
     own[wave] = mine;
@@ -41,13 +46,22 @@ __global__ __launch_bounds__(1024) void k_moe_plan(const int* ids, int pairs, in
     if (w < wave) at += own[w];
   }
   if (threadIdx.x == 0) counts[e] = total;
-  for (int i = from; i < to; i += 64) {
-    const bool is = i + lane < to && ids[i + lane] == e;
-    const uint64_t m = __ballot(is);
-    if (is)
-      order[at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
-                                           __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u))] = i + lane;
-    at += __popcll(m);
+  for (int i = from; i < to; i += 256) {
+    bool is[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const int at = i + 64 * k + lane;
+      is[k] = at < to && ids[min(at, to - 1)] == e;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const uint64_t m = __ballot(is[k]);
+      if (is[k])
+        order[at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
+                                             __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u))] =
+            i + 64 * k + lane;
+      at += __popcll(m);
+    }
   }
 }
 
@@ -72,13 +86,23 @@ __global__ __launch_bounds__(256) void k_moe_sum(SumArgs p) {
   if (ch >= p.out) return;
   const float* y = p.y + t * p.top_k * p.out + ch;
   f32x4 sum = {};
-  for (int s = 0; s < p.top_k; s++) {
-    const int e = p.ids[t * p.top_k + s];
-    if ((unsigned)e >= (unsigned)p.experts) continue;  // its y was not written
-    const float w = p.weights[t * p.top_k + s];
-    const f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(y + (int64_t)s * p.out));
+  // eight experts at a time, all their loads in flight; one out of range has no y
+  constexpr int kAt = 8;
+  for (int s0 = 0; s0 < p.top_k; s0 += kAt) {
+    f32x4 v[kAt];
+    float w[kAt];
+    bool in[kAt];
 #pragma unroll
-    for (int k = 0; k < 4; k++) sum[k] = sum[k] + w * v[k];
+    for (int s = 0; s < kAt; s++) {
+      const int at = min(s0 + s, p.top_k - 1);
+      w[s] = p.weights[t * p.top_k + at];
+      in[s] = s0 + s < p.top_k && (unsigned)p.ids[t * p.top_k + at] < (unsigned)p.experts;
+      v[s] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(y + (int64_t)at * p.out));
+    }
+#pragma unroll
+    for (int s = 0; s < kAt; s++)
+#pragma unroll
+      for (int k = 0; k < 4; k++) sum[k] = in[s] ? sum[k] + w[s] * v[s][k] : sum[k];
   }
   const int64_t off = t * p.out + ch;
   if (p.res) {
@@ -130,17 +154,24 @@ bool moe_sizes(int64_t tokens, int64_t K, int64_t inner, int64_t out, int64_t ex
          out <= kMost && experts >= 1 && experts <= kMaxExperts && top_k >= 1 && top_k <= kMaxTopK;
 }
 
-// Which kernel: tiles of 32 rows with k split over the waves while an expert has no more rows than
-// that on average, else the tile kernel with 64 or 128.
+// Which kernel, by the mean number of rows of the experts that can have any. Measured, us, gated and
+// down product, MXFP4 then MXFP8 between them:
+//   experts, top k, K -> inner, tokens (mean)   split, 32 rows   tile, 64 rows   tile, 128 rows
+//   64, 8, 4096 -> 1536, 24 (3)                 65 + 51          81 + 54         85 + 63
+//   32, 4, 4096 -> 1536, 128 (16)               50 + 40          49 + 40         50 + 44
+//   8, 2, 4096 -> 4096, 100 (25)                37 + 25          33 + 32         35 + 37
+//   64, 8, 2048 -> 1024, 300 (37)               48 + 44          44 + 32         42 + 37
+//   32, 4, 4096 -> 1536, 700 (87)               84 + 84          69 + 58         75 + 58
+//   64, 8, 2048 -> 1024, 3000 (375)             249 + 244        115 + 106       94 + 102
 template <bool ACT8, bool GATED, int OUT>
 hipError_t launch_experts(const MlpArgs& p, Experts x, hipStream_t s) {
   const int used = std::min(x.pairs, x.experts), mean = x.pairs / used;
   auto slots = [&](int tile) { return used + x.pairs / tile; };
-  if (mean <= 32) {
+  if (mean <= 24) {
     x.slots = slots(32);
     return launch_split<ACT8, GATED, OUT, 2, 1>(p, x, s);
   }
-  if (mean <= 64) {
+  if (mean <= 128) {
     x.slots = slots(64);
     return launch_tile<ACT8, GATED, OUT, 2>(p, x, s);
   }
