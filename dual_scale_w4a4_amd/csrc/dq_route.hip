@@ -4,16 +4,23 @@
 // Which experts a token takes must not depend on the order of a sum, so a logit is the fp64 sum of
 // the exact products rounded once to fp32, and scores and selection keys are fp64.
 //
-// Two launches. The logits: with few tokens a wave takes one expert and up to 8 tokens, k over its
-// lanes; with more the fp64 matrix instruction takes tiles of 32 tokens by 32 experts a wave, k over
+// Two launches. The logits: for small products a wave takes one expert and up to 4 tokens, k over its
+// lanes; for larger ones the fp64 matrix instruction takes tiles of 32 tokens by 32 experts a wave, k over
 // the workgroup's waves. Then a wave per token selects.
+//
+// For large products of bf16 values the fp64 instruction is what bounds that (4096 tokens, 128 experts,
+// K 4096: 79 us of 87, 54 TFLOP/s), so the first launch takes the bf16 instruction instead and gives each
+// logit with a bound on its error, and the second computes in fp64 the few experts of each token
+// that the bounds leave in question, the chosen ones among them: the same result. Where scores of other
+// experts enter the result (the softmax's sum with a bias or without renormalization), or a value is
+// not finite, that is every expert.
 #include <float.h>
 #include <limits.h>
 
 #include <algorithm>
 
 #include "../../include/dq_layer.h"
-#include "dq_outq.h"
+#include "dq_mlp_kernels.h"
 
 namespace dqr {
 
@@ -133,84 +140,378 @@ __global__ __launch_bounds__(W * 64) void k_logits_many(LogitArgs p) {
   }
 }
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+// Logits within a bound: {l, d} with |l - the exact sum| <= d. A workgroup takes 32 tokens and 64
+// experts; its waves share the two blocks of 32 experts and, in periods of 64 k, the channels. Each
+// runs by itself through two LDS stages of its own (rows of one cache line, pieces swizzled), as the
+// adapters' rank kernel does. Products of bf16 values are exact in fp32; a period's 64 are added in
+// fp32, with at most 64 roundings of 2^-23 of the sum of their magnitudes, which a second product of
+// the magnitudes gives; the periods' sums are added in fp64.
+constexpr int kFastWaves = 8, kFastCols = 1 << 16;
+
+struct FastArgs {
+  const uint16_t* X;
+  const uint16_t* W;
+  float* out;        // tokens x experts x 2
+  int64_t tokens;
+  int cols, experts;
+};
+
+__global__ __launch_bounds__(kFastWaves * 64) void k_logits_fast(FastArgs p) {
+  using namespace dqm;
+  constexpr int kTile = 32 * kRowB, kRing = 4 * kTile, kShare = kFastWaves / 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kFastWaves * kRing];
+  const int lane = threadIdx.x & 63, rl = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ne = (p.experts + 63) / 64;
+  const int e0 = (blockIdx.x % ne) * 64 + (wave & 1) * 32;
+  const int64_t t0 = (int64_t)(blockIdx.x / ne) * 32;
+  const uint32_t pitch = (uint32_t)p.cols * 2u;
+  // rows past the end read zeros
+  const int nt = (int)min((int64_t)32, p.tokens - t0), nx = max(min(32, p.experts - e0), 0);
+  const __amdgpu_buffer_rsrc_t rx = rsrc(p.X + t0 * p.cols, (uint32_t)nt * pitch);
+  const __amdgpu_buffer_rsrc_t rw = rsrc(p.W + (int64_t)(nx ? e0 : 0) * p.cols, (uint32_t)nx * pitch);
+  const __amdgpu_buffer_rsrc_t rnone = rsrc(p.X, 0u);
+  uint32_t vo[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const int r = 8 * j + (lane >> 3);
+    vo[j] = (uint32_t)r * pitch + (uint32_t)(((lane & 7) ^ (r & 7) ^ ((r >> 3) & 1)) * 16);
+  }
+  uint8_t* ring = lds + wave * kRing;
+  const int xt = (rl & 7) ^ ((rl >> 3) & 1);
+  const int periods = p.cols / 64, first = wave >> 1;
+  double sum[16] = {};
+  v16f size = {};
+  auto load = [&](int c, int st) {  // past the last period nothing is read
+    const bool on = c < periods;
+    uint8_t* dst = ring + st * (2 * kTile);
+#pragma unroll
+    for (int j = 0; j < 4; j++) load_lds(on ? rx : rnone, dst + j * 1024, vo[j], c * kRowB);
+#pragma unroll
+    for (int j = 0; j < 4; j++) load_lds(on ? rw : rnone, dst + kTile + j * 1024, vo[j], c * kRowB);
+  };
+  auto stage = [&](int c, int st) {
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(8));
+    wave_lds_order();
+    const uint8_t* src = ring + st * (2 * kTile) + rl * kRowB;
+    u32x4 x[4], w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int at = ((2 * i + h) ^ xt) * 16;
+      x[i] = *reinterpret_cast<const u32x4*>(src + at);
+      w[i] = *reinterpret_cast<const u32x4*>(src + kTile + at);
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): read before the stage is loaded again
+    wave_lds_order();
+    load(c + 2 * kShare, st);
+    v16f acc = {};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x[i]),
+                                                    __builtin_bit_cast(bf16x8, w[i]), acc, 0, 0, 0);
+      const u32x4 ax = x[i] & 0x7FFF7FFFu, aw = w[i] & 0x7FFF7FFFu;
+      size = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, ax),
+                                                     __builtin_bit_cast(bf16x8, aw), size, 0, 0, 0);
+    }
+#pragma unroll
+    for (int v = 0; v < 16; v++) sum[v] += (double)acc[v];
+  };
+  load(first, 0);
+  load(first + kShare, 1);
+  for (int c = first; c < periods; c += 2 * kShare) {
+    stage(c, 0);
+    stage(c + kShare, 1);  // zeros past the last
+  }
+  // the last loads read nothing but still write zeros into LDS: drain them before the join
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  __syncthreads();
+  // join: value v of a lane is token 8 (v / 4) + 4 h + v % 4, expert lane % 32
+  double* part = reinterpret_cast<double*>(lds);                            // [wave][v][lane]
+  float* part2 = reinterpret_cast<float*>(lds + kFastWaves * 16 * 64 * 8);  // likewise
+  static_assert(kFastWaves * 16 * 64 * 12 <= kFastWaves * kRing, "the join's LDS");
+#pragma unroll
+  for (int v = 0; v < 16; v++) {
+    part[(wave * 16 + v) * 64 + lane] = sum[v];
+    part2[(wave * 16 + v) * 64 + lane] = size[v];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * 16 * 64; i += kFastWaves * 64) {
+    const int b = i >> 10, v = (i >> 6) & 15, l = i & 63;
+    double s = 0.0;
+    float m = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kShare; w++) {
+      s += part[((2 * w + b) * 16 + v) * 64 + l];
+      m += part2[((2 * w + b) * 16 + v) * 64 + l];
+    }
+    const int64_t t = t0 + 8 * (v / 4) + 4 * (l >> 5) + v % 4;
+    const int e = (blockIdx.x % ne) * 64 + b * 32 + (l & 31);
+    if (t < p.tokens && e < p.experts) {
+      // the magnitudes' sum is itself off by up to cols / 2^23 of it, at most 1 / 128; the logit is
+      // rounded here and once more to compare; products below fp32's range may be lost
+      float2 o;
+      o.x = (float)s;
+      o.y = m * (1.02f / (1 << 17)) + fabsf(o.x) * 0x1p-22f + 0x1p-100f;
+      *reinterpret_cast<float2*>(p.out + (t * p.experts + e) * 2) = o;
+    }
+  }
+}
+
 struct SelectArgs {
-  const float* logits;
+  const float* logits; // tokens x experts, or tokens x experts x {logit, bound}
   const float* bias;   // experts, or null
   int* ids;
   float* weights;
   int64_t tokens;
   int experts, top_k, renormalize;
   float scale;
+  const uint16_t* X;   // with bounds: bf16 tokens x cols
+  const uint16_t* W;   // and experts x cols
+  int cols;
 };
 
-// Wave: one token; lane l holds experts l, l + 64, ... N of them. The k-th largest key is found k
-// times: the largest of each lane's, then of the wave's, ties to the lower index; a taken key becomes
-// -inf. NaN keys rank as -inf, and -inf keys by index.
-template <bool SIGMOID, int N>
-__global__ __launch_bounds__(256) void k_select(SelectArgs p) {
+// the largest of the wave's values, none of them NaN
+__device__ __forceinline__ double wave_max(double v) {
+  v = fmax(v, dq::dpp_f64<dq::kDppQuadXor1>(v));
+  v = fmax(v, dq::dpp_f64<dq::kDppQuadXor2>(v));
+  v = fmax(v, dq::dpp_f64<dq::kDppRowHalfMirror>(v));
+  v = fmax(v, dq::dpp_f64<dq::kDppRowMirror>(v));
+  return fmax(fmax(__shfl(v, 0, 64), __shfl(v, 16, 64)), fmax(__shfl(v, 32, 64), __shfl(v, 48, 64)));
+}
+
+__device__ __forceinline__ double wave_add(double v) {
+  v = dq::sum16_dpp(v);
+  return ((__shfl(v, 0, 64) + __shfl(v, 16, 64)) + __shfl(v, 32, 64)) + __shfl(v, 48, 64);
+}
+
+// The next of the largest keys among those still free, ties to the lowest index: its index, no longer
+// free.
+template <int N>
+__device__ __forceinline__ int take_largest(const double (&key)[N], bool (&is_free)[N], double& best) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= p.tokens) return;
-  double score[N], key[N];
-  bool free_[N];
+  double mine = -INFINITY;
+#pragma unroll
+  for (int n = 0; n < N; n++)
+    if (is_free[n]) mine = fmax(mine, key[n]);
+  best = wave_max(mine);
+  int at = -1;
+#pragma unroll
+  for (int n = 0; n < N; n++) {
+    const uint64_t m = __ballot(is_free[n] && key[n] == best);
+    if (at < 0 && m) {
+      at = n * 64 + __builtin_ctzll(m);
+      if (lane == (at & 63)) is_free[n] = false;
+    }
+  }
+  return at;
+}
+
+__device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
+
+// The product of two bf16 values, finite, times 2^-896 as fp64. It is exact in fp32 (16 bits; what
+// fp32's range may cut is below 2^-149, and no score tells logits that small from zero), and fp32's
+// exponent field is taken as fp64's: a shift, which loses none of the bits set, where a conversion
+// takes four times as long.
+constexpr int kShift = 896;
+__device__ __forceinline__ double shifted_product(float x, float w) {
+  const uint32_t u = dq::f2u(x * w);
+  return dq::u2d((unsigned long long)((u & 0x80000000u) | ((u & 0x7FFFFFFFu) >> 3)) << 32);
+}
+
+// fp64 dot products of a token's row with G experts' rows, in every lane. FINITE: all values are. A
+// wave waits for memory here, so U 512-channel pieces of all rows are loaded at once.
+template <int G, int U, bool FINITE>
+__device__ __forceinline__ void dots(const SelectArgs& p, const uint16_t* x, const int (&e)[G],
+                                     double (&s)[G]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int g = 0; g < G; g++) s[g] = 0.0;
+  for (int c0 = lane * 8; c0 < p.cols; c0 += 512 * U) {
+    u32x4 xr[U], wr[U][G];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int c = c0 + 512 * u;
+      const bool in = c < p.cols;
+      xr[u] = in ? *reinterpret_cast<const u32x4*>(x + c) : u32x4{};
+#pragma unroll
+      for (int g = 0; g < G; g++)
+        wr[u][g] = in ? *reinterpret_cast<const u32x4*>(p.W + (int64_t)e[g] * p.cols + c) : u32x4{};
+    }
+    auto value = [](const u32x4& r, int k) { return u2f(k & 1 ? r[k / 2] & 0xFFFF0000u : r[k / 2] << 16); };
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const float xv = value(xr[u], k);
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+          const float w = value(wr[u][g], k);
+          if (FINITE) s[g] += shifted_product(xv, w);
+          else s[g] = fma((double)xv, (double)w, s[g]);
+        }
+      }
+  }
+#pragma unroll
+  for (int g = 0; g < G; g++) {
+    s[g] = wave_add(s[g]);
+    if (FINITE) s[g] = ldexp(s[g], kShift);
+  }
+}
+
+// Which experts of the token can be among the top_k, and their exact logits (in l of their lanes).
+// Keys grow with the logits, so an expert whose key at its upper bound lies below the top_k-th
+// largest of the keys at the lower bounds cannot; a margin covers the last bits of exp, where a tie
+// could lie. A bound that is no number leaves its expert in question.
+// WPT waves share the token's sums and hand them on in LDS.
+template <bool SIGMOID, int N, int WPT>
+__device__ __forceinline__ void recheck(const SelectArgs& p, int64_t t, double (&l)[N],
+                                        bool (&is_free)[N]) {
+  constexpr int G = WPT == 1 ? 4 : 2;
+  __shared__ float exact[WPT == 1 ? 1 : 64 * N];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  double lo[N], hi[N];
+  bool open[N], wild = false;
   double top = -INFINITY;
 #pragma unroll
   for (int n = 0; n < N; n++) {
     const int e = n * 64 + lane;
-    free_[n] = e < p.experts;
-    score[n] = free_[n] ? (double)p.logits[t * p.experts + e] : -INFINITY;
-    top = fmax(top, score[n]);
+    open[n] = is_free[n];
+    lo[n] = hi[n] = -INFINITY;
+    if (is_free[n]) {
+      const float2 v = *reinterpret_cast<const float2*>(p.logits + (t * p.experts + e) * 2);
+      lo[n] = (double)v.x - (double)v.y;
+      hi[n] = (double)v.x + (double)v.y;
+      top = fmax(top, hi[n]);
+      wild |= !(fabsf(v.x) + v.y < 1e38f);
+      if (SIGMOID) {
+        const double b = p.bias ? (double)p.bias[e] : 0.0;
+        lo[n] = sigmoid64(lo[n]) + b;
+        hi[n] = sigmoid64(hi[n]) + b;
+      }
+      if (!(lo[n] == lo[n])) lo[n] = -INFINITY;
+    }
   }
-  double total = 1.0;
+  double kth = -INFINITY;
+  for (int k = 0; k < p.top_k; k++) take_largest<N>(lo, open, kth);
+  kth -= 1e-12 * (1.0 + fabs(kth));
+  // softmax scores that underflow are equal, and one logit that is not finite is in every score
+  if (!SIGMOID && (__any(wild) || !(wave_max(top) - kth < 700.0))) kth = -INFINITY;
+#pragma unroll
+  for (int n = 0; n < N; n++) is_free[n] = is_free[n] && !(hi[n] < kth);
+  // their sums in fp64, G experts at a time and the last ones singly; a logit's magnitude and bound
+  // are not finite where one of its values is not
+  const uint16_t* x = p.X + t * p.cols;
+  const bool finite = !__any(wild);
+  uint64_t m[N];
+  int count = 0;
+#pragma unroll
+  for (int n = 0; n < N; n++) {
+    m[n] = __ballot(is_free[n]);
+    count += __popcll(m[n]);
+  }
+  auto next = [&] {
+    int e = -1;
+#pragma unroll
+    for (int n = 0; n < N; n++)
+      if (e < 0 && m[n]) {
+        e = n * 64 + __builtin_ctzll(m[n]);
+        m[n] &= m[n] - 1;
+      }
+    count--;
+    return e;
+  };
+  auto set = [&](int e, double sum) {
+    if (WPT > 1) {
+      if (lane == 0) exact[e] = (float)sum;
+      return;
+    }
+#pragma unroll
+    for (int n = 0; n < N; n++)
+      if (n == e >> 6 && lane == (e & 63)) l[n] = (double)(float)sum;
+  };
+  for (int q = 0; count > 0; q++) {
+    const bool mine = WPT == 1 || q % WPT == wave;
+    if (finite && count >= G) {
+      int e[G];
+      double v[G];
+#pragma unroll
+      for (int g = 0; g < G; g++) e[g] = next();
+      if (!mine) continue;
+      dots<G, 4, true>(p, x, e, v);
+#pragma unroll
+      for (int g = 0; g < G; g++) set(e[g], v[g]);
+    } else {
+      const int e[1] = {next()};
+      double v[1];
+      if (!mine) continue;
+      if (finite) dots<1, 8, true>(p, x, e, v);
+      else dots<1, 1, false>(p, x, e, v);
+      set(e[0], v[0]);
+    }
+  }
+  if (WPT > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; n++)
+      if (is_free[n]) l[n] = (double)exact[n * 64 + lane];
+  }
+}
+
+// Wave: one token; lane l holds experts l, l + 64, ... N of them. NaN keys rank as -inf. BOUNDS: the
+// logits come with bounds; experts that are not in question have no score, and the softmax's sum
+// cancels in the weights.
+template <bool SIGMOID, int N, bool BOUNDS, int WPT = 1>
+__global__ __launch_bounds__(256) void k_select(SelectArgs p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = WPT == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= p.tokens) return;
+  double score[N], key[N];
+  bool is_free[N];
+#pragma unroll
+  for (int n = 0; n < N; n++) {
+    const int e = n * 64 + lane;
+    is_free[n] = e < p.experts;
+    score[n] = -INFINITY;
+    if (!BOUNDS && is_free[n]) score[n] = (double)p.logits[t * p.experts + e];
+  }
+  if (BOUNDS) recheck<SIGMOID, N, WPT>(p, t, score, is_free);
+  if (WPT > 1 && threadIdx.x >= 64) return;
   if (SIGMOID) {
 #pragma unroll
-    for (int n = 0; n < N; n++) score[n] = 1.0 / (1.0 + exp(-score[n]));
+    for (int n = 0; n < N; n++) score[n] = sigmoid64(score[n]);
   } else {
+    double top = -INFINITY;
 #pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) top = fmax(top, __shfl_xor(top, m, 64));
+    for (int n = 0; n < N; n++) top = fmax(top, score[n]);
+    top = wave_max(top);
     double sum = 0.0;
 #pragma unroll
     for (int n = 0; n < N; n++) {
-      score[n] = free_[n] ? exp(score[n] - top) : 0.0;
+      score[n] = is_free[n] ? exp(score[n] - top) : 0.0;
       sum += score[n];
     }
-    total = dq::wave_sum(sum);
+    const double total = wave_add(sum);
 #pragma unroll
     for (int n = 0; n < N; n++) score[n] = score[n] / total;
   }
 #pragma unroll
   for (int n = 0; n < N; n++) {
     const int e = n * 64 + lane;
-    key[n] = score[n] + (p.bias && free_[n] ? (double)p.bias[e] : 0.0);
+    key[n] = score[n] + (p.bias && is_free[n] ? (double)p.bias[e] : 0.0);
     if (!(key[n] == key[n])) key[n] = -INFINITY;
   }
   double chosen = 0.0, mine = 0.0;  // the sum of the chosen scores; lane k: the k-th chosen
   int id = 0;
   for (int k = 0; k < p.top_k; k++) {
-    double best = -INFINITY;
-    int at = INT_MAX;
-#pragma unroll
-    for (int n = 0; n < N; n++)
-      if (free_[n] && (at == INT_MAX || key[n] > best)) {
-        best = key[n];
-        at = n * 64 + lane;
-      }
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const double b = __shfl_xor(best, m, 64);
-      const int a = __shfl_xor(at, m, 64);
-      if (b > best || (b == best && a < at)) {
-        best = b;
-        at = a;
-      }
-    }
+    double best;
+    const int at = take_largest<N>(key, is_free, best);
     double s = 0.0;
 #pragma unroll
     for (int n = 0; n < N; n++)
-      if (n * 64 + lane == at) {
-        free_[n] = false;
-        s = score[n];
-      }
+      if (n == at >> 6) s = score[n];
     s = __shfl(s, at & 63, 64);
     chosen += s;
     if (lane == k) {
@@ -230,9 +531,30 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs p) {
 
 constexpr int kMaxTopK = 32;
 
+// Which kernels, by tokens x experts x channels; logits + selection measured, us, 8 experts, sigmoid:
+//   experts, K     tokens   a wave an expert   fp64 instruction   bounds, 1 wave a token to select
+//   128, 4096      64       11 + 5             46 + 5             12 + 19
+//                  256      22 + 5             46 + 5             12 + 18
+//                  512      42 + 5             46 + 5             13 + 20
+//                  4096                        79 + 8             18 + 39
+//   64, 2048       512      15 + 4             24 + 5             9 + 12
+//                  4096                        29 + 7             10 + 25
+//   256, 7168      128      35 + 7             78 + 7             20 + 30
+//                  256      68 + 7             89 + 7             21 + 33
+//                  4096                        278 + 11           50 + 70
+// so bounds from 2^27 on, where they can be had, and the fp64 instruction from 2^28.
+// Whether they can: bf16 values in whole periods, and a result that only the chosen experts' scores
+// enter.
+bool with_bounds(dq_dtype xt, dq_dtype wt, int64_t tokens, int64_t cols, int64_t experts,
+                 const float* bias, dq_score score, int renormalize) {
+  return xt == DQ_BF16 && wt == DQ_BF16 && cols % 64 == 0 && cols <= kFastCols &&
+         (score == DQ_SCORE_SIGMOID || (renormalize && !bias)) &&
+         tokens * experts >= ((int64_t)1 << 27) / cols;
+}
+
 template <bool XB, bool WB>
 hipError_t launch_logits(const LogitArgs& p, hipStream_t s) {
-  if (p.tokens <= 64) {
+  if (p.tokens * p.experts < ((int64_t)1 << 28) / p.cols) {
     const int64_t ne = (p.experts + 3) / 4;
     if (p.tokens == 1)
       hipLaunchKernelGGL((k_logits_few<XB, WB, 1>), dim3((unsigned)ne), dim3(256), 0, s, p);
@@ -246,14 +568,37 @@ hipError_t launch_logits(const LogitArgs& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool SIGMOID>
-hipError_t launch_select(const SelectArgs& p, hipStream_t s) {
-  const dim3 grid((unsigned)((p.tokens + 3) / 4)), block(256);
-  if (p.experts <= 64) hipLaunchKernelGGL((k_select<SIGMOID, 1>), grid, block, 0, s, p);
-  else if (p.experts <= 128) hipLaunchKernelGGL((k_select<SIGMOID, 2>), grid, block, 0, s, p);
-  else if (p.experts <= 256) hipLaunchKernelGGL((k_select<SIGMOID, 4>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((k_select<SIGMOID, 16>), grid, block, 0, s, p);
+hipError_t launch_logits_fast(const LogitArgs& l, hipStream_t s) {
+  FastArgs p{};
+  p.X = static_cast<const uint16_t*>(l.X);
+  p.W = static_cast<const uint16_t*>(l.W);
+  p.out = l.logits;
+  p.tokens = l.tokens;
+  p.cols = l.cols;
+  p.experts = l.experts;
+  const int64_t n = (int64_t)((p.experts + 63) / 64) * ((p.tokens + 31) / 32);
+  hipLaunchKernelGGL(k_logits_fast, dim3((unsigned)n), dim3(kFastWaves * 64), 0, s, p);
   return hipGetLastError();
+}
+
+template <bool SIGMOID, int N>
+hipError_t launch_select_n(const SelectArgs& p, bool bounds, hipStream_t s) {
+  const dim3 grid((unsigned)((p.tokens + 3) / 4)), block(256);
+  if (!bounds)
+    hipLaunchKernelGGL((k_select<SIGMOID, N, false>), grid, block, 0, s, p);
+  else if (p.tokens <= 1024)  // a token's sums take a wave 14 us (K 4096), which waves then share
+    hipLaunchKernelGGL((k_select<SIGMOID, N, true, 4>), dim3((unsigned)p.tokens), block, 0, s, p);
+  else
+    hipLaunchKernelGGL((k_select<SIGMOID, N, true>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+template <bool SIGMOID>
+hipError_t launch_select(const SelectArgs& p, bool bounds, hipStream_t s) {
+  if (p.experts <= 64) return launch_select_n<SIGMOID, 1>(p, bounds, s);
+  if (p.experts <= 128) return launch_select_n<SIGMOID, 2>(p, bounds, s);
+  if (p.experts <= 256) return launch_select_n<SIGMOID, 4>(p, bounds, s);
+  return launch_select_n<SIGMOID, 16>(p, bounds, s);
 }
 
 }  // namespace dqr
@@ -264,7 +609,7 @@ dq_status dq_moe_route_workspace_bytes(int64_t tokens, int64_t experts, size_t* 
   using namespace dqr;
   if (!bytes || tokens < 1 || tokens > INT32_MAX - 256 || experts < 1 || experts > kMaxExperts)
     return DQ_ERR_ARG;
-  *bytes = ((size_t)tokens * (size_t)experts * 4 + 255) / 256 * 256;
+  *bytes = ((size_t)tokens * (size_t)experts * 8 + 255) / 256 * 256;
   return DQ_OK;
 }
 
@@ -292,17 +637,19 @@ dq_status dq_moe_route(const void* X, dq_dtype xt, int64_t tokens, int64_t cols,
                        {bias, (size_t)experts * 4}}))
     return DQ_ERR_ARG;
   // rounds of tokens so that no grid passes 2^31 threads
-  const int64_t chunk = 1 << 22;
+  const int64_t chunk = 1 << 20;
+  const bool bounds = with_bounds(xt, wt, tokens, cols, experts, bias, score, renormalize);
   for (int64_t t = 0; t < tokens; t += chunk) {
     LogitArgs l{};
     l.X = static_cast<const char*>(X) + t * cols * (xt == DQ_BF16 ? 2 : 4);
     l.W = W;
-    l.logits = static_cast<float*>(workspace) + t * experts;
+    l.logits = static_cast<float*>(workspace) + t * experts * 2;
     l.tokens = std::min(chunk, tokens - t);
     l.cols = (int)cols;
     l.experts = (int)experts;
     hipError_t e;
-    if (xt == DQ_BF16) e = wt == DQ_BF16 ? launch_logits<true, true>(l, stream)
+    if (bounds) e = launch_logits_fast(l, stream);
+    else if (xt == DQ_BF16) e = wt == DQ_BF16 ? launch_logits<true, true>(l, stream)
                                          : launch_logits<true, false>(l, stream);
     else e = wt == DQ_BF16 ? launch_logits<false, true>(l, stream)
                            : launch_logits<false, false>(l, stream);
@@ -317,7 +664,11 @@ dq_status dq_moe_route(const void* X, dq_dtype xt, int64_t tokens, int64_t cols,
     s.top_k = top_k;
     s.renormalize = renormalize;
     s.scale = scale;
-    e = score == DQ_SCORE_SIGMOID ? launch_select<true>(s, stream) : launch_select<false>(s, stream);
+    s.X = static_cast<const uint16_t*>(l.X);
+    s.W = static_cast<const uint16_t*>(W);
+    s.cols = l.cols;
+    e = score == DQ_SCORE_SIGMOID ? launch_select<true>(s, bounds, stream)
+                                  : launch_select<false>(s, bounds, stream);
     if (e != hipSuccess) return DQ_ERR_HIP;
   }
   return DQ_OK;

@@ -56,7 +56,8 @@ def _check(dq, tokens, cols, experts, top_k, xdt="bf16", wdt="bf16", score="soft
 @pytest.mark.parametrize("tokens,cols,experts,top_k", [
     (1, 8, 1, 1), (1, 4096, 64, 8), (1, 520, 257, 32), (2, 1000, 63, 5), (3, 512, 65, 8),
     (5, 2048, 128, 4), (17, 128, 1024, 32), (33, 8, 7, 7), (64, 1536, 129, 6), (65, 4096, 64, 8),
-    (70, 24, 5, 2), (97, 1000, 33, 3), (256, 520, 256, 8), (1000, 264, 100, 1), (130, 40, 1024, 32)])
+    (70, 24, 5, 2), (97, 1000, 33, 3), (256, 520, 256, 8), (1000, 264, 100, 1), (130, 40, 1024, 32),
+    (2100, 1000, 130, 8), (1111, 520, 520, 5)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_shapes(dq, tokens, cols, experts, top_k, score):
     _check(dq, tokens, cols, experts, top_k, score=score, bias=tokens % 2 == 1)
@@ -64,7 +65,7 @@ def test_shapes(dq, tokens, cols, experts, top_k, score):
 
 @pytest.mark.parametrize("xdt", ["bf16", "f32"])
 @pytest.mark.parametrize("wdt", ["bf16", "f32"])
-@pytest.mark.parametrize("tokens", [1, 9, 200])
+@pytest.mark.parametrize("tokens", [1, 9, 200, 4000])
 def test_types_and_weights(dq, xdt, wdt, tokens):
     for k, (score, bias, renormalize, scale) in enumerate((
             ("softmax", False, True, 1.0), ("softmax", True, False, 2.5),
@@ -129,7 +130,52 @@ def test_extreme_and_non_finite_values(dq):
     assert got[0].tolist() == [[2, 5, 1, 6, 0, 7, 8, 9, 3, 4]]
 
 
-@pytest.mark.parametrize("tokens", [6, 130])
+@pytest.mark.parametrize("score,bias", [("softmax", False), ("sigmoid", False), ("sigmoid", True)])
+@pytest.mark.parametrize("tokens,cols,experts,top_k", [
+    (150, 64, 40, 8), (700, 1024, 200, 8), (1100, 1024, 130, 32), (260, 4096, 130, 8),
+    (690, 192, 1024, 5), (500, 8192, 33, 1), (1500, 2048, 50, 4), (3000, 2560, 129, 32)])
+def test_many_tokens_close_logits(dq, tokens, cols, experts, top_k, score, bias):
+    # sums of large terms that cancel, and experts that differ in the last bit of a few weights: far
+    # more of them in question than are chosen (the products from 2^27 on go by bounds, those of up to
+    # 1024 tokens with four waves a token)
+    rng = np.random.default_rng(cols + experts)
+    X = ref.bf16(rng.standard_normal((tokens, cols)).astype(np.float32) * 8)
+    W = ref.bf16(rng.standard_normal((experts // 8 + 1, cols)).astype(np.float32))
+    W = W[rng.integers(0, len(W), experts)].copy()
+    at = rng.integers(0, cols, (experts, 2))
+    bits = W.view(np.uint32)
+    for k in range(2):
+        bits[np.arange(experts), at[:, k]] ^= rng.integers(0, 2, experts).astype(np.uint32) << 16
+    X *= 2.0 ** -np.round(np.log2(np.sqrt(cols)))
+    b = (rng.integers(0, 3, experts) * 0.25).astype(np.float32) if bias else None
+    got = dq.moe_route(_tensor(X, "bf16"), _tensor(W, "bf16"), top_k, score=score, bias=_tensor(b),
+                       scale=2.0)
+    _check_result(got, X, W, top_k, score, b, True, 2.0)
+
+
+@pytest.mark.parametrize("tokens", [100, 1000, 1030])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_many_tokens_non_finite_and_extreme_values(dq, score, tokens):
+    rng = np.random.default_rng(8)
+    cols, n = 2048, 70
+    W = ref.bf16(rng.standard_normal((n, cols)).astype(np.float32))
+    X = ref.bf16(rng.standard_normal((tokens, cols)).astype(np.float32))
+    X[3], X[4, 7], X[5, 9], X[6] = 0, np.nan, np.inf, X[6] * np.float32(2 ** 100)
+    X[7], X[8], X[9] = X[7] * np.float32(2 ** 124), X[8] * np.float32(2 ** -130), X[9] * np.float32(2 ** 12)
+    X[8] = ref.bf16(X[8])  # subnormal there
+    for change in ("none", "nan", "inf", "huge"):
+        V = W.copy()
+        if change != "none":
+            V[50, 3] = dict(nan=np.nan, inf=-np.inf, huge=np.float32(2 ** 126))[change]
+        print(f"[route] many tokens, {score}, {change}", flush=True)
+        with np.errstate(all="ignore"):
+            got = dq.moe_route(_tensor(X, "bf16"), _tensor(V, "bf16"), 6, score=score)
+            # rows whose sums have several infinities or NaN depend on nothing here: NaN or not is
+            # the definition's in every row, and so are the experts
+            _check_result(got, X, V, 6, score)
+
+
+@pytest.mark.parametrize("tokens", [6, 130, 6600])
 def test_given_arrays_streams_and_graph_replays(dq, tokens):
     import torch
 
