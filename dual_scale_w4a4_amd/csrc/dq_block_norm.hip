@@ -45,29 +45,64 @@ __device__ __forceinline__ void load_ones(const void* p, bool bf, int64_t c, flo
   }
 }
 
-__device__ __forceinline__ float rstd_of(double sum, int64_t n, double eps) {
-  return (float)(1.0 / sqrt(sum / (double)n + eps));
-}
-
-// m = X of 16 channels after the post norm and the gates
-__device__ __forceinline__ void gate16(float (&m)[kNormEpl], bool norm1, float r1,
-                                       const float (&post)[kNormEpl], const float (&gate)[kNormEpl],
-                                       float tg) {
-#pragma unroll
-  for (int k = 0; k < kNormEpl; k++) {
-    if (norm1) m[k] = m[k] * r1 * post[k];
-    m[k] = m[k] * gate[k] * tg;
-  }
-}
-
-// h = rs R + m of 16 channels, rounded to the stream's type
+// v rounded to bf16 (or as it is), stored
 template <bool BF>
-__device__ __forceinline__ void join16(float (&m)[kNormEpl], const float (&r)[kNormEpl], float rs) {
+__device__ __forceinline__ void store_rounded(float (&v)[kNormEpl], void* p, int64_t off, bool act) {
+  if (BF) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    Raw16<true> o;
 #pragma unroll
-  for (int k = 0; k < kNormEpl; k++) {
-    m[k] = r[k] * rs + m[k];
-    if (BF) m[k] = to_bf16(m[k]);
+    for (int k = 0; k < kNormEpl / 2; k++)
+      o.v[k / 4][k % 4] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2 * k], (__bf16)v[2 * k + 1]});
+    if (act)
+#pragma unroll
+      for (int k = 0; k < 2; k++) reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + off)[k] = o.v[k];
+    o.unpack(v);
+  } else if (act) {
+    store16<false>(p, off, v);
   }
+}
+
+// fl32(1 / sqrt(sum / n + eps)): the hardware's approximation (2^-26) and a Newton step in fp64
+// (2^-50), a quarter of the instructions of a square root and a quotient
+__device__ __forceinline__ float rstd_of(double sum, double rn, double eps) {
+  const double v = fma(sum, rn, eps), y = __builtin_amdgcn_rsq(v);
+  const double e = fma(-v * y, y, 1.0);
+  return (float)fma(0.5 * e, y, y);
+}
+
+// The largest |v| of 16 values as bits: above every finite value's for an infinity or a NaN
+__device__ __forceinline__ uint32_t top_bits(const float (&v)[kNormEpl]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int k = 0; k < kNormEpl; k++) m = max(m, f2u(v[k]) & 0x7FFFFFFFu);
+  return m;
+}
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// Sum of squares of 16 values, exact but for the additions. bf16 values whose squares stay in fp32's
+// normal range (or below 2^-150 of the largest) are squared there, exactly (16 bits), and become
+// fp64 values times 2^-896 by a shift of their bits: three instructions each, where the conversion
+// alone costs four times one.
+template <bool BF>
+__device__ __forceinline__ double squares16(const float (&h)[kNormEpl], uint32_t top) {
+  if (BF && top < 0x5F000000u && (top > 0x26800000u || top == 0u)) {  // 2^-50 .. 2^63, or all zero
+    double s[2] = {};
+#pragma unroll
+    for (int k = 0; k < kNormEpl; k++)
+      s[k & 1] += u2d((unsigned long long)(f2u(h[k] * h[k]) >> 3) << 32);
+    return (s[0] + s[1]) * 0x1p896;
+  }
+  return sum_squares(h);
+}
+
+// h = rs R + m of 16 channels, rounded to the stream's type and stored
+template <bool BF>
+__device__ __forceinline__ void join16(float (&m)[kNormEpl], const float (&r)[kNormEpl], float rs,
+                                       void* p, int64_t off, bool act) {
+#pragma unroll
+  for (int k = 0; k < kNormEpl; k++) m[k] = r[k] * rs + m[k];
+  store_rounded<BF>(m, p, off, act);
 }
 
 // n = h r2 w; stores n rounded to x_out's type and returns whether a stored value is not finite
@@ -75,13 +110,13 @@ __device__ __forceinline__ bool norm16(float (&h)[kNormEpl], float r2, const flo
                                        const BlockNormArgs& p, int64_t off, bool act) {
 #pragma unroll
   for (int k = 0; k < kNormEpl; k++) h[k] = h[k] * r2 * w[k];
-  if (!p.xo || !act) return false;
+  if (!p.xo) return false;
   float v[kNormEpl];
 #pragma unroll
-  for (int k = 0; k < kNormEpl; k++) v[k] = p.xobf ? to_bf16(h[k]) : h[k];
-  if (p.xobf) store16<true>(p.xo, off, v);
-  else store16<false>(p.xo, off, v);
-  return any_nonfinite(v);
+  for (int k = 0; k < kNormEpl; k++) v[k] = h[k];
+  if (p.xobf) store_rounded<true>(v, p.xo, off, act);
+  else store_rounded<false>(v, p.xo, off, act);
+  return act && top_bits(v) >= kInfBits;
 }
 
 // A workgroup of up to NW waves has a thread per 16 channels and takes row after row, each array
@@ -128,36 +163,38 @@ __global__ __launch_bounds__(NW * kWave, 4) void k_block_norm(BlockNormArgs p) {
       for (int e = 0; e < 4; e++) x[4 * k + e] = x[4 * k + e] * u2f(u[e]);
     }
   };
+  const double rn = 1.0 / (double)p.n;
   int flags = 0;
   for (; row < p.m; row += gridDim.x) {
     const int64_t off = row * p.n + c, next = row + gridDim.x;
-    const float tg = p.tgate ? p.tgate[row] : 1.0f;
     float h[kNormEpl], r[kNormEpl];
     xr.unpack(h);
-    bool in = any_nonfinite(h);
-    double sum1 = 0.0;
-    if (p.norm1) sum1 = sum_squares(h);
     if (act && next < p.m) xr.load(p.X, next * p.n + c);
+    const uint32_t topx = top_bits(h);
+    double sum1 = 0.0;
     if (p.norm1) {
-      sum1 = block_sum(sum1, red[0], waves);
-      const float r1 = rstd_of(sum1, p.n, p.post_eps);
+      sum1 = block_sum(squares16<BF>(h, topx), red[0], waves);
+      const float r1 = rstd_of(sum1, rn, p.post_eps);
 #pragma unroll
       for (int k = 0; k < kNormEpl; k++) h[k] = h[k] * r1 * post[k];
     }
     if (p.gate) times(h, 0);
+    if (p.tgate) {
+      const float tg = p.tgate[row];
 #pragma unroll
-    for (int k = 0; k < kNormEpl; k++) h[k] = h[k] * tg;
+      for (int k = 0; k < kNormEpl; k++) h[k] = h[k] * tg;
+    }
     rr.unpack(r);
-    in |= any_nonfinite(r);
-    join16<BF>(h, r, p.rs);
-    if (act) store16<BF>(p.h, off, h);
+    join16<BF>(h, r, p.rs, p.h, off, act);
+    const uint32_t toph = top_bits(h);
+    if (toph >= kInfBits) {  // rare: what is not finite in X or R is not in h either
+      if (topx >= kInfBits || top_bits(r) >= kInfBits) flags |= kStNonFinite;
+      else if (act && sum1 <= DBL_MAX) flags |= kStRange;  // else another lane's X, reported there
+    }
     if (act && p.R && next < p.m) rr.load(p.R, next * p.n + c);
-    double sum2 = sum_squares(h);
-    if (in) flags |= kStNonFinite;
-    else if (act && !(sum2 <= DBL_MAX) && sum1 <= DBL_MAX) flags |= kStRange;
-    sum2 = block_sum(sum2, red[1], waves);
+    const double sum2 = block_sum(squares16<BF>(h, toph), red[1], waves);
     // a value of n or x that is not finite, unless the row's h already was not (reported above)
-    bool over = norm16(h, rstd_of(sum2, p.n, p.eps), w, p, off, act);
+    bool over = norm16(h, rstd_of(sum2, rn, p.eps), w, p, off, act);
     if (p.b) times(h, 1);
     over |= quantize16<FMT, G>(h, act, p, off, q);
     if (over && sum2 <= DBL_MAX) flags |= kStRange;
@@ -176,31 +213,36 @@ __global__ __launch_bounds__(kBlock) void k_block_norm_wide(BlockNormArgs p) {
     for (int64_t c = threadIdx.x * kNormEpl; c < p.n; c += kBlock * kNormEpl) {
       float x[kNormEpl];
       load16<BF>(p.X, row + c, x);
-      sum1 += sum_squares(x);
+      sum1 += squares16<BF>(x, top_bits(x));
     }
     sum1 = block_sum(sum1, red[0], kWaves);
   }
-  const float r1 = rstd_of(sum1, p.n, p.post_eps), tg = p.tgate ? p.tgate[blockIdx.x] : 1.0f;
+  const double rn = 1.0 / (double)p.n;
+  const float r1 = rstd_of(sum1, rn, p.post_eps), tg = p.tgate ? p.tgate[blockIdx.x] : 1.0f;
   for (int64_t c = threadIdx.x * kNormEpl; c < p.n; c += kBlock * kNormEpl) {
-    float h[kNormEpl], r[kNormEpl] = {}, post[kNormEpl], gate[kNormEpl];
+    float h[kNormEpl], r[kNormEpl] = {}, v[kNormEpl];
     load16<BF>(p.X, row + c, h);
-    bool in = any_nonfinite(h);
+    bool in = top_bits(h) >= kInfBits;
     if (p.R) {
       load16<BF>(p.R, row + c, r);
-      in |= any_nonfinite(r);
+      in |= top_bits(r) >= kInfBits;
     }
-    load_ones(p.post, p.wbf, c, post);
-    load_ones(p.gate, false, c, gate);
-    gate16(h, p.norm1, r1, post, gate, tg);
-    join16<BF>(h, r, p.rs);
-    store16<BF>(p.h, row + c, h);
-    const double s = sum_squares(h);
+    if (p.norm1) {
+      load_ones(p.post, p.wbf, c, v);
+#pragma unroll
+      for (int k = 0; k < kNormEpl; k++) h[k] = h[k] * r1 * v[k];
+    }
+    load_ones(p.gate, false, c, v);
+#pragma unroll
+    for (int k = 0; k < kNormEpl; k++) h[k] = h[k] * v[k] * tg;
+    join16<BF>(h, r, p.rs, p.h, row + c, true);
+    const uint32_t top = top_bits(h);
     if (in) flags |= kStNonFinite;
-    else if (!(s <= DBL_MAX) && sum1 <= DBL_MAX) flags |= kStRange;
-    sum2 += s;
+    else if (top >= kInfBits && sum1 <= DBL_MAX) flags |= kStRange;
+    sum2 += squares16<BF>(h, top);
   }
   sum2 = block_sum(sum2, red[1], kWaves);
-  const float r2 = rstd_of(sum2, p.n, p.eps);
+  const float r2 = rstd_of(sum2, rn, p.eps);
   const QuantConst q = quant_const(p.g);
   // every lane of a wave runs the same trips (the group maxima exchange lanes); lanes past the
   // row's end read its start and store nothing

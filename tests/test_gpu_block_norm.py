@@ -146,6 +146,31 @@ def test_rows_of_zeros_and_extreme_values(dq, oracle_lib):
             _check(dq, oracle_lib, c, fmt, post_norm=post_norm, xdt="f32")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [1024, 16416])
+def test_every_magnitude(dq, oracle_lib, dtype, cols):
+    # rows, and parts of rows, of every magnitude, around those where squares leave fp32's range
+    powers = [-140, -126, -100, -76, -75, -64, -63, -52, -51, -50, -49, -20, 0, 30, 61, 62, 63, 64, 100, 120]
+    rng = np.random.default_rng(cols)
+    X = rng.standard_normal((len(powers), cols)) * np.exp2(np.array(powers, float))[:, None]
+    X[3, ::7] *= 2.0 ** 40
+    X[12, 100:300] *= 2.0 ** -90
+    X[14, 5] *= 2.0 ** 50
+    R = rng.standard_normal((len(powers), cols)) * np.exp2(np.array(powers[::-1], float))[:, None]
+    R[5:9] = 0
+    c = dict(_case(len(powers), cols, dtype, 3), X=layer_ref.rounded(X.astype(np.float32), dtype),
+             R=layer_ref.rounded(R.astype(np.float32), dtype))
+    for post_norm in (True, False):
+        for eps in (1e-5, 1e-75):  # 1 / sqrt(eps) has to fit fp32, where the definition rounds it to
+            _check(dq, oracle_lib, c, "mxfp8", post_norm=post_norm, xdt="f32", eps=eps, post_eps=eps)
+
+
+def test_many_rows(dq, oracle_lib):
+    # a wrong last bit of either root shows in some row
+    for dtype, cols in (("bf16", 512), ("f32", 352)):
+        _check(dq, oracle_lib, _case(20000, cols, dtype, 9), "mxfp8", xdt="f32")
+
+
 @pytest.mark.parametrize("cols", [544, 2080, 16416])
 @pytest.mark.parametrize("post_norm", [True, False])
 def test_errors_are_reported_and_other_rows_are_right(dq, cols, post_norm):
