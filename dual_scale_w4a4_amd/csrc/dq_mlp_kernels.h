@@ -468,7 +468,7 @@ __device__ __forceinline__ const uint16_t* parts_of(const Adapters& x, int t0) {
 // (up to kSliceTokens tokens, which no tile kernel takes). Columns of tokens without an adapter
 // hold anything.
 template <int NP, bool SUM>
-__device__ __forceinline__ void load_u(const Adapters& x, int t0, int tokens, float scale, int j0,
+__device__ __forceinline__ void load_u(const Adapters& x, int t0, int tokens, int id, int j0,
                                        bf16x8 (&part)[NP]) {
   const int lane = threadIdx.x & 63;
   if (!SUM || x.parts) {
@@ -479,6 +479,7 @@ __device__ __forceinline__ void load_u(const Adapters& x, int t0, int tokens, fl
   }
   const int t = min(t0 + (lane & 31), tokens - 1), j = j0 + 8 * (lane >> 5);
   const float* at = x.u + (int64_t)t * x.rank + j;
+  const float scale = x.scale && id >= 0 ? x.scale[id] : 1.0f;
   f32x4 w[kMaxSlices][2], v[2] = {};
 #pragma unroll
   for (int s = 0; s < kMaxSlices; s++)
@@ -499,36 +500,45 @@ __device__ __forceinline__ void load_u(const Adapters& x, int t0, int tokens, fl
   }
 }
 
-// The distinct adapters of 32 tokens in order of their first token, those numbered first, first +
-// step, .., up to T at a time with their rows of B (M blocks of 32 channels, 16 rank values).
+// The adapters' work on 32 tokens: units of one distinct adapter (in order of their first token) and
+// 16 rank values, numbered adapter by adapter; those numbered first, first + step, .. are taken, up
+// to T of the same rank values at a time, with their rows of B (M blocks of 32 channels).
 template <int M, int T>
 struct AdapterWalk {
   int id;              // this lane's token's adapter
-  uint32_t all, left;  // tokens with an adapter; with one not taken yet
-  int q, r[T];
+  uint32_t all, left;  // tokens with an adapter; with one not looked at yet for these rank values
+  int q, j0, first, step, r[T];
   bf16x8 b[T][M];
 
-  __device__ __forceinline__ void start(const Adapters& x, int t0, int tokens) {
+  __device__ __forceinline__ void start(const Adapters& x, int t0, int tokens, int first_, int step_) {
     id = adapter_of(x, t0 + (threadIdx.x & 31), tokens);
-    all = (uint32_t)__ballot(id >= 0);  // the halves agree
-    again();
+    all = left = (uint32_t)__ballot(id >= 0);  // the halves agree
+    q = j0 = 0;
+    first = first_;
+    step = step_;
+    r[0] = -1;
   }
-  __device__ __forceinline__ void again() {
-    left = all;
-    q = 0;
-  }
-  __device__ __forceinline__ void next(const Adapters& x, int rb0, int out, int j0, int first, int step) {
-    const int rl = threadIdx.x & 31, j = j0 + 8 * ((threadIdx.x & 63) >> 5);
+  // the next units, if there are any (r[0] >= 0)
+  __device__ __forceinline__ void next(const Adapters& x, int rb0, int out) {
+    const int steps = (x.rank + 15) / 16;
+    for (;;) {
 #pragma unroll
-    for (int g = 0; g < T; g++) {
-      r[g] = -1;
-      while (left && r[g] < 0) {
-        const int one = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-        left &= ~(uint32_t)__ballot(id == one);
-        if (q % step == first) r[g] = one;
-        q++;
+      for (int g = 0; g < T; g++) {
+        r[g] = -1;
+        while (left && r[g] < 0) {
+          const int one = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+          left &= ~(uint32_t)__ballot(id == one);
+          if ((q * steps + j0 / 16) % step == first) r[g] = one;
+          q++;
+        }
       }
+      if (r[0] >= 0) break;
+      if (j0 + 16 >= x.rank || !all) return;
+      j0 += 16;
+      left = all;
+      q = 0;
     }
+    const int rl = threadIdx.x & 31, j = j0 + 8 * ((threadIdx.x & 63) >> 5);
 #pragma unroll
     for (int g = 0; g < T; g++)
       if (r[g] >= 0)
@@ -538,61 +548,62 @@ struct AdapterWalk {
 };
 
 // Adds the adapters' part to the sums of M blocks of 32 channels (from row block rb0 on) of the 32
-// tokens from t0 on (matrix results; lane: token lane % 32), adapter by adapter of `walk`, whose first
-// step has been taken. Each is a product of B's rows with the rank values of all 32 tokens, of which
-// its own tokens keep theirs: columns do not mix, so a NaN or an infinity in one adapter reaches no
-// other's tokens. B's rows of the next T adapters are loaded meanwhile.
+// tokens from t0 on (matrix results; lane: token lane % 32): the units of `walk`, whose first step has
+// been taken, `part` its rank values. Each is a product of B's rows with the rank values of all 32
+// tokens, of which its own tokens keep theirs: columns do not mix, so a NaN or an infinity in one
+// adapter reaches no other's tokens. The next units' rows are loaded meanwhile.
 template <int OUT, int M, bool SUM, int T>
-__device__ __forceinline__ void adapter_blocks(const Adapters& x, AdapterWalk<M, T>& walk, int t0,
-                                               int tokens, int rb0, int out, int first, int step,
-                                               v16f (&sum)[M]) {
+__device__ __forceinline__ void adapter_blocks(const Adapters& x, AdapterWalk<M, T>& walk,
+                                               bf16x8 (&part)[kParts<OUT>], int t0, int tokens, int rb0,
+                                               int out, v16f (&sum)[M]) {
   constexpr int NP = kParts<OUT>;
-  if (!walk.all) return;
   const int id = walk.id;
-  const float scale = SUM && !x.parts && x.scale && id >= 0 ? x.scale[id] : 1.0f;
-  for (int j0 = 0; j0 < x.rank; j0 += 16) {
-    bf16x8 part[NP];
-    load_u<NP, SUM>(x, t0, tokens, scale, j0, part);
-    if (j0) {
-      walk.again();
-      walk.next(x, rb0, out, j0, first, step);
+  int loaded = walk.j0;
+  while (walk.r[0] >= 0) {
+    const AdapterWalk<M, T> now = walk;
+    walk.next(x, rb0, out);
+    if (now.j0 != loaded) {
+      load_u<NP, SUM>(x, t0, tokens, id, now.j0, part);
+      loaded = now.j0;
     }
-    while (walk.r[0] >= 0) {
-      AdapterWalk<M, T> now = walk;
-      walk.next(x, rb0, out, j0, first, step);
 #pragma unroll
-      for (int g = 0; g < T; g++)
-        if (now.r[g] >= 0)
+    for (int g = 0; g < T; g++)
+      if (now.r[g] >= 0)
 #pragma unroll
-          for (int m = 0; m < M; m++) {
-            v16f d = sum[m];
+        for (int m = 0; m < M; m++) {
+          v16f d = sum[m];
 #pragma unroll
-            for (int k = 0; k < NP; k++)
-              d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now.b[g][m], part[k], d, 0, 0, 0);
+          for (int k = 0; k < NP; k++)
+            d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now.b[g][m], part[k], d, 0, 0, 0);
 #pragma unroll
-            for (int v = 0; v < 16; v++) sum[m][v] = id == now.r[g] ? d[v] : sum[m][v];
-          }
-    }
+          for (int v = 0; v < 16; v++) sum[m][v] = id == now.r[g] ? d[v] : sum[m][v];
+        }
   }
 }
 
-// acc times a_i for a wave's M row blocks and NB blocks of 32 tokens
-template <int M, int NB>
-__device__ __forceinline__ void times_a(const MlpArgs& p, int rb0, v16f (&acc)[M][NB]) {
-  if (!p.a[0]) return;
-  const int h = (threadIdx.x & 63) >> 5;
+// a_i of a wave's M row blocks, as matrix results lie, and the sums of NB blocks of tokens times it
+template <int M>
+struct RowScales {
+  f32x4 a[M][4];
+
+  __device__ __forceinline__ void load(const MlpArgs& p, int rb0) {
+    const int h = (threadIdx.x & 63) >> 5;
 #pragma unroll
-  for (int m = 0; m < M; m++) {
-    f32x4 a[4];
+    for (int m = 0; m < M; m++)
 #pragma unroll
-    for (int g = 0; g < 4; g++)
-      a[g] = load_channels(p.a[0], (rb0 + m) * 32 + g * 8 + h * 4, p.out, 1.0f);
-#pragma unroll
-    for (int n = 0; n < NB; n++)
-#pragma unroll
-      for (int v = 0; v < 16; v++) acc[m][n][v] = acc[m][n][v] * a[v / 4][v % 4];
+      for (int g = 0; g < 4; g++)
+        a[m][g] = load_channels(p.a[0], (rb0 + m) * 32 + g * 8 + h * 4, p.out, 1.0f);
   }
-}
+  template <int NB>
+  __device__ __forceinline__ void apply(v16f (&acc)[M][NB]) const {
+#pragma unroll
+    for (int m = 0; m < M; m++)
+#pragma unroll
+      for (int n = 0; n < NB; n++)
+#pragma unroll
+        for (int v = 0; v < 16; v++) acc[m][n][v] = acc[m][n][v] * a[m][v / 4][v % 4];
+  }
+};
 
 // The tile kernel's sums become a_i s plus the adapters' part. A block of 32 tokens with one adapter
 // takes its products straight onto the sums: B's rows go through LDS (`region`, 8 KiB of the wave's own),
@@ -606,7 +617,11 @@ __device__ __forceinline__ void adapter_tile(const MlpArgs& p, const Adapters& x
   constexpr int NP = kParts<OUT>;
   const int lane = threadIdx.x & 63, rl = lane & 31, h = lane >> 5;
   __builtin_amdgcn_sched_barrier(0);
-  times_a<2, NB>(p, rb0, acc);
+  if (p.a[0]) {
+    RowScales<2> a;
+    a.load(p, rb0);
+    a.template apply<NB>(acc);
+  }
   __builtin_amdgcn_sched_barrier(0);
   constexpr int kMixed = -2;
   int one[NB];  // each block's adapter, -1 for none
@@ -633,7 +648,7 @@ __device__ __forceinline__ void adapter_tile(const MlpArgs& p, const Adapters& x
     auto load = [&](int n, bf16x8 (&f)[4][NP]) {
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        if (i < steps) load_u<NP, false>(x, t0 + n * 32, p.tokens, 1.0f, j0 + 16 * i, f[i]);
+        if (i < steps) load_u<NP, false>(x, t0 + n * 32, p.tokens, 0, j0 + 16 * i, f[i]);
     };
     int staged = -1;
     if (one[0] >= 0) load(0, u[0]);
@@ -679,10 +694,12 @@ __device__ __forceinline__ void adapter_tile(const MlpArgs& p, const Adapters& x
 #pragma unroll
     for (int m = 0; m < 2; m++) {
       AdapterWalk<1, 2> walk;
-      walk.start(x, t0 + n * 32, p.tokens);
-      walk.next(x, rb0 + m, p.out, 0, 0, 1);
+      walk.start(x, t0 + n * 32, p.tokens, 0, 1);
+      walk.next(x, rb0 + m, p.out);
+      bf16x8 part[NP];
+      load_u<NP, false>(x, t0 + n * 32, p.tokens, walk.id, 0, part);
       v16f d[1] = {acc[m][n]};
-      adapter_blocks<OUT, 1, false, 2>(x, walk, t0 + n * 32, p.tokens, rb0 + m, p.out, 0, 1, d);
+      adapter_blocks<OUT, 1, false, 2>(x, walk, part, t0 + n * 32, p.tokens, rb0 + m, p.out, d);
       acc[m][n] = d[0];
       __builtin_amdgcn_sched_barrier(0);  // one block's registers at a time
     }
@@ -869,13 +886,21 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p, X x) {
       load(std::integral_constant<int, J + 2 - PER>{}, q + W, par ^ 1, f);
     __builtin_amdgcn_sched_barrier(0);
   };
-  // the first adapters of the first tokens are found, and their rows of B loaded, before the loop
-  AdapterWalk<M, 4> walk;
-  if constexpr (kAdapters<X>) walk.start(x, t0, p.tokens);
+  // adapters: the first units of the first tokens are found, their operands and a_i loaded, while the
+  // loop's first loads are on their way
+  constexpr int NP = kParts<OUT>;
+  AdapterWalk<M, M == 1 ? 8 : 4> walk;
+  bf16x8 ranks[NP];
+  RowScales<M> scales;
+  if constexpr (kAdapters<X>) walk.start(x, t0, p.tokens, wave, W);
   load(std::integral_constant<int, 0>{}, wave, 0, f0);
   __builtin_amdgcn_sched_barrier(0);
   load(std::integral_constant<int, 1>{}, wave, 0, f1);
-  if constexpr (kAdapters<X>) walk.next(x, rb0, p.out, 0, wave, W);
+  if constexpr (kAdapters<X>) {
+    walk.next(x, rb0, p.out);
+    load_u<NP, NB == 1>(x, t0, p.tokens, walk.id, walk.j0, ranks);
+    scales.load(p, rb0);
+  }
   for (int q = wave, par = 0; q < nper; q += W, par ^= 1) {
     stage(std::integral_constant<int, 0>{}, q, par);
     stage(std::integral_constant<int, 1>{}, q, par);
@@ -888,19 +913,21 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p, X x) {
   // reuses that memory
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
 
-  // adapters: this wave's share of them, joined with its share of k
+  // adapters: this wave's share of them, joined with its share of k; the blocks' units begin at
+  // different waves, since most blocks have few
   if constexpr (kAdapters<X>) {
-    times_a<M, NB>(p, rb0, acc);
+    scales.template apply<NB>(acc);
 #pragma unroll
     for (int n = 0; n < NB; n++) {
       v16f d[M];
 #pragma unroll
       for (int m = 0; m < M; m++) d[m] = acc[m][n];
       if (n) {
-        walk.start(x, t0 + n * 32, p.tokens);
-        walk.next(x, rb0, p.out, 0, wave, W);
+        walk.start(x, t0 + n * 32, p.tokens, (wave + n * W / NB) % W, W);
+        walk.next(x, rb0, p.out);
+        load_u<NP, NB == 1>(x, t0 + n * 32, p.tokens, walk.id, walk.j0, ranks);
       }
-      adapter_blocks<OUT, M, NB == 1>(x, walk, t0 + n * 32, p.tokens, rb0, p.out, wave, W, d);
+      adapter_blocks<OUT, M, NB == 1>(x, walk, ranks, t0 + n * 32, p.tokens, rb0, p.out, d);
 #pragma unroll
       for (int m = 0; m < M; m++) acc[m][n] = d[m];
     }
