@@ -154,29 +154,39 @@ bool moe_sizes(int64_t tokens, int64_t K, int64_t inner, int64_t out, int64_t ex
          out <= kMost && experts >= 1 && experts <= kMaxExperts && top_k >= 1 && top_k <= kMaxTopK;
 }
 
-// Which kernel, by the mean number of rows of the experts that can have any. Measured, us, gated and
-// down product, MXFP4 then MXFP8 between them:
-//   experts, top k, K -> inner, tokens (mean)   split, 32 rows   tile, 64 rows   tile, 128 rows
-//   64, 8, 4096 -> 1536, 24 (3)                 65 + 51          81 + 54         85 + 63
-//   32, 4, 4096 -> 1536, 128 (16)               50 + 40          49 + 40         50 + 44
-//   8, 2, 4096 -> 4096, 100 (25)                37 + 25          33 + 32         35 + 37
-//   64, 8, 2048 -> 1024, 300 (37)               48 + 44          44 + 32         42 + 37
-//   32, 4, 4096 -> 1536, 700 (87)               84 + 84          69 + 58         75 + 58
-//   64, 8, 2048 -> 1024, 3000 (375)             249 + 244        115 + 106       94 + 102
+// Which kernel: the tile kernel, of 64 rows of an expert or 128, where an expert has a few rows and
+// there are tiles for the whole chip, or many rows; else tiles of 32 rows with k split over the waves.
+// Measured, us, gated and down product (number of workgroups of the 64-row tiles), MXFP4 then MXFP8:
+//   experts, top k, K -> inner, tokens (mean rows)   split, 32 rows   tiles of 64             of 128
+//   64, 8, 2048 -> 1024, 32 (4)                      63 in all        51 in all
+//   64, 8, 4096 -> 1536, 24 (3)                      119 in all       114 in all
+//   8, 2, 4096 -> 14336, 16 (4)                      126 in all       136 in all
+//   64, 8, 4096 -> 1536, 40 (5)                      79 + 58          72 (828) + 46 (1104)
+//   64, 8, 2048 -> 1024, 60 (7)                      40 + 31          31 (568) + 21 (568)
+//   8, 2, 4096 -> 4096, 32 (8)                       29 + 17          30 (288) + 30 (144)
+//   32, 4, 4096 -> 1536, 64 (8)                      42 + 33          44 (432) + 24 (576)
+//   32, 4, 4096 -> 1536, 128 (16)                    51 + 40          48 (480) + 29 (640)     51 + 32
+//   8, 2, 4096 -> 4096, 100 (25)                     37 + 25          33 (352) + 32 (176)     35 + 37
+//   32, 4, 4096 -> 1536, 700 (87)                    83 + 84          65 (900) + 47 (1200)    56 + 57
+//   32, 4, 4096 -> 1536, 1000 (125)                  105 + 109        73 (1128) + 62 (1504)   77 + 62
+//   8, 2, 4096 -> 14336, 600 (150)                   360 + 186        168 (2912) + 130 (416)  146 + 117
+//   64, 8, 2048 -> 1024, 3000 (375)                  249 + 246        103 (3512) + 106 (3512) 93 + 102
 template <bool ACT8, bool GATED, int OUT>
 hipError_t launch_experts(const MlpArgs& p, Experts x, hipStream_t s) {
+  constexpr int kRows = GATED ? 128 : 256;
   const int used = std::min(x.pairs, x.experts), mean = x.pairs / used;
   auto slots = [&](int tile) { return used + x.pairs / tile; };
-  if (mean <= 24) {
-    x.slots = slots(32);
-    return launch_split<ACT8, GATED, OUT, 2, 1>(p, x, s);
+  if (mean > 128) {
+    x.slots = slots(128);
+    return launch_tile<ACT8, GATED, OUT, 4>(p, x, s);
   }
-  if (mean <= 128) {
+  const int64_t tiles = (int64_t)slots(64) * ((p.out + kRows - 1) / kRows);
+  if (mean >= 40 || (mean >= 3 && tiles >= 340)) {
     x.slots = slots(64);
     return launch_tile<ACT8, GATED, OUT, 2>(p, x, s);
   }
-  x.slots = slots(128);
-  return launch_tile<ACT8, GATED, OUT, 4>(p, x, s);
+  x.slots = slots(32);
+  return launch_split<ACT8, GATED, OUT, 2, 1>(p, x, s);
 }
 
 }  // namespace dqm

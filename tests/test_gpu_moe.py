@@ -94,13 +94,14 @@ def _check(dq, L, xc, xs, ids, w, act_fmt="mxfp4", mid="mxfp8", dtype="bf16", ki
     return y
 
 
-# tokens, K, inner, out, experts, top_k: one token and many; up to 32 rows an expert on average, up
-# to 64 and beyond; more pairs than a workgroup counts by itself; one expert; more experts than pairs
+# tokens, K, inner, out, experts, top_k: one token and many; every kernel of the selection (tiles of 32
+# rows, of 64 where an expert has 3 rows or more and there are 340 tiles or where it has 40, of 128 from
+# 129 on); more pairs than a workgroup counts by itself; one expert; more experts than pairs
 SHAPES = [(1, 512, 512, 512, 4, 2), (1, 1024, 512, 32, 64, 8), (3, 512, 1024, 96, 5, 3),
           (24, 512, 512, 160, 16, 4), (33, 1536, 512, 64, 2, 1), (40, 512, 512, 64, 3, 2),
           (61, 512, 1536, 288, 2, 2), (90, 512, 512, 64, 3, 2), (130, 1024, 512, 96, 2, 2),
           (200, 512, 512, 352, 1, 1), (300, 512, 512, 64, 12, 4), (700, 512, 512, 96, 6, 3),
-          (45, 512, 512, 64, 40, 30)]
+          (45, 512, 512, 64, 40, 30), (200, 512, 1024, 1312, 64, 2), (130, 512, 1536, 1504, 32, 5)]
 
 
 @pytest.mark.parametrize("tokens,K,inner,out,n,top_k", SHAPES)
