@@ -164,7 +164,8 @@ __global__ __launch_bounds__(NW * kWave, 4) void k_block_norm(BlockNormArgs p) {
     }
   };
   const double rn = 1.0 / (double)p.n;
-  int flags = 0;
+  int flags = 0, turn = 0;  // the sums take the two arrays in turn: one barrier lies between a read
+                            // of an array and its next use
   for (; row < p.m; row += gridDim.x) {
     const int64_t off = row * p.n + c, next = row + gridDim.x;
     float h[kNormEpl], r[kNormEpl];
@@ -173,7 +174,8 @@ __global__ __launch_bounds__(NW * kWave, 4) void k_block_norm(BlockNormArgs p) {
     const uint32_t topx = top_bits(h);
     double sum1 = 0.0;
     if (p.norm1) {
-      sum1 = block_sum(squares16<BF>(h, topx), red[0], waves);
+      sum1 = block_sum(squares16<BF>(h, topx), red[turn], waves);
+      turn ^= 1;
       const float r1 = rstd_of(sum1, rn, p.post_eps);
 #pragma unroll
       for (int k = 0; k < kNormEpl; k++) h[k] = h[k] * r1 * post[k];
@@ -192,7 +194,8 @@ __global__ __launch_bounds__(NW * kWave, 4) void k_block_norm(BlockNormArgs p) {
       else if (act && sum1 <= DBL_MAX) flags |= kStRange;  // else another lane's X, reported there
     }
     if (act && p.R && next < p.m) rr.load(p.R, next * p.n + c);
-    const double sum2 = block_sum(squares16<BF>(h, toph), red[1], waves);
+    const double sum2 = block_sum(squares16<BF>(h, toph), red[turn], waves);
+    turn ^= 1;
     // a value of n or x that is not finite, unless the row's h already was not (reported above)
     bool over = norm16(h, rstd_of(sum2, rn, p.eps), w, p, off, act);
     if (p.b) times(h, 1);
