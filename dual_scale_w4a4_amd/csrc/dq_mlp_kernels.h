@@ -267,6 +267,34 @@ __device__ __forceinline__ v16f mfma(const u32x4& a, const u32x4* b, v16f c, uin
   }
 }
 
+// E4M3 codes of at least 4 in magnitude, and the others: b = hi + lo, zeros in each other's places.
+// With a run's products all of one kind the truncation leaves them whole: those of hi are multiples
+// of 2^-2 (times the scales) and at most 2688, 2^-2 being 2^-13 of 2^11; those of lo are multiples of
+// 2^-10 below 24, which loses at most their last bit, 2^-21 of a group's largest value.
+__device__ __forceinline__ void split_codes(const u32x4& b, u32x4& hi, u32x4& lo) {
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const uint32_t t = ((b[k] & 0x7F7F7F7Fu) + 0x38383838u) & 0x80808080u;  // 0x48 is 4
+    hi[k] = b[k] & (t | (t - (t >> 7)));
+    lo[k] = b[k] ^ hi[k];
+  }
+}
+
+// One step's products; WHOLE: E4M3 activations in two parts, so that they are not truncated
+template <bool ACT8, bool WHOLE>
+__device__ __forceinline__ v16f products_of(const u32x4& a, const u32x4 (&b)[ACT8 ? 2 : 1], v16f c,
+                                            uint32_t sa, uint32_t sb, int step) {
+  if constexpr (WHOLE) {
+    u32x4 hi[2], lo[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++) split_codes(b[e], hi[e], lo[e]);
+    c = mfma<ACT8>(a, hi, c, sa, sb, step);
+    return mfma<ACT8>(a, lo, c, sa, sb, step);
+  } else {
+    return mfma<ACT8>(a, b, c, sa, sb, step);
+  }
+}
+
 // ------------------------------------------------------------------- what a call adds
 
 struct Plain {};
@@ -422,6 +450,12 @@ template <class X>
 constexpr bool kExperts = std::is_same<X, Experts>::value;
 template <class X>
 constexpr bool kAdapters = std::is_same<X, Adapters>::value;
+
+// Where a sum's truncation would be seen: a value near a border of the quantizer changes its code, so
+// that an error of 10^-4 of a sum becomes one of 6 10^-3 of what the codes are multiplied into (K 4096,
+// outlier channels). The dense gated product (dq_mlp.h) documents that instead.
+template <bool ACT8, int OUT, class X>
+constexpr bool kWhole = ACT8 && OUT >= kOutFp4 && kExperts<X>;
 
 __device__ __forceinline__ const float* shifted(const float* p, int64_t by) { return p ? p + by : p; }
 
@@ -863,8 +897,9 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p, X x) {
       if (k + kAhead < F) read(k + kAhead);
 #pragma unroll
       for (int m = 0; m < M; m++)
-        acc[m][k % NB] = mfma<ACT8>(f.a[m][k / NB], b[k % 4], acc[m][k % NB], f.sa[m], sx[k % NB],
-                                    ACT8 ? 2 * HS + k / NB : k / NB);
+        acc[m][k % NB] = products_of<ACT8, kWhole<ACT8, OUT, X>>(
+            f.a[m][k / NB], b[k % 4], acc[m][k % NB], f.sa[m], sx[k % NB],
+            ACT8 ? 2 * HS + k / NB : k / NB);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -1052,7 +1087,7 @@ __device__ __forceinline__ uint32_t load_ws(const TileCtx<ACT8, NB>& c, int m, i
 // wave. It also stands between the last reads of a token buffer, whose products every wave has
 // issued a stage before, and the loads that fill the buffer again: with four buffers stage
 // s + 1 loads into the one that stage s - 1 read.
-template <bool ACT8, int NB, int KS, int HS, bool XS>
+template <bool ACT8, int NB, int KS, int HS, bool XS, bool WHOLE>
 __device__ __forceinline__ void tile_step(v16f (&acc)[2][NB], u32x4 (&fa)[2][steps(ACT8)],
                                           u32x4 (&fb)[4][ACT8 ? 2 : 1], uint32_t (&sw)[2],
                                           const uint32_t (&sx)[NB], uint32_t (&sn)[NB],
@@ -1082,7 +1117,8 @@ __device__ __forceinline__ void tile_step(v16f (&acc)[2][NB], u32x4 (&fa)[2][ste
     }
 #pragma unroll
     for (int m = 0; m < 2; m++) {
-      acc[m][n] = mfma<ACT8>(fa[m][KS], fb[i % 4], acc[m][n], sw[m], sx[n], ACT8 ? 2 * HS + KS : KS);
+      acc[m][n] = products_of<ACT8, WHOLE>(fa[m][KS], fb[i % 4], acc[m][n], sw[m], sx[n],
+                                           ACT8 ? 2 * HS + KS : KS);
       if (XS && KS == 0 && n == 0 && m == 0) load_xs(c, xsb, q, xs_on);
       if (KS == 0 && m == 0) load_x(c, xb, n, s2, on);
       if (ACT8 || m == 0)
@@ -1453,8 +1489,8 @@ __global__ __launch_bounds__(256, 2) void k_mlp_tile(MlpArgs p, int nti, int ntt
     uint8_t* xsb = L.xs[(q + 1) & 1];
     auto step = [&](auto kc) {
       constexpr int KS = decltype(kc)::value;
-      tile_step<ACT8, NB, KS, P, XS>(acc, fa[P], fb, sw[P], sx[P], sx[P ^ 1], lx, lxn, xsn, xt, c,
-                                     xb, xsb, s, q + 1, more);
+      tile_step<ACT8, NB, KS, P, XS, kWhole<ACT8, OUT, X>>(
+          acc, fa[P], fb, sw[P], sx[P], sx[P ^ 1], lx, lxn, xsn, xt, c, xb, xsb, s, q + 1, more);
     };
     step(std::integral_constant<int, 0>{});
     step(std::integral_constant<int, 1>{});

@@ -118,8 +118,10 @@ dq_status dq_moe_route(const void* X, dq_dtype xt, int64_t tokens, int64_t cols,
  *     H  = act(a_gate_ei * sum_k x^ Qgate_e) * (a_up_ei * sum_k x^ Qup_e),  e = ids[t][s]
  *     q  = the quantizer's values of fl32(H * b_e) in groups of 32 channels (inner_fmt)
  *     Y[t][i] = residual[t][i] + sum_s weights[t][s] * (a_down_ei * sum_j q_j Qdown_e)
- * products as dq_gated_mx_quantized and dq_gemm_mx_epilogue compute them, the sum over s in fp32 in
- * ascending order, residual last, one rounding to Y's type.
+ * products as dq_gated_mx_quantized and dq_gemm_mx_epilogue compute them, except that MXFP8
+ * activations are multiplied in two parts (codes of at least 4, and the others), which leaves the
+ * gate's and up products whole: truncated sums would change codes near a border (up to 6 10^-3 of Y).
+ * The sum over s in fp32 in ascending order, residual last, one rounding to Y's type.
  *  act_codes, act_scales, act_fmt, K: the activations, as for dq_gated_mx.
  *  ids:          tokens x top_k experts (4-byte aligned), in any order; a value outside
  *                0 .. experts - 1 contributes nothing; an expert named twice counts twice.

@@ -130,6 +130,41 @@ def test_activations_and_optional_arrays(dq, kind, tokens):
         _check(dq, L, xc, xs, ids, w, kind=kind, sample=40)
 
 
+@pytest.mark.parametrize("tokens,n,top_k", [(3, 6, 2), (60, 2, 1), (300, 2, 2), (130, 64, 6)])
+def test_8_bit_sums_are_whole(dq, tokens, n, top_k):
+    # the values between the products show in what the down product makes of them: identity-like down
+    # weights hand on one channel each, so a code that a truncated sum changed would be seen, step by
+    # step. Outlier channels make the truncation of whole runs as large as it gets.
+    K, inner, out = 2048, 512, 512
+    rng = np.random.default_rng(tokens)
+    x = rng.standard_normal((tokens, K))
+    x[:, rng.random(K) < 0.02] *= 30.0
+    xc, xs = ref.mxfp8(x.astype(np.float32), 32)
+    L = _layer(dq, n, K, inner, out, 80, a=False)
+    c, s = np.zeros((n, out, inner // 2), np.uint8), np.full((n, out, inner // 32), 127, np.uint8)
+    for i in range(out):
+        c[:, i, i // 2] = 2 << (4 * (i % 2))  # 1.0
+    L["down"] = (c, s, None)
+    L["dev"]["down"] = _pack(dq, L["down"])
+    ids, _ = _routing(rng, tokens, n, top_k)
+    w = np.zeros((tokens, top_k), np.float32)
+    w[:, 0] = 1.0
+    y = dq.moe_mx(_dev(xc), _dev(xs), _dev(ids), _dev(w), act_fmt="mxfp8", inner_fmt="mxfp4",
+                  activation="relu", **L["dev"])
+    wrong = total = 0
+    for e in np.unique(ids[:, 0]):
+        t = np.nonzero(ids[:, 0] == e)[0]
+        one = lambda v: (v[0][e], v[1][e], None)  # noqa: E731
+        h, dh = layer_ref.gated_whole(xc[t], xs[t], "mxfp8", one(L["gate"]), one(L["up"]), "relu")
+        q, dq_ = layer_ref.quantized(h, dh, "mxfp4")
+        got = _f64(y)[t]
+        assert np.all(np.abs(got - q) <= dq_ + np.abs(q) * 2.0 ** -8)
+        wrong += np.sum(np.abs(got - q) > np.abs(q) * 2.0 ** -8)
+        total += q.size
+    # only sums beside a border between two codes may go the other way
+    assert wrong <= 1e-3 * total, (wrong, total)
+
+
 @pytest.mark.parametrize("tokens", [1, 30, 400])
 def test_ids_out_of_range_twice_and_all_alike(dq, tokens):
     n, K, inner, out, top_k = 5, 512, 512, 96, 4
