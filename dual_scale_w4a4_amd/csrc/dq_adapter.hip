@@ -5,7 +5,14 @@
 //   u[t][j] = sum_k X[t][k] A_r[j][k],  r = adapter[t]
 //
 // Two launches: u (here), then the products of dq_mlp.hip, whose kernels add the adapters' part to
-// their sums (adapter_blocks and adapter_tile in dq_mlp_kernels.h).
+// their sums (adapter_blocks and adapter_tile in dq_mlp_kernels.h). Measured, us, u + product (the
+// product without adapters):
+//   32 sequences, 28 of 40 adapters, rank 16, 14336 -> 4096, bf16       8.3 + 14.5   (9.3)
+//   4096 tokens in runs, 6 adapters, rank 64, 4096 -> 14336, bf16      18.5 + 143-150  (114-124)
+//   515 tokens in runs, 5 adapters, rank 24, 2560 -> 1733, fp32         8.5 + 11.8   (7.8)
+// The first reads 13 MB of A next to 31 MB of weights. In the second u is 2 10^9 multiply-adds on
+// 33 MB of X (1.8 TB/s: 256 workgroups, one a CU, each waiting for its own loads), and B's products
+// are 1/64 of the main ones but at a quarter of their rate and with a third more operands.
 #include "../../include/dq_layer.h"
 #include "dq_mlp_kernels.h"
 
@@ -29,7 +36,7 @@ struct RankArgs {
 //
 // V_MFMA_F32_32X32X16_BF16 takes A's rows as operand A and the tokens as operand B; lane half h takes
 // pieces 2 i + h of 8 values of each row's period, the i-th step's. Loaded straight into such
-// registers every lane would touch a cache line of its own (16 sequences with adapters of rank 16, K
+// registers every lane would touch a cache line of its own (32 sequences, rank 16, K
 // 14336: 29 us); so rows go to a ring of two LDS stages of the wave's own, eight lanes to a line, their
 // pieces XOR-swizzled as the products' tokens are. Rows past the rank, and tokens of other adapters,
 // read zeros through an offset past the buffer.
@@ -167,8 +174,9 @@ __global__ __launch_bounds__(W * 64) void k_adapter_rank(RankArgs p) {
 constexpr int kMaxRank = 256;
 
 // How the rank values' kernel fills the chip: 32 rank values and eight waves a workgroup with few
-// blocks of tokens, 64 and four with many; slots up to the distinct adapters that a block can have;
-// and with one block of tokens k in slices (at least 512 each).
+// blocks of tokens, 64 and four with many (4096 tokens, K 4096: rank 64 17.7 against 20.0 us, rank 128
+// 25.1 against 32.4); slots up to the distinct adapters that a block can have; and with one block of
+// tokens k in slices (at least 512 each).
 struct RankShape {
   int mr, slots, slices;
   size_t bytes;

@@ -7,6 +7,12 @@
 //
 // As for the single norm (dq_norm.hip) codes have to be the definition's bit for bit: one fp32
 // rounding per step, sums of squares and roots in fp64.
+//
+// Memory bounds it: every array moves once, and the rest is kept below that (exact bf16 squares in
+// fp32, roots by Newton steps, packed stores: with fp64 conversions, square roots and quotients
+// 8192 x 4096 took 66 us). 8192 x 4096 bf16 with post norm, gate and x_out to MXFP8: 54 - 55 us for
+// 303 MB, 5.5 TB/s. 1003 x 8160 fp32 with a token gate to MXFP8: 22 us for 107 MB, 4.8 TB/s. One
+// token of 4096: 4.2 us.
 #include <limits.h>
 
 #include "../../include/dq_layer.h"
@@ -63,12 +69,13 @@ __device__ __forceinline__ void store_rounded(float (&v)[kNormEpl], void* p, int
   }
 }
 
-// fl32(1 / sqrt(sum / n + eps)): the hardware's approximation (2^-26) and a Newton step in fp64
-// (2^-50), a quarter of the instructions of a square root and a quotient
+// fl32(1 / sqrt(sum / n + eps)): the hardware's approximation (measured 2^-24.2) and two Newton steps
+// in fp64 (2^-47.7 after one; the second costs nothing that shows), fewer instructions than a square
+// root and a quotient
 __device__ __forceinline__ float rstd_of(double sum, double rn, double eps) {
   const double v = fma(sum, rn, eps), y = __builtin_amdgcn_rsq(v);
-  const double e = fma(-v * y, y, 1.0);
-  return (float)fma(0.5 * e, y, y);
+  const double e = fma(-v * y, y, 1.0), z = fma(0.5 * e, y, y);
+  return (float)fma(0.5 * fma(-v * z, z, 1.0), z, z);
 }
 
 // The largest |v| of 16 values as bits: above every finite value's for an infinity or a NaN
