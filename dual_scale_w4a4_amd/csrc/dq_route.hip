@@ -13,9 +13,10 @@
 // logit with a bound on its error, and the second computes in fp64 the few experts of each token
 // that the bounds leave in question, the chosen ones among them: the same result. Where scores of other
 // experts enter the result (the softmax's sum with a bias or without renormalization), or a value is
-// not finite, that is every expert. That takes 18.2 + 40 us: the bf16 products wait for their operands'
-// way through LDS, and the selection's 8.1 experts a token (8 asked for) are 1.4 10^8 exact products at five vector
-// instructions each. One token, 64 experts: 4.1 + 3.2 us, latency.
+// not finite, that is every expert. That takes 18 + 27 us: the bf16 products wait for their operands'
+// way through LDS; the selection's 8.1 experts a token (8 asked for) are 1.4 10^8 exact products at
+// 4.4 vector instructions each, and about 14 us that do not depend on K. One token, 64 experts: 4.0 + 3.0
+// us, latency.
 #include <float.h>
 #include <limits.h>
 
@@ -275,18 +276,25 @@ struct SelectArgs {
   int cols;
 };
 
+// v of a lane that is the same for the whole wave
+__device__ __forceinline__ double of_lane(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return dq::u2d((uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(u >> 32), lane) << 32 |
+                 (uint32_t)__builtin_amdgcn_readlane((uint32_t)u, lane));
+}
+
 // the largest of the wave's values, none of them NaN
 __device__ __forceinline__ double wave_max(double v) {
   v = fmax(v, dq::dpp_f64<dq::kDppQuadXor1>(v));
   v = fmax(v, dq::dpp_f64<dq::kDppQuadXor2>(v));
   v = fmax(v, dq::dpp_f64<dq::kDppRowHalfMirror>(v));
   v = fmax(v, dq::dpp_f64<dq::kDppRowMirror>(v));
-  return fmax(fmax(__shfl(v, 0, 64), __shfl(v, 16, 64)), fmax(__shfl(v, 32, 64), __shfl(v, 48, 64)));
+  return fmax(fmax(of_lane(v, 0), of_lane(v, 16)), fmax(of_lane(v, 32), of_lane(v, 48)));
 }
 
 __device__ __forceinline__ double wave_add(double v) {
   v = dq::sum16_dpp(v);
-  return ((__shfl(v, 0, 64) + __shfl(v, 16, 64)) + __shfl(v, 32, 64)) + __shfl(v, 48, 64);
+  return ((of_lane(v, 0) + of_lane(v, 16)) + of_lane(v, 32)) + of_lane(v, 48);
 }
 
 // The next of the largest keys among those still free, ties to the lowest index: its index, no longer
@@ -313,21 +321,46 @@ __device__ __forceinline__ int take_largest(const double (&key)[N], bool (&is_fr
 
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
-// The product of two bf16 values, finite, times 2^-896 as fp64. It is exact in fp32 (16 bits; what
-// fp32's range may cut is below 2^-149, and no score tells logits that small from zero), and fp32's
-// exponent field is taken as fp64's: a shift, which loses none of the bits set, where a conversion
-// takes four times as long.
+// The k-th of two bf16 values in a word, finite, times 2^-896 as fp64: its exponent field is taken as
+// fp64's (a subnormal one's too), by a shift that leaves copies of the sign to be masked out. Two or
+// three instructions, where a conversion takes the time of four.
 constexpr int kShift = 896;
-__device__ __forceinline__ double shifted_product(float x, float w) {
-  const uint32_t u = dq::f2u(x * w);
-  return dq::u2d((unsigned long long)((u & 0x80000000u) | ((u & 0x7FFFFFFFu) >> 3)) << 32);
+__device__ __forceinline__ double shifted(uint32_t r, int k) {
+  const uint32_t u = (uint32_t)((int32_t)(k ? r : r << 16) >> 3) & 0x8FFFE000u;
+  return dq::u2d((unsigned long long)u << 32);
 }
 
-// fp64 dot products of a token's row with G experts' rows, in every lane. FINITE: all values are. A
-// wave waits for memory here, so U 512-channel pieces of all rows are loaded at once.
+constexpr int kDppRowRor4 = 0x124, kDppRowRor8 = 0x128;  // lane i from i - 4, i - 8 within each 16 lanes
+
+// The sum over the wave of one of eight values a lane: v[l % 8] in lane l. Halves of the values are
+// exchanged with lane l ^ 1 and l ^ 2, and a lane four away takes the other half (3/4 fewer steps than a
+// sum for each).
+__device__ __forceinline__ double wave_add8(const double (&v)[8]) {
+  const int lane = threadIdx.x & 63;
+  double a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const double keep = lane & 1 ? v[2 * i + 1] : v[2 * i], send = lane & 1 ? v[2 * i] : v[2 * i + 1];
+    a[i] = keep + dq::dpp_f64<dq::kDppQuadXor1>(send);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const double keep = lane & 2 ? a[2 * i + 1] : a[2 * i], send = lane & 2 ? a[2 * i] : a[2 * i + 1];
+    b[i] = keep + dq::dpp_f64<dq::kDppQuadXor2>(send);
+  }
+  const double keep = lane & 4 ? b[1] : b[0], send = lane & 4 ? b[0] : b[1];
+  double s = keep + dq::dpp_f64<kDppRowRor4>(send);
+  s += dq::dpp_f64<kDppRowRor8>(s);
+  s += __shfl_xor(s, 16, 64);
+  return s + __shfl_xor(s, 32, 64);
+}
+
+// fp64 dot products of a token's row with G experts' rows: with 8 that of e[l % 8] in lane l, with
+// fewer the sums in v of every lane. FINITE: all values are. U 512-channel pieces of all rows are
+// loaded at once.
 template <int G, int U, bool FINITE>
-__device__ __forceinline__ void dots(const SelectArgs& p, const uint16_t* x, const int (&e)[G],
-                                     double (&s)[G]) {
+__device__ __forceinline__ double dots(const SelectArgs& p, const uint16_t* x, const int (&e)[G],
+                                       double (&s)[G]) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int g = 0; g < G; g++) s[g] = 0.0;
@@ -342,76 +375,111 @@ __device__ __forceinline__ void dots(const SelectArgs& p, const uint16_t* x, con
       for (int g = 0; g < G; g++)
         wr[u][g] = in ? *reinterpret_cast<const u32x4*>(p.W + (int64_t)e[g] * p.cols + c) : u32x4{};
     }
+    __builtin_amdgcn_sched_barrier(0);  // all of them in flight
     auto value = [](const u32x4& r, int k) { return u2f(k & 1 ? r[k / 2] & 0xFFFF0000u : r[k / 2] << 16); };
 #pragma unroll
     for (int u = 0; u < U; u++)
 #pragma unroll
       for (int k = 0; k < 8; k++) {
-        const float xv = value(xr[u], k);
+        const double xv = FINITE ? shifted(xr[u][k / 2], k & 1) * 0x1p896 : (double)value(xr[u], k);
 #pragma unroll
-        for (int g = 0; g < G; g++) {
-          const float w = value(wr[u][g], k);
-          if (FINITE) s[g] += shifted_product(xv, w);
-          else s[g] = fma((double)xv, (double)w, s[g]);
-        }
+        for (int g = 0; g < G; g++)
+          s[g] = fma(xv, FINITE ? shifted(wr[u][g][k / 2], k & 1) : (double)value(wr[u][g], k), s[g]);
       }
   }
+  if constexpr (G == 8) {
+    const double v = wave_add8(s);
+    return FINITE ? ldexp(v, kShift) : v;
+  } else {
 #pragma unroll
-  for (int g = 0; g < G; g++) {
-    s[g] = wave_add(s[g]);
-    if (FINITE) s[g] = ldexp(s[g], kShift);
+    for (int g = 0; g < G; g++) {
+      s[g] = wave_add(s[g]);
+      if (FINITE) s[g] = ldexp(s[g], kShift);
+    }
+    return 0.0;
   }
 }
 
-// Which experts of the token can be among the top_k, and their exact logits (in l of their lanes).
+// The bits of v in an order of unsigned numbers; a NaN is the largest
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = dq::f2u(v);
+  return v == v ? u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u) : 0xFFFFFFFFu;
+}
+__device__ __forceinline__ float of_order(uint32_t u) {
+  return u2f(u ^ (u >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// The token's experts that can be among the top_k, in ascending order, the j-th in slot j / 64 of lane
+// j % 64: their exact logits and numbers; returns how many.
+//
 // Keys grow with the logits, so an expert whose key at its upper bound lies below the top_k-th
-// largest of the keys at the lower bounds cannot; a margin covers the last bits of exp, where a tie
-// could lie. A bound that is no number leaves its expert in question.
+// largest of the keys at the lower bounds cannot. The keys of the bounds are fp32, widened by more
+// than fp32's roundings and exp's last bits (where fp64 keys can tie): a logit's bound holds
+// 2^-22 of it for three roundings of 2^-24, a score is off by less than 5 10^-7 of itself. A bound
+// that is no number leaves its expert in question.
 // WPT waves share the token's sums and hand them on in LDS.
 template <bool SIGMOID, int N, int WPT>
-__device__ __forceinline__ void recheck(const SelectArgs& p, int64_t t, double (&l)[N],
-                                        bool (&is_free)[N]) {
-  constexpr int G = WPT == 1 ? 4 : 2;
+__device__ __forceinline__ int recheck(const SelectArgs& p, int64_t t, double (&l)[N], int (&id)[N]) {
+  constexpr int G = WPT == 1 ? 8 : 2;
   __shared__ float exact[WPT == 1 ? 1 : 64 * N];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  double lo[N], hi[N];
-  bool open[N], wild = false;
-  double top = -INFINITY;
+  uint32_t lo[N], hi[N];
+  bool wild = false;
+  float top = -INFINITY;
 #pragma unroll
   for (int n = 0; n < N; n++) {
     const int e = n * 64 + lane;
-    open[n] = is_free[n];
-    lo[n] = hi[n] = -INFINITY;
-    if (is_free[n]) {
+    lo[n] = hi[n] = 0u;
+    id[n] = 0;
+    l[n] = -INFINITY;
+    if (e < p.experts) {
       const float2 v = *reinterpret_cast<const float2*>(p.logits + (t * p.experts + e) * 2);
-      lo[n] = (double)v.x - (double)v.y;
-      hi[n] = (double)v.x + (double)v.y;
-      top = fmax(top, hi[n]);
+      float from = v.x - v.y, to = v.x + v.y, slack = 1e-7f;
+      top = fmaxf(top, to);
       wild |= !(fabsf(v.x) + v.y < 1e38f);
       if (SIGMOID) {
-        const double b = p.bias ? (double)p.bias[e] : 0.0;
-        lo[n] = sigmoid64(lo[n]) + b;
-        hi[n] = sigmoid64(hi[n]) + b;
+        const float b = p.bias ? p.bias[e] : 0.0f;
+        from = __builtin_amdgcn_rcpf(1.0f + expf(-from));
+        to = __builtin_amdgcn_rcpf(1.0f + expf(-to));
+        slack = 1e-6f * (to + fabsf(b)) + 1e-37f;
+        from += b;
+        to += b;
       }
-      if (!(lo[n] == lo[n])) lo[n] = -INFINITY;
+      from -= slack;
+      lo[n] = from == from ? ordered(from) : 0u;
+      hi[n] = ordered(to + slack);
     }
   }
-  double kth = -INFINITY;
-  for (int k = 0; k < p.top_k; k++) take_largest<N>(lo, open, kth);
-  kth -= 1e-12 * (1.0 + fabs(kth));
-  // softmax scores that underflow are equal, and one logit that is not finite is in every score
-  if (!SIGMOID && (__any(wild) || !(wave_max(top) - kth < 700.0))) kth = -INFINITY;
+  // the top_k-th largest of lo, bit by bit until the top_k are apart, then the least of them
+  uint32_t kth = 0u;
+  for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
+    int above = 0;
 #pragma unroll
-  for (int n = 0; n < N; n++) is_free[n] = is_free[n] && !(hi[n] < kth);
+    for (int n = 0; n < N; n++) above += __popcll(__ballot(lo[n] >= (kth | bit)));
+    if (above >= p.top_k) kth |= bit;
+    if (above == p.top_k) break;
+  }
+  uint32_t least = 0xFFFFFFFFu;
+#pragma unroll
+  for (int n = 0; n < N; n++)
+    if (lo[n] >= kth) least = min(least, lo[n]);
+  least = min(least, dq::dpp_u32<dq::kDppQuadXor1>(least));
+  least = min(least, dq::dpp_u32<dq::kDppQuadXor2>(least));
+  least = min(least, dq::dpp_u32<dq::kDppRowHalfMirror>(least));
+  least = min(least, dq::dpp_u32<dq::kDppRowMirror>(least));
+  auto row = [&](int i) { return (uint32_t)__builtin_amdgcn_readlane(least, 16 * i); };
+  kth = min(min(row(0), row(1)), min(row(2), row(3)));
+  const bool finite = !__any(wild);
+  // softmax scores that underflow are equal, and one logit that is not finite is in every score
+  if (!SIGMOID && (!finite || __any(!(top - 700.0f < of_order(kth))))) kth = 0u;
   // their sums in fp64, G experts at a time and the last ones singly; a logit's magnitude and bound
   // are not finite where one of its values is not
   const uint16_t* x = p.X + t * p.cols;
-  const bool finite = !__any(wild);
   uint64_t m[N];
   int count = 0;
 #pragma unroll
   for (int n = 0; n < N; n++) {
-    m[n] = __ballot(is_free[n]);
+    m[n] = __ballot(n * 64 + lane < p.experts && hi[n] >= kth);
     count += __popcll(m[n]);
   }
   auto next = [&] {
@@ -422,65 +490,57 @@ __device__ __forceinline__ void recheck(const SelectArgs& p, int64_t t, double (
         e = n * 64 + __builtin_ctzll(m[n]);
         m[n] &= m[n] - 1;
       }
-    count--;
     return e;
   };
-  auto set = [&](int e, double sum) {
-    if (WPT > 1) {
-      if (lane == 0) exact[e] = (float)sum;
-      return;
-    }
-#pragma unroll
-    for (int n = 0; n < N; n++)
-      if (n == e >> 6 && lane == (e & 63)) l[n] = (double)(float)sum;
-  };
-  for (int q = 0; count > 0; q++) {
+  for (int j = 0, q = 0; j < count; q++) {
     const bool mine = WPT == 1 || q % WPT == wave;
-    if (finite && count >= G) {
+    const int width = finite && count - j >= G ? G : 1;
+    auto set = [&](int at, int e, double sum, bool here) {
+      if (WPT > 1 && lane == 0 && here) exact[at] = (float)sum;
+#pragma unroll
+      for (int n = 0; n < N; n++)
+        if (n == at >> 6 && lane == (at & 63)) {
+          id[n] = e;
+          if (WPT == 1) l[n] = (double)(float)sum;
+        }
+    };
+    if (width == G) {
       int e[G];
       double v[G];
 #pragma unroll
       for (int g = 0; g < G; g++) e[g] = next();
-      if (!mine) continue;
-      dots<G, 4, true>(p, x, e, v);
+      double sum = 0.0;
+      if (mine) sum = dots<G, G == 8 ? 2 : 4, true>(p, x, e, v);
 #pragma unroll
-      for (int g = 0; g < G; g++) set(e[g], v[g]);
+      for (int g = 0; g < G; g++) set(j + g, e[g], G == 8 ? sum : v[g], mine);
     } else {
       const int e[1] = {next()};
       double v[1];
-      if (!mine) continue;
-      if (finite) dots<1, 8, true>(p, x, e, v);
-      else dots<1, 1, false>(p, x, e, v);
-      set(e[0], v[0]);
+      if (mine) {
+        if (finite) dots<1, 8, true>(p, x, e, v);
+        else dots<1, 1, false>(p, x, e, v);
+      }
+      set(j, e[0], v[0], mine);
     }
+    j += width;
   }
   if (WPT > 1) {
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < N; n++)
-      if (is_free[n]) l[n] = (double)exact[n * 64 + lane];
+      if (n * 64 + lane < count) l[n] = (double)exact[n * 64 + lane];
   }
+  return count;
 }
 
-// Wave: one token; lane l holds experts l, l + 64, ... N of them. NaN keys rank as -inf. BOUNDS: the
-// logits come with bounds; experts that are not in question have no score, and the softmax's sum
-// cancels in the weights.
-template <bool SIGMOID, int N, bool BOUNDS, int WPT = 1>
-__global__ __launch_bounds__(256) void k_select(SelectArgs p) {
+// The token's top_k of the experts that the wave holds (in ascending order, slot after slot) and their
+// weights. NaN keys rank as -inf. RANKED: `count` experts, one a lane, each of which counts those before
+// it; else the largest is taken top_k times.
+template <bool SIGMOID, int N, bool RANKED>
+__device__ __forceinline__ void finish(const SelectArgs& p, int64_t t, double (&score)[N],
+                                       const int (&id)[N], bool (&is_free)[N], int count) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = WPT == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= p.tokens) return;
-  double score[N], key[N];
-  bool is_free[N];
-#pragma unroll
-  for (int n = 0; n < N; n++) {
-    const int e = n * 64 + lane;
-    is_free[n] = e < p.experts;
-    score[n] = -INFINITY;
-    if (!BOUNDS && is_free[n]) score[n] = (double)p.logits[t * p.experts + e];
-  }
-  if (BOUNDS) recheck<SIGMOID, N, WPT>(p, t, score, is_free);
-  if (WPT > 1 && threadIdx.x >= 64) return;
+  double key[N];
   if (SIGMOID) {
 #pragma unroll
     for (int n = 0; n < N; n++) score[n] = sigmoid64(score[n]);
@@ -501,31 +561,80 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs p) {
   }
 #pragma unroll
   for (int n = 0; n < N; n++) {
-    const int e = n * 64 + lane;
-    key[n] = score[n] + (p.bias && is_free[n] ? (double)p.bias[e] : 0.0);
+    key[n] = score[n] + (p.bias && is_free[n] ? (double)p.bias[id[n]] : 0.0);
     if (!(key[n] == key[n])) key[n] = -INFINITY;
   }
-  double chosen = 0.0, mine = 0.0;  // the sum of the chosen scores; lane k: the k-th chosen
-  int id = 0;
-  for (int k = 0; k < p.top_k; k++) {
-    double best;
-    const int at = take_largest<N>(key, is_free, best);
-    double s = 0.0;
+  double chosen = 0.0, mine = 0.0;  // the sum of the chosen scores
+  int place = kMaxExperts, expert = 0;
+  if constexpr (RANKED) {
+    int rank = 0;
+    for (int j = 0; j < count; j++) {
+      const double other = of_lane(key[0], j);
+      rank += other > key[0] || (other == key[0] && j < lane);
+    }
+    for (int k = 0; k < p.top_k; k++)
+      chosen += of_lane(score[0], __builtin_ctzll(__ballot(lane < count && rank == k)));
+    if (lane < count) place = rank;
+    mine = score[0];
+    expert = id[0];
+  } else {
+    for (int k = 0; k < p.top_k; k++) {  // the k-th goes to lane k
+      double best;
+      const int at = __builtin_amdgcn_readfirstlane(take_largest<N>(key, is_free, best));
+      double s = 0.0;
+      int e = 0;
 #pragma unroll
-    for (int n = 0; n < N; n++)
-      if (n == at >> 6) s = score[n];
-    s = __shfl(s, at & 63, 64);
-    chosen += s;
-    if (lane == k) {
-      mine = s;
-      id = at;
+      for (int n = 0; n < N; n++)
+        if (n == at >> 6) {
+          s = score[n];
+          e = id[n];
+        }
+      s = of_lane(s, at & 63);
+      e = __builtin_amdgcn_readlane(e, at & 63);
+      chosen += s;
+      if (lane == k) {
+        place = k;
+        mine = s;
+        expert = e;
+      }
     }
   }
-  if (lane < p.top_k) {
+  if (place < p.top_k) {
     double w = mine;
     if (p.renormalize) w = chosen == 0.0 ? 0.0 : mine / chosen;
-    p.ids[t * p.top_k + lane] = id;
-    p.weights[t * p.top_k + lane] = (float)(w * (double)p.scale);
+    p.ids[t * p.top_k + place] = expert;
+    p.weights[t * p.top_k + place] = (float)(w * (double)p.scale);
+  }
+}
+
+// Wave: one token; lane l holds experts l, l + 64, ... N of them. BOUNDS: the logits come with bounds;
+// only the experts in question are held, and the softmax's sum cancels in the weights.
+template <bool SIGMOID, int N, bool BOUNDS, int WPT = 1>
+__global__ __launch_bounds__(256) void k_select(SelectArgs p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = WPT == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= p.tokens) return;
+  double score[N];
+  int id[N];
+  bool is_free[N];
+  int count = p.experts;
+  if (BOUNDS) count = recheck<SIGMOID, N, WPT>(p, t, score, id);
+  if (WPT > 1 && threadIdx.x >= 64) return;
+#pragma unroll
+  for (int n = 0; n < N; n++) {
+    is_free[n] = n * 64 + lane < count;
+    if (!BOUNDS) {
+      id[n] = n * 64 + lane;
+      score[n] = is_free[n] ? (double)p.logits[t * p.experts + id[n]] : -INFINITY;
+    }
+  }
+  if (BOUNDS && count <= 64) {
+    double s[1] = {score[0]};
+    const int i[1] = {id[0]};
+    bool f[1] = {is_free[0]};
+    finish<SIGMOID, 1, true>(p, t, s, i, f, count);
+  } else {
+    finish<SIGMOID, N, false>(p, t, score, id, is_free, count);
   }
 }
 
@@ -534,24 +643,29 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs p) {
 constexpr int kMaxTopK = 32;
 
 // Which kernels, by tokens x experts x channels; logits + selection measured, us, 8 experts, sigmoid:
-//   experts, K     tokens   a wave an expert   fp64 instruction   bounds, 1 wave a token to select
-//   128, 4096      64       11 + 5             46 + 5             12 + 19
-//                  256      22 + 5             46 + 5             12 + 18
-//                  512      42 + 5             46 + 5             13 + 20
-//                  4096                        79 + 8             18 + 39
-//   64, 2048       512      15 + 4             24 + 5             9 + 12
-//                  4096                        29 + 7             10 + 25
-//   256, 7168      128      35 + 7             78 + 7             20 + 30
-//                  256      68 + 7             89 + 7             21 + 33
-//                  4096                        278 + 11           50 + 70
-// so bounds from 2^27 on, where they can be had, and the fp64 instruction from 2^28.
+//   experts, K     tokens   a wave an expert   fp64 instruction   bounds, and the sums in question
+//   128, 4096      64       12 + 5             46 + 5             14 + 8
+//                  128      15 + 5                                14 + 9
+//                  256      22 + 5             46 + 5             14 + 9
+//                  512      42 + 5             46 + 5             14 + 11
+//                  4096                        79 + 8             18 + 27
+//   64, 2048       256      9 + 4                                 9 + 6
+//                  512      15 + 4             24 + 5             9 + 7
+//                  1000     24 + 5                                10 + 10
+//                  4096                        29 + 7             10 + 18
+//   256, 7168      32       15 + 7                                21 + 12
+//                  64       26 + 7                                21 + 12
+//                  128      35 + 7             78 + 7             21 + 12
+//                  256      68 + 7             89 + 7             21 + 15
+//                  4096                        278 + 11           50 + 46
+// so bounds from 3 2^25 on, where they can be had, and the fp64 instruction from 2^28.
 // Whether they can: bf16 values in whole periods, and a result that only the chosen experts' scores
 // enter.
 bool with_bounds(dq_dtype xt, dq_dtype wt, int64_t tokens, int64_t cols, int64_t experts,
                  const float* bias, dq_score score, int renormalize) {
   return xt == DQ_BF16 && wt == DQ_BF16 && cols % 64 == 0 && cols <= kFastCols &&
          (score == DQ_SCORE_SIGMOID || (renormalize && !bias)) &&
-         tokens * experts >= ((int64_t)1 << 27) / cols;
+         tokens * experts >= ((int64_t)3 << 25) / cols;
 }
 
 template <bool XB, bool WB>
@@ -588,7 +702,7 @@ hipError_t launch_select_n(const SelectArgs& p, bool bounds, hipStream_t s) {
   const dim3 grid((unsigned)((p.tokens + 3) / 4)), block(256);
   if (!bounds)
     hipLaunchKernelGGL((k_select<SIGMOID, N, false>), grid, block, 0, s, p);
-  else if (p.tokens <= 1024)  // a token's sums take a wave 14 us (K 4096), which waves then share
+  else if (p.tokens <= 1024)  // fewer waves than the chip holds: four of them share a token's sums
     hipLaunchKernelGGL((k_select<SIGMOID, N, true, 4>), dim3((unsigned)p.tokens), block, 0, s, p);
   else
     hipLaunchKernelGGL((k_select<SIGMOID, N, true>), grid, block, 0, s, p);
