@@ -136,7 +136,7 @@ def test_extreme_and_non_finite_values(dq):
     (690, 192, 1024, 5), (500, 8192, 33, 1), (1500, 2048, 50, 4), (3000, 2560, 129, 32)])
 def test_many_tokens_close_logits(dq, tokens, cols, experts, top_k, score, bias):
     # sums of large terms that cancel, and experts that differ in the last bit of a few weights: far
-    # more of them in question than are chosen (the products from 2^27 on go by bounds, those of up to
+    # more of them in question than are chosen (the products from 3 2^25 on go by bounds, those of up to
     # 1024 tokens with four waves a token)
     rng = np.random.default_rng(cols + experts)
     X = ref.bf16(rng.standard_normal((tokens, cols)).astype(np.float32) * 8)
@@ -151,6 +151,46 @@ def test_many_tokens_close_logits(dq, tokens, cols, experts, top_k, score, bias)
     got = dq.moe_route(_tensor(X, "bf16"), _tensor(W, "bf16"), top_k, score=score, bias=_tensor(b),
                        scale=2.0)
     _check_result(got, X, W, top_k, score, b, True, 2.0)
+
+
+@pytest.mark.parametrize("tokens", [600, 1100])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_many_tokens_numbers_of_experts_in_question(dq, score, tokens):
+    # n experts that are alike and above all others: that many are in question, in several registers of
+    # a wave from 65 on; ties go to the lowest, scattered as they lie
+    cols, experts, top_k = 1024, 200, 8
+    rng = np.random.default_rng(tokens)
+    X = ref.bf16(rng.standard_normal((tokens, cols)).astype(np.float32))
+    X[:, 0] = 4.0
+    for n in (8, 9, 15, 16, 17, 63, 64, 65, 72, 129, 200):
+        W = ref.bf16((rng.standard_normal((experts, cols)) / 64).astype(np.float32))
+        alike = np.sort(rng.permutation(experts)[:n])
+        W[alike] = W[alike[0]]
+        W[alike, 0], W[np.setdiff1d(np.arange(experts), alike), 0] = 2.0, -2.0
+        print(f"[route] {n} in question", flush=True)
+        got = dq.moe_route(_tensor(X, "bf16"), _tensor(W, "bf16"), top_k, score=score)
+        assert np.array_equal(got[0].cpu().numpy(), np.tile(alike[:top_k], (tokens, 1)))
+        _check_result(got, X, W, top_k, score)
+
+
+@pytest.mark.parametrize("tokens", [600, 1100])
+def test_many_tokens_wide_scores_and_biases(dq, tokens):
+    # logits from -900 to 900: scores down to the smallest fp64 values and ties at 0 and 1; biases
+    # beyond fp32's resolution of the scores, of both signs, infinite and NaN
+    cols, experts, top_k = 1024, 200, 12
+    rng = np.random.default_rng(tokens + 1)
+    X = ref.bf16(rng.standard_normal((tokens, cols)).astype(np.float32))
+    W = ref.bf16((rng.standard_normal((experts, cols)) * 4).astype(np.float32))
+    X *= np.exp2(rng.integers(-12, 2, (tokens, 1))).astype(np.float32)
+    X[:40] = -np.abs(X[:40])
+    W[:, :512] = np.abs(W[:, :512])
+    b = (rng.standard_normal(experts) * 10.0 ** rng.integers(-9, 3, experts)).astype(np.float32)
+    b[[3, 50, 120, 199]] = [np.inf, -np.inf, np.nan, 1e38]
+    for bias in (None, b):
+        print(f"[route] wide, bias {bias is not None}", flush=True)
+        got = dq.moe_route(_tensor(X, "bf16"), _tensor(W, "bf16"), top_k, score="sigmoid",
+                           bias=_tensor(bias))
+        _check_result(got, X, W, top_k, "sigmoid", bias)
 
 
 @pytest.mark.parametrize("tokens", [100, 1000, 1030])
