@@ -177,24 +177,27 @@ __global__ __launch_bounds__(kFastWaves * 64) void k_logits_fast(FastArgs p) {
   const __amdgpu_buffer_rsrc_t rx = rsrc(p.X + t0 * p.cols, (uint32_t)nt * pitch);
   const __amdgpu_buffer_rsrc_t rw = rsrc(p.W + (int64_t)(nx ? e0 : 0) * p.cols, (uint32_t)nx * pitch);
   const __amdgpu_buffer_rsrc_t rnone = rsrc(p.X, 0u);
-  uint32_t vo[4];
+  const int periods = (p.cols + 63) / 64, first = wave >> 1;
+  uint32_t vo[4], vend[4];  // vend: in the last period, whose pieces past the row's end read zeros
 #pragma unroll
   for (int j = 0; j < 4; j++) {
-    const int r = 8 * j + (lane >> 3);
-    vo[j] = (uint32_t)r * pitch + (uint32_t)(((lane & 7) ^ (r & 7) ^ ((r >> 3) & 1)) * 16);
+    const int r = 8 * j + (lane >> 3), piece = (lane & 7) ^ (r & 7) ^ ((r >> 3) & 1);
+    vo[j] = (uint32_t)r * pitch + (uint32_t)(piece * 16);
+    vend[j] = (periods - 1) * 64 + piece * 8 < p.cols ? vo[j] : kOob;
   }
   uint8_t* ring = lds + wave * kRing;
   const int xt = (rl & 7) ^ ((rl >> 3) & 1);
-  const int periods = p.cols / 64, first = wave >> 1;
   double sum[16] = {};
   v16f size = {};
   auto load = [&](int c, int st) {  // past the last period nothing is read
-    const bool on = c < periods;
+    const bool on = c < periods, end = c == periods - 1;
     uint8_t* dst = ring + st * (2 * kTile);
 #pragma unroll
-    for (int j = 0; j < 4; j++) load_lds(on ? rx : rnone, dst + j * 1024, vo[j], c * kRowB);
+    for (int j = 0; j < 4; j++)
+      load_lds(on ? rx : rnone, dst + j * 1024, end ? vend[j] : vo[j], c * kRowB);
 #pragma unroll
-    for (int j = 0; j < 4; j++) load_lds(on ? rw : rnone, dst + kTile + j * 1024, vo[j], c * kRowB);
+    for (int j = 0; j < 4; j++)
+      load_lds(on ? rw : rnone, dst + kTile + j * 1024, end ? vend[j] : vo[j], c * kRowB);
   };
   auto stage = [&](int c, int st) {
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(8));
@@ -659,11 +662,10 @@ constexpr int kMaxTopK = 32;
 //                  256      68 + 7             89 + 7             21 + 15
 //                  4096                        278 + 11           50 + 46
 // so bounds from 3 2^25 on, where they can be had, and the fp64 instruction from 2^28.
-// Whether they can: bf16 values in whole periods, and a result that only the chosen experts' scores
-// enter.
+// Whether they can: bf16 values, and a result that only the chosen experts' scores enter.
 bool with_bounds(dq_dtype xt, dq_dtype wt, int64_t tokens, int64_t cols, int64_t experts,
                  const float* bias, dq_score score, int renormalize) {
-  return xt == DQ_BF16 && wt == DQ_BF16 && cols % 64 == 0 && cols <= kFastCols &&
+  return xt == DQ_BF16 && wt == DQ_BF16 && cols <= kFastCols &&
          (score == DQ_SCORE_SIGMOID || (renormalize && !bias)) &&
          tokens * experts >= ((int64_t)3 << 25) / cols;
 }

@@ -57,7 +57,8 @@ def _check(dq, tokens, cols, experts, top_k, xdt="bf16", wdt="bf16", score="soft
     (1, 8, 1, 1), (1, 4096, 64, 8), (1, 520, 257, 32), (2, 1000, 63, 5), (3, 512, 65, 8),
     (5, 2048, 128, 4), (17, 128, 1024, 32), (33, 8, 7, 7), (64, 1536, 129, 6), (65, 4096, 64, 8),
     (70, 24, 5, 2), (97, 1000, 33, 3), (256, 520, 256, 8), (1000, 264, 100, 1), (130, 40, 1024, 32),
-    (2100, 1000, 130, 8), (1111, 520, 520, 5)])
+    (2100, 1000, 130, 8), (1111, 520, 520, 5), (13000, 8, 1024, 4), (3000, 1032, 129, 8),
+    (1000, 2056, 70, 5), (700, 1144, 200, 6)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_shapes(dq, tokens, cols, experts, top_k, score):
     _check(dq, tokens, cols, experts, top_k, score=score, bias=tokens % 2 == 1)
