@@ -164,7 +164,7 @@ bool moe_sizes(int64_t tokens, int64_t K, int64_t inner, int64_t out, int64_t ex
 
 // Which kernel: the tile kernel, of 64 rows of an expert or 128, where an expert has a few rows and
 // there are tiles for the whole chip, or many rows; else tiles of 32 rows with k split over the waves.
-// Measured, us, gated and down product (number of workgroups of the 64-row tiles), MXFP4 then MXFP8:
+// Measured, us, gated and down product (number of workgroups of the tiles):
 //   experts, top k, K -> inner, tokens (mean rows)   split, 32 rows   tiles of 64             of 128
 //   64, 8, 2048 -> 1024, 32 (4)                      63 in all        51 in all
 //   64, 8, 4096 -> 1536, 24 (3)                      119 in all       114 in all
@@ -175,21 +175,34 @@ bool moe_sizes(int64_t tokens, int64_t K, int64_t inner, int64_t out, int64_t ex
 //   32, 4, 4096 -> 1536, 64 (8)                      42 + 33          44 (432) + 24 (576)
 //   32, 4, 4096 -> 1536, 128 (16)                    51 + 40          48 (480) + 29 (640)     51 + 32
 //   8, 2, 4096 -> 4096, 100 (25)                     37 + 25          33 (352) + 32 (176)     35 + 37
-//   32, 4, 4096 -> 1536, 700 (87)                    83 + 84          65 (900) + 47 (1200)    56 + 57
-//   32, 4, 4096 -> 1536, 1000 (125)                  105 + 109        73 (1128) + 62 (1504)   77 + 62
-//   8, 2, 4096 -> 14336, 600 (150)                   360 + 186        168 (2912) + 130 (416)  146 + 117
-//   64, 8, 2048 -> 1024, 3000 (375)                  249 + 246        103 (3512) + 106 (3512) 93 + 102
+//   4, 2, 4096 -> 2048, 100 (50)                     15 + 12          17 (112) + 15 (112)
+//   8, 2, 4096 -> 2048, 200 (50)                     28 + 25          25 (224) + 21 (224)
+//   8, 2, 2048 -> 1024, 300 (75)                     14 + 12          14 (136) + 12 (136)
+//   4, 2, 4096 -> 4096, 300 (150)                    55 + 38          34 (416) + 33 (208)     30 (256) + 39 (128)
+//   8, 2, 4096 -> 14336, 600 (150)                   344 + 186        166 (2912) + 127 (416)  147 (1904) + 117 (272)
+//   8, 2, 2048 -> 2048, 600 (150)                    30 + 22          17 (416) + 16 (208)     17 (272) + 21 (136)
+//   64, 8, 2048 -> 1024, 3000 (375)                  246 + 243        103 (3512) + 110 (3512) 93 (2008) + 102 (2008)
+// The gated product of MXFP8 activations, which takes two matrix instructions for one:
+//   4, 2, 4096 -> 2048, 100 (50)                     18               34 (112)                61
+//   8, 2, 4096 -> 2048, 200 (50)                     37               43 (224)                65
+//   4, 4, 6144 -> 1536, 151 (151)                    39               53 (192)                93
+//   4, 2, 4096 -> 4096, 300 (150)                    73               58 (416)                70
+//   8, 2, 4096 -> 14336, 600 (150)                   457              295 (2912)              352
+//   64, 8, 2048 -> 1024, 3000 (375)                  342              210 (3512)              201
 template <bool ACT8, bool GATED, int OUT>
 hipError_t launch_experts(const MlpArgs& p, Experts x, hipStream_t s) {
   constexpr int kRows = GATED ? 128 : 256;
+  constexpr bool kTwice = ACT8 && GATED;
   const int used = std::min(x.pairs, x.experts), mean = x.pairs / used;
   auto slots = [&](int tile) { return used + x.pairs / tile; };
-  if (mean > 128) {
-    x.slots = slots(128);
-    return launch_tile<ACT8, GATED, OUT, 4>(p, x, s);
+  auto tiles = [&](int tile) { return (int64_t)slots(tile) * ((p.out + kRows - 1) / kRows); };
+  if constexpr (!kTwice) {
+    if (mean > 128 && tiles(128) >= 256) {
+      x.slots = slots(128);
+      return launch_tile<ACT8, GATED, OUT, 4>(p, x, s);
+    }
   }
-  const int64_t tiles = (int64_t)slots(64) * ((p.out + kRows - 1) / kRows);
-  if (mean >= 40 || (mean >= 3 && tiles >= 340)) {
+  if (mean >= 3 && tiles(64) >= (mean < 40 ? 340 : kTwice ? 256 : 128)) {
     x.slots = slots(64);
     return launch_tile<ACT8, GATED, OUT, 2>(p, x, s);
   }
