@@ -1,8 +1,8 @@
 """Python binding of libdq.so, the MI355X dual-scale weight-reconstruction solver.
 
 Argument marshalling only: every step runs in the HIP kernels behind the C ABI declared in
-include/dq.h (through ctypes) and include/dq_mlp.h (through the compiled _bind.so). PyTorch
-provides device memory and the current stream. There is no CPU fallback: if libdq.so is missing
+include/dq.h (through ctypes), include/dq_mlp.h and include/dq_layer.h (through the compiled
+_bind.so). PyTorch provides device memory and the current stream. There is no CPU fallback: if libdq.so is missing
 or no GPU is present, calls raise.
 
     import dual_scale_w4a4_amd as dq

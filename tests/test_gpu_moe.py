@@ -95,13 +95,15 @@ def _check(dq, L, xc, xs, ids, w, act_fmt="mxfp4", mid="mxfp8", dtype="bf16", ki
 
 
 # tokens, K, inner, out, experts, top_k: one token and many; every kernel of the selection (tiles of 32
-# rows, of 64 where an expert has 3 rows or more and there are 340 tiles or where it has 40, of 128 from
-# 129 on); more pairs than a workgroup counts by itself; one expert; more experts than pairs
+# rows, of 64 where an expert has 3 rows or more and there are 340 tiles or where it has 40 and there are
+# 128, or 256, of 128 from 129 rows and 256 tiles on); more pairs than a workgroup counts by itself; one
+# expert; more experts than pairs
 SHAPES = [(1, 512, 512, 512, 4, 2), (1, 1024, 512, 32, 64, 8), (3, 512, 1024, 96, 5, 3),
           (24, 512, 512, 160, 16, 4), (33, 1536, 512, 64, 2, 1), (40, 512, 512, 64, 3, 2),
           (61, 512, 1536, 288, 2, 2), (90, 512, 512, 64, 3, 2), (130, 1024, 512, 96, 2, 2),
           (200, 512, 512, 352, 1, 1), (300, 512, 512, 64, 12, 4), (700, 512, 512, 96, 6, 3),
-          (45, 512, 512, 64, 40, 30), (200, 512, 1024, 1312, 64, 2), (130, 512, 1536, 1504, 32, 5)]
+          (45, 512, 512, 64, 40, 30), (200, 512, 1024, 1312, 64, 2), (130, 512, 1536, 1504, 32, 5),
+          (700, 512, 1024, 1504, 4, 2), (4000, 512, 512, 1024, 2, 2), (3700, 512, 1024, 1120, 3, 3)]
 
 
 @pytest.mark.parametrize("tokens,K,inner,out,n,top_k", SHAPES)
