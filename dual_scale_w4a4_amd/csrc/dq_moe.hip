@@ -14,8 +14,8 @@
 //   experts, top k, K -> inner -> K, tokens             sort   gated   down   sum   in all
 //   64, 8, 2048 -> 1024, 1 token (27 MB)                       7.3     5.8    2.3   15.4
 //   64, 8, 4096 -> 1536, 24 tokens (618 MB)                    67      43     4.6   114, 5.4 TB/s
-//   8, 2, 4096 -> 14336, 5 tokens, MXFP8 (572 MB)              67      39     4.6   101 - 111, 5.1 - 5.6 TB/s
-//   32, 4, 4096 -> 1536, 700 tokens (335 MB)            4.6    62      47     12    124, 0.85 PFLOP/s
+//   8, 2, 4096 -> 14336, 5 tokens, MXFP8 (572 MB)              67      39     4.6   93 - 111, 5.1 - 6.1 TB/s
+//   32, 4, 4096 -> 1536, 700 tokens (335 MB)            4.6    56      48     12    119, 0.89 PFLOP/s
 #include "../../include/dq_layer.h"
 #include "dq_mlp_kernels.h"
 
