@@ -645,7 +645,7 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs p) {
 
 constexpr int kMaxTopK = 32;
 
-// Which kernels, by tokens x experts x channels; logits + selection measured, us, 8 experts, sigmoid:
+// Which kernels; logits + selection measured, us, 8 experts, sigmoid, bf16 values:
 //   experts, K     tokens   a wave an expert   fp64 instruction   bounds, and the sums in question
 //   128, 4096      64       12 + 5             46 + 5             14 + 8
 //                  128      15 + 5                                14 + 9
@@ -661,18 +661,24 @@ constexpr int kMaxTopK = 32;
 //                  128      35 + 7             78 + 7             21 + 12
 //                  256      68 + 7             89 + 7             21 + 15
 //                  4096                        278 + 11           50 + 46
-// so bounds from 3 2^25 on, where they can be had, and the fp64 instruction from 2^28.
+// A wave an expert takes about 2 10^-7 us a product; bounds take 2.5 10^-3 us a channel and then little
+// more. So bounds, where they can be had, from (tokens experts - 3 2^12) channels = 2^25 on: also with few
+// tokens of many channels the time stays near the lesser.
+// Where they cannot, the fp64 instruction from tokens experts = 9 2^13 on, whatever K; logits of fp32
+// values, a wave an expert and the instruction:
+//   128, 4096: 512 tokens 49 and 55, 640 60 and 55     256, 7168: 256 tokens 78 and 93, 320 98 and 94
+//   64, 2048: 1024 tokens 25 and 29, 1300 31 and 29    1024, 8192: 8 tokens 24 and 100
 // Whether they can: bf16 values, and a result that only the chosen experts' scores enter.
 bool with_bounds(dq_dtype xt, dq_dtype wt, int64_t tokens, int64_t cols, int64_t experts,
                  const float* bias, dq_score score, int renormalize) {
   return xt == DQ_BF16 && wt == DQ_BF16 && cols <= kFastCols &&
          (score == DQ_SCORE_SIGMOID || (renormalize && !bias)) &&
-         tokens * experts >= ((int64_t)3 << 25) / cols;
+         (tokens * experts - (3 << 12)) * cols >= (1 << 25);
 }
 
 template <bool XB, bool WB>
 hipError_t launch_logits(const LogitArgs& p, hipStream_t s) {
-  if (p.tokens * p.experts < ((int64_t)1 << 28) / p.cols) {
+  if (p.tokens * p.experts < 9 << 13) {
     const int64_t ne = (p.experts + 3) / 4;
     if (p.tokens == 1)
       hipLaunchKernelGGL((k_logits_few<XB, WB, 1>), dim3((unsigned)ne), dim3(256), 0, s, p);

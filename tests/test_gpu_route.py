@@ -58,7 +58,8 @@ def _check(dq, tokens, cols, experts, top_k, xdt="bf16", wdt="bf16", score="soft
     (5, 2048, 128, 4), (17, 128, 1024, 32), (33, 8, 7, 7), (64, 1536, 129, 6), (65, 4096, 64, 8),
     (70, 24, 5, 2), (97, 1000, 33, 3), (256, 520, 256, 8), (1000, 264, 100, 1), (130, 40, 1024, 32),
     (2100, 1000, 130, 8), (1111, 520, 520, 5), (13000, 8, 1024, 4), (3000, 1032, 129, 8),
-    (1000, 2056, 70, 5), (700, 1144, 200, 6)])
+    (1000, 2056, 70, 5), (700, 1144, 200, 6), (16, 4096, 1024, 4), (2, 65536, 100, 3),
+    (20, 65536, 1000, 2)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_shapes(dq, tokens, cols, experts, top_k, score):
     _check(dq, tokens, cols, experts, top_k, score=score, bias=tokens % 2 == 1)
@@ -137,8 +138,8 @@ def test_extreme_and_non_finite_values(dq):
     (690, 192, 1024, 5), (500, 8192, 33, 1), (1500, 2048, 50, 4), (3000, 2560, 129, 32)])
 def test_many_tokens_close_logits(dq, tokens, cols, experts, top_k, score, bias):
     # sums of large terms that cancel, and experts that differ in the last bit of a few weights: far
-    # more of them in question than are chosen (the products from 3 2^25 on go by bounds, those of up to
-    # 1024 tokens with four waves a token)
+    # more of them in question than are chosen (large products go by bounds, those of up to 1024 tokens
+    # with four waves a token)
     rng = np.random.default_rng(cols + experts)
     X = ref.bf16(rng.standard_normal((tokens, cols)).astype(np.float32) * 8)
     W = ref.bf16(rng.standard_normal((experts // 8 + 1, cols)).astype(np.float32))
