@@ -5,11 +5,11 @@
 // the exact products rounded once to fp32, and scores and selection keys are fp64.
 //
 // Two launches. The logits: for small products a wave takes one expert and up to 4 tokens, k over its
-// lanes; for larger ones the fp64 matrix instruction takes tiles of 32 tokens by 32 experts a wave, k over
-// the workgroup's waves. Then a wave per token selects.
+// lanes; for larger ones the fp64 matrix instruction takes tiles of 16 or 32 tokens by as many experts,
+// k over the workgroup's waves. Then a wave per token selects.
 //
 // For large products of bf16 values the fp64 instruction is what bounds that (4096 tokens, 128 experts,
-// K 4096: 79 us of 87, 54 TFLOP/s), so the first launch takes the bf16 instruction instead and gives each
+// K 4096: 82 us of 90, 52 TFLOP/s), so the first launch takes the bf16 instruction instead and gives each
 // logit with a bound on its error, and the second computes in fp64 the few experts of each token
 // that the bounds leave in question, the chosen ones among them: the same result. Where scores of other
 // experts enter the result (the softmax's sum with a bias or without renormalization), or a value is
@@ -87,32 +87,34 @@ __global__ __launch_bounds__(256) void k_logits_few(LogitArgs p) {
   }
 }
 
-// Workgroup of W waves: 32 tokens by 32 experts, wave w taking channels 32 w .. of every 32 W (one
-// wave's partial sums joined in wave order). V_MFMA_F64_16X16X4: lane l holds row (column) l % 16,
-// k l / 16; result v of lane l is D[4 v + l / 16][l % 16]. The order of k inside a sum is free, so
-// lane quarter q takes channels 8 q .. 8 q + 7 of the 32, in 8 steps.
-template <bool XB, bool WB, int W>
-__global__ __launch_bounds__(W * 64) void k_logits_many(LogitArgs p) {
-  __shared__ double part[W][4][4][64];
+// Workgroup of 16 waves: 16 M tokens by 16 M experts, wave w taking channels 32 w .. of every 512 (the
+// waves' partial sums joined in wave order; with 4 waves 640 tokens, 128 experts, K 4096 in fp32 take 55
+// us, with 8 44, with 16 41). V_MFMA_F64_16X16X4: lane l holds row (column) l % 16, k l / 16; result v
+// of lane l is D[4 v + l / 16][l % 16]. The order of k inside a sum is free, so lane quarter q takes
+// channels 8 q .. 8 q + 7 of the 32, in 8 steps.
+template <bool XB, bool WB, int M>
+__global__ __launch_bounds__(1024) void k_logits_many(LogitArgs p) {
+  constexpr int W = 16, T = 16 * M;
+  __shared__ double part[W][M * M][4][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int rl = lane & 15, q = lane >> 4;
-  const int ne = (p.experts + 31) / 32;
-  const int e0 = (blockIdx.x % ne) * 32;
-  const int64_t t0 = (int64_t)(blockIdx.x / ne) * 32;
+  const int ne = (p.experts + T - 1) / T;
+  const int e0 = (blockIdx.x % ne) * T;
+  const int64_t t0 = (int64_t)(blockIdx.x / ne) * T;
   // rows past the end read the last one; their results are not stored
-  int64_t xo[2], wo[2];
+  int64_t xo[M], wo[M];
 #pragma unroll
-  for (int m = 0; m < 2; m++) {
+  for (int m = 0; m < M; m++) {
     xo[m] = min(t0 + 16 * m + rl, p.tokens - 1) * p.cols;
     wo[m] = (int64_t)min(e0 + 16 * m + rl, p.experts - 1) * p.cols;
   }
-  f64x4 acc[2][2] = {};
+  f64x4 acc[M][M] = {};
   for (int c0 = wave * 32; c0 < p.cols; c0 += W * 32) {
     const int c = c0 + 8 * q;
-    float x[2][8] = {}, w[2][8] = {};
+    float x[M][8] = {}, w[M][8] = {};
     if (c < p.cols) {
 #pragma unroll
-      for (int m = 0; m < 2; m++) {
+      for (int m = 0; m < M; m++) {
         load8<XB>(p.X, xo[m] + c, x[m]);
         load8<WB>(p.W, wo[m] + c, w[m]);
       }
@@ -120,25 +122,25 @@ __global__ __launch_bounds__(W * 64) void k_logits_many(LogitArgs p) {
 #pragma unroll
     for (int k = 0; k < 8; k++)
 #pragma unroll
-      for (int m = 0; m < 2; m++)
+      for (int m = 0; m < M; m++)
 #pragma unroll
-        for (int n = 0; n < 2; n++)
+        for (int n = 0; n < M; n++)
           acc[m][n] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)x[m][k], (double)w[n][k],
                                                            acc[m][n], 0, 0, 0);
   }
 #pragma unroll
-  for (int m = 0; m < 2; m++)
+  for (int m = 0; m < M; m++)
 #pragma unroll
-    for (int n = 0; n < 2; n++)
+    for (int n = 0; n < M; n++)
 #pragma unroll
-      for (int v = 0; v < 4; v++) part[wave][2 * m + n][v][lane] = acc[m][n][v];
+      for (int v = 0; v < 4; v++) part[wave][M * m + n][v][lane] = acc[m][n][v];
   __syncthreads();
-  for (int i = threadIdx.x; i < 1024; i += W * 64) {
+  for (int i = threadIdx.x; i < T * T; i += W * 64) {
     const int b = i >> 8, v = (i >> 6) & 3, l = i & 63;
     double s = 0.0;
     for (int w = 0; w < W; w++) s += part[w][b][v][l];
-    const int64_t t = t0 + 16 * (b >> 1) + 4 * v + (l >> 4);
-    const int e = e0 + 16 * (b & 1) + (l & 15);
+    const int64_t t = t0 + 16 * (b / M) + 4 * v + (l >> 4);
+    const int e = e0 + 16 * (b % M) + (l & 15);
     if (t < p.tokens && e < p.experts) p.logits[t * p.experts + e] = (float)s;
   }
 }
@@ -645,40 +647,40 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs p) {
 
 constexpr int kMaxTopK = 32;
 
-// Which kernels; logits + selection measured, us, 8 experts, sigmoid, bf16 values:
-//   experts, K     tokens   a wave an expert   fp64 instruction   bounds, and the sums in question
-//   128, 4096      64       12 + 5             46 + 5             14 + 8
-//                  128      15 + 5                                14 + 9
-//                  256      22 + 5             46 + 5             14 + 9
-//                  512      42 + 5             46 + 5             14 + 11
-//                  4096                        79 + 8             18 + 27
-//   64, 2048       256      9 + 4                                 9 + 6
-//                  512      15 + 4             24 + 5             9 + 7
-//                  1000     24 + 5                                10 + 10
-//                  4096                        29 + 7             10 + 18
-//   256, 7168      32       15 + 7                                21 + 12
-//                  64       26 + 7                                21 + 12
-//                  128      35 + 7             78 + 7             21 + 12
-//                  256      68 + 7             89 + 7             21 + 15
-//                  4096                        278 + 11           50 + 46
-// A wave an expert takes about 2 10^-7 us a product; bounds take 2.5 10^-3 us a channel and then little
-// more. So bounds, where they can be had, from (tokens experts - 3 2^12) channels = 2^25 on: also with few
-// tokens of many channels the time stays near the lesser.
-// Where they cannot, the fp64 instruction from tokens experts = 9 2^13 on, whatever K; logits of fp32
-// values, a wave an expert and the instruction:
-//   128, 4096: 512 tokens 49 and 55, 640 60 and 55     256, 7168: 256 tokens 78 and 93, 320 98 and 94
-//   64, 2048: 1024 tokens 25 and 29, 1300 31 and 29    1024, 8192: 8 tokens 24 and 100
+// Which kernels; logits + selection measured, us, 8 experts, sigmoid:
+//   experts, K     tokens   a wave an    fp64 instruction,    .. of 32   bounds, and the sums
+//                           expert       tiles of 16                     in question (bf16)
+//   128, 4096      96       15 + 5       17 + 5                          14 + 8
+//                  192      21 + 5       18 + 5                          14 + 9
+//                  512      46 + 5       18 + 5                          14 + 11
+//                  640      57 + 5       32 + 5               41 + 5     14 + 12
+//                  1024                  32 + 6               41 + 6     14 + 15
+//                  1500                  45 + 6               41 + 6
+//                  4096                  118 + 8              82 + 8     18 + 27
+//   64, 2048       256      10 + 4       11 + 4                          9 + 6
+//                  512      16 + 4       11 + 4                          9 + 7
+//                  1300                  17 + 4               22 + 4     10 + 11
+//                  4096                  31 + 6               22 + 6     10 + 18
+//   256, 7168      64       23 + 8       27 + 8                          21 + 12
+//                  128      45 + 8       28 + 8                          21 + 12
+//                  256                   28 + 8                          21 + 15
+//                  320                   52 + 8               70 + 8
+//   128, 1024      160      8 + 5        6 + 5
+//                  4096                                       20 + 8     9 + 15
+// So by tokens x experts, nearly whatever K: the fp64 instruction from 5 2^12 on, in tiles of 16 as long
+// as those of 32 are at most 160. Bounds, where they can be had, above 2^16 (more tiles of 16 than CUs)
+// and from 2^28 products on.
 // Whether they can: bf16 values, and a result that only the chosen experts' scores enter.
 bool with_bounds(dq_dtype xt, dq_dtype wt, int64_t tokens, int64_t cols, int64_t experts,
                  const float* bias, dq_score score, int renormalize) {
   return xt == DQ_BF16 && wt == DQ_BF16 && cols <= kFastCols &&
          (score == DQ_SCORE_SIGMOID || (renormalize && !bias)) &&
-         (tokens * experts - (3 << 12)) * cols >= (1 << 25);
+         tokens * experts > (1 << 16) && tokens * experts * cols >= (1 << 28);
 }
 
 template <bool XB, bool WB>
 hipError_t launch_logits(const LogitArgs& p, hipStream_t s) {
-  if (p.tokens * p.experts < 9 << 13) {
+  if (p.tokens * p.experts < 5 << 12) {
     const int64_t ne = (p.experts + 3) / 4;
     if (p.tokens == 1)
       hipLaunchKernelGGL((k_logits_few<XB, WB, 1>), dim3((unsigned)ne), dim3(256), 0, s, p);
@@ -686,8 +688,11 @@ hipError_t launch_logits(const LogitArgs& p, hipStream_t s) {
       hipLaunchKernelGGL((k_logits_few<XB, WB, 4>), dim3((unsigned)(ne * ((p.tokens + 3) / 4))),
                          dim3(256), 0, s, p);
   } else {
-    const int64_t n = (int64_t)((p.experts + 31) / 32) * ((p.tokens + 31) / 32);
-    hipLaunchKernelGGL((k_logits_many<XB, WB, 4>), dim3((unsigned)n), dim3(256), 0, s, p);
+    auto tiles = [&](int t) { return ((p.experts + t - 1) / t) * ((p.tokens + t - 1) / t); };
+    if (tiles(32) <= 160)
+      hipLaunchKernelGGL((k_logits_many<XB, WB, 1>), dim3((unsigned)tiles(16)), dim3(1024), 0, s, p);
+    else
+      hipLaunchKernelGGL((k_logits_many<XB, WB, 2>), dim3((unsigned)tiles(32)), dim3(1024), 0, s, p);
   }
   return hipGetLastError();
 }
@@ -708,10 +713,12 @@ hipError_t launch_logits_fast(const LogitArgs& l, hipStream_t s) {
 template <bool SIGMOID, int N>
 hipError_t launch_select_n(const SelectArgs& p, bool bounds, hipStream_t s) {
   const dim3 grid((unsigned)((p.tokens + 3) / 4)), block(256);
+  // up to 1024 tokens, so above 64 experts: fewer waves than the chip holds; four share a token's sums
+  constexpr int kShare = N > 1 ? 4 : 1;
   if (!bounds)
     hipLaunchKernelGGL((k_select<SIGMOID, N, false>), grid, block, 0, s, p);
-  else if (p.tokens <= 1024)  // fewer waves than the chip holds: four of them share a token's sums
-    hipLaunchKernelGGL((k_select<SIGMOID, N, true, 4>), dim3((unsigned)p.tokens), block, 0, s, p);
+  else if (kShare > 1 && p.tokens <= 1024)
+    hipLaunchKernelGGL((k_select<SIGMOID, N, true, kShare>), dim3((unsigned)p.tokens), block, 0, s, p);
   else
     hipLaunchKernelGGL((k_select<SIGMOID, N, true>), grid, block, 0, s, p);
   return hipGetLastError();

@@ -57,9 +57,9 @@ def _check(dq, tokens, cols, experts, top_k, xdt="bf16", wdt="bf16", score="soft
     (1, 8, 1, 1), (1, 4096, 64, 8), (1, 520, 257, 32), (2, 1000, 63, 5), (3, 512, 65, 8),
     (5, 2048, 128, 4), (17, 128, 1024, 32), (33, 8, 7, 7), (64, 1536, 129, 6), (65, 4096, 64, 8),
     (70, 24, 5, 2), (97, 1000, 33, 3), (256, 520, 256, 8), (1000, 264, 100, 1), (130, 40, 1024, 32),
-    (2100, 1000, 130, 8), (1111, 520, 520, 5), (13000, 8, 1024, 4), (3000, 1032, 129, 8),
-    (1000, 2056, 70, 5), (700, 1144, 200, 6), (16, 4096, 1024, 4), (2, 65536, 100, 3),
-    (20, 65536, 1000, 2)])
+    (2100, 1000, 130, 8), (1111, 520, 520, 5), (33000, 8, 1024, 4), (3000, 1032, 129, 8),
+    (1000, 4104, 70, 5), (700, 2104, 200, 6), (16, 4096, 1024, 4), (2, 65536, 100, 3),
+    (20, 65536, 1000, 2), (66, 8200, 1000, 7), (300, 520, 130, 4), (900, 264, 150, 2)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_shapes(dq, tokens, cols, experts, top_k, score):
     _check(dq, tokens, cols, experts, top_k, score=score, bias=tokens % 2 == 1)
@@ -134,8 +134,8 @@ def test_extreme_and_non_finite_values(dq):
 
 @pytest.mark.parametrize("score,bias", [("softmax", False), ("sigmoid", False), ("sigmoid", True)])
 @pytest.mark.parametrize("tokens,cols,experts,top_k", [
-    (150, 64, 40, 8), (700, 1024, 200, 8), (1100, 1024, 130, 32), (260, 4096, 130, 8),
-    (690, 192, 1024, 5), (500, 8192, 33, 1), (1500, 2048, 50, 4), (3000, 2560, 129, 32)])
+    (150, 64, 40, 8), (700, 2048, 200, 8), (1100, 2048, 130, 32), (600, 4096, 130, 8),
+    (690, 448, 1024, 5), (2100, 8192, 33, 1), (1500, 4096, 50, 4), (3000, 2560, 129, 32)])
 def test_many_tokens_close_logits(dq, tokens, cols, experts, top_k, score, bias):
     # sums of large terms that cancel, and experts that differ in the last bit of a few weights: far
     # more of them in question than are chosen (large products go by bounds, those of up to 1024 tokens
@@ -160,7 +160,7 @@ def test_many_tokens_close_logits(dq, tokens, cols, experts, top_k, score, bias)
 def test_many_tokens_numbers_of_experts_in_question(dq, score, tokens):
     # n experts that are alike and above all others: that many are in question, in several registers of
     # a wave from 65 on; ties go to the lowest, scattered as they lie
-    cols, experts, top_k = 1024, 200, 8
+    cols, experts, top_k = 2304, 200, 8
     rng = np.random.default_rng(tokens)
     X = ref.bf16(rng.standard_normal((tokens, cols)).astype(np.float32))
     X[:, 0] = 4.0
@@ -179,7 +179,7 @@ def test_many_tokens_numbers_of_experts_in_question(dq, score, tokens):
 def test_many_tokens_wide_scores_and_biases(dq, tokens):
     # logits from -900 to 900: scores down to the smallest fp64 values and ties at 0 and 1; biases
     # beyond fp32's resolution of the scores, of both signs, infinite and NaN
-    cols, experts, top_k = 1024, 200, 12
+    cols, experts, top_k = 2304, 200, 12
     rng = np.random.default_rng(tokens + 1)
     X = ref.bf16(rng.standard_normal((tokens, cols)).astype(np.float32))
     W = ref.bf16((rng.standard_normal((experts, cols)) * 4).astype(np.float32))
@@ -199,7 +199,7 @@ def test_many_tokens_wide_scores_and_biases(dq, tokens):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_many_tokens_non_finite_and_extreme_values(dq, score, tokens):
     rng = np.random.default_rng(8)
-    cols, n = 2048, 70
+    cols, n = 4096, 70
     W = ref.bf16(rng.standard_normal((n, cols)).astype(np.float32))
     X = ref.bf16(rng.standard_normal((tokens, cols)).astype(np.float32))
     X[3], X[4, 7], X[5, 9], X[6] = 0, np.nan, np.inf, X[6] * np.float32(2 ** 100)
@@ -217,7 +217,7 @@ def test_many_tokens_non_finite_and_extreme_values(dq, score, tokens):
             _check_result(got, X, V, 6, score)
 
 
-@pytest.mark.parametrize("tokens", [6, 130, 6600])
+@pytest.mark.parametrize("tokens", [6, 130, 6600, 13200])
 def test_given_arrays_streams_and_graph_replays(dq, tokens):
     import torch
 
