@@ -498,9 +498,9 @@ __device__ __forceinline__ const uint16_t* parts_of(const Adapters& x, int t0) {
   return x.parts + (int64_t)(t0 / 32) * ((x.rank + 15) / 16) * (NP * 512);
 }
 
-// The rank values j0 .. j0 + 15 of the 32 tokens from t0 on, split; SUM: they may lie in partial sums
-// (up to kSliceTokens tokens, which no tile kernel takes). Columns of tokens without an adapter
-// hold anything.
+// The rank values j0 .. j0 + 15 of the 32 tokens from t0 on (t0 < tokens), split; SUM: they may lie in
+// partial sums (up to kSliceTokens tokens, which no tile kernel takes). Columns of tokens without an
+// adapter hold anything.
 template <int NP, bool SUM>
 __device__ __forceinline__ void load_u(const Adapters& x, int t0, int tokens, int id, int j0,
                                        bf16x8 (&part)[NP]) {
@@ -949,11 +949,13 @@ __global__ __launch_bounds__(W * 64) void k_mlp_split(MlpArgs p, X x) {
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
 
   // adapters: this wave's share of them, joined with its share of k; the blocks' units begin at
-  // different waves, since most blocks have few
+  // different waves, since most blocks have few. With an odd number of blocks of 32 tokens the last
+  // tile's second does not exist, nor do its parts, which would lie past the workspace's end.
   if constexpr (kAdapters<X>) {
     scales.template apply<NB>(acc);
 #pragma unroll
     for (int n = 0; n < NB; n++) {
+      if (n && n * 32 >= rows) continue;
       v16f d[M];
 #pragma unroll
       for (int m = 0; m < M; m++) d[m] = acc[m][n];
