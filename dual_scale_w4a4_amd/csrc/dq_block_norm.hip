@@ -87,13 +87,14 @@ __device__ __forceinline__ uint32_t top_bits(const float (&v)[kNormEpl]) {
 }
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// Sum of squares of 16 values, exact but for the additions. bf16 values whose squares stay in fp32's
-// normal range (or below 2^-150 of the largest) are squared there, exactly (16 bits), and become
-// fp64 values times 2^-896 by a shift of their bits: three instructions each, where the conversion
-// alone costs four times one.
+// Sum of squares of 16 values, exact but for the additions. bf16 values are squared in fp32 where that
+// is exact (16 bits) and become fp64 values times 2^-896 by a shift of their bits: three instructions
+// each, where the conversion alone costs four times one. A square below fp32's normal range keeps a
+// multiple of 2^-146; with a largest value above 2^-44 fifteen of them lose less than 2^-54 of its square,
+// an addition's rounding.
 template <bool BF>
 __device__ __forceinline__ double squares16(const float (&h)[kNormEpl], uint32_t top) {
-  if (BF && top < 0x5F000000u && (top > 0x26800000u || top == 0u)) {  // 2^-50 .. 2^63, or all zero
+  if (BF && top < 0x5F000000u && (top > 0x29800000u || top == 0u)) {  // 2^-44 .. 2^63, or all zero
     double s[2] = {};
 #pragma unroll
     for (int k = 0; k < kNormEpl; k++)
