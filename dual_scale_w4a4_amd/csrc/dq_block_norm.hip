@@ -172,6 +172,7 @@ __global__ __launch_bounds__(NW * kWave, 4) void k_block_norm(BlockNormArgs p) {
     }
   };
   const double rn = 1.0 / (double)p.n;
+  constexpr int kInput = 1 << 30;  // this lane's X or R of the row is not finite
   int flags = 0, turn = 0;  // the sums take the two arrays in turn: one barrier lies between a read
                             // of an array and its next use
   for (; row < p.m; row += gridDim.x) {
@@ -180,9 +181,8 @@ __global__ __launch_bounds__(NW * kWave, 4) void k_block_norm(BlockNormArgs p) {
     xr.unpack(h);
     if (act && next < p.m) xr.load(p.X, next * p.n + c);
     const uint32_t topx = top_bits(h);
-    double sum1 = 0.0;
     if (p.norm1) {
-      sum1 = block_sum(squares16<BF>(h, topx), red[turn], waves);
+      const double sum1 = block_sum(squares16<BF>(h, topx), red[turn], waves);
       turn ^= 1;
       const float r1 = rstd_of(sum1, rn, p.post_eps);
 #pragma unroll
@@ -197,18 +197,20 @@ __global__ __launch_bounds__(NW * kWave, 4) void k_block_norm(BlockNormArgs p) {
     rr.unpack(r);
     join16<BF>(h, r, p.rs, p.h, off, act);
     const uint32_t toph = top_bits(h);
-    if (toph >= kInfBits) {  // rare: what is not finite in X or R is not in h either
-      if (topx >= kInfBits || top_bits(r) >= kInfBits) flags |= kStNonFinite;
-      else if (act && sum1 <= DBL_MAX) flags |= kStRange;  // else another lane's X, reported there
-    }
+    // rare: what is not finite in X or R is not in h either
+    if (toph >= kInfBits && (topx >= kInfBits || top_bits(r) >= kInfBits)) flags |= kInput;
     if (act && p.R && next < p.m) rr.load(p.R, next * p.n + c);
     const double sum2 = block_sum(squares16<BF>(h, toph), red[turn], waves);
     turn ^= 1;
-    // a value of n or x that is not finite, unless the row's h already was not (reported above)
+    if (!(sum2 <= DBL_MAX)) {  // a value of h that is not finite, which any lane's X or R explains
+      const bool in = block_sum(flags & kInput ? 1.0 : 0.0, red[turn], waves) > 0.0;
+      turn ^= 1;
+      flags = (flags & ~kInput) | (in ? kStNonFinite : kStRange);
+    }
     bool over = norm16(h, rstd_of(sum2, rn, p.eps), w, p, off, act);
     if (p.b) times(h, 1);
     over |= quantize16<FMT, G>(h, act, p, off, q);
-    if (over && sum2 <= DBL_MAX) flags |= kStRange;
+    if (over && sum2 <= DBL_MAX) flags |= kStRange;  // a value of n or x that is not finite
   }
   if (flags) atomicOr(p.status, flags);
 }
@@ -219,6 +221,7 @@ __global__ __launch_bounds__(kBlock) void k_block_norm_wide(BlockNormArgs p) {
   __shared__ double red[2][kWaves];
   const int64_t row = (int64_t)blockIdx.x * p.n;
   int flags = 0;
+  bool wild = false;  // X or R is not finite
   double sum1 = 0.0, sum2 = 0.0;
   if (p.norm1) {
     for (int64_t c = threadIdx.x * kNormEpl; c < p.n; c += kBlock * kNormEpl) {
@@ -233,10 +236,10 @@ __global__ __launch_bounds__(kBlock) void k_block_norm_wide(BlockNormArgs p) {
   for (int64_t c = threadIdx.x * kNormEpl; c < p.n; c += kBlock * kNormEpl) {
     float h[kNormEpl], r[kNormEpl] = {}, v[kNormEpl];
     load16<BF>(p.X, row + c, h);
-    bool in = top_bits(h) >= kInfBits;
+    wild |= top_bits(h) >= kInfBits;
     if (p.R) {
       load16<BF>(p.R, row + c, r);
-      in |= top_bits(r) >= kInfBits;
+      wild |= top_bits(r) >= kInfBits;
     }
     if (p.norm1) {
       load_ones(p.post, p.wbf, c, v);
@@ -247,12 +250,12 @@ __global__ __launch_bounds__(kBlock) void k_block_norm_wide(BlockNormArgs p) {
 #pragma unroll
     for (int k = 0; k < kNormEpl; k++) h[k] = h[k] * v[k] * tg;
     join16<BF>(h, r, p.rs, p.h, row + c, true);
-    const uint32_t top = top_bits(h);
-    if (in) flags |= kStNonFinite;
-    else if (top >= kInfBits && sum1 <= DBL_MAX) flags |= kStRange;
-    sum2 += squares16<BF>(h, top);
+    sum2 += squares16<BF>(h, top_bits(h));
   }
   sum2 = block_sum(sum2, red[1], kWaves);
+  // a value of h that is not finite: any lane's X or R explains it
+  if (!(sum2 <= DBL_MAX))
+    flags |= block_sum(wild ? 1.0 : 0.0, red[0], kWaves) > 0.0 ? kStNonFinite : kStRange;
   const float r2 = rstd_of(sum2, rn, p.eps);
   const QuantConst q = quant_const(p.g);
   // every lane of a wave runs the same trips (the group maxima exchange lanes); lanes past the

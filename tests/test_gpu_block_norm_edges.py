@@ -1,4 +1,5 @@
-"""The block norm where its sums could go wrong: squares next to fp32's smallest."""
+"""The block norm where its sums and its status word could go wrong: squares next to fp32's smallest,
+rows that hold both kinds of error."""
 from fractions import Fraction
 
 import numpy as np
@@ -47,3 +48,34 @@ def test_squares_below_fp32_normal_range_count(dq, power, cols):
     assert np.array_equal(got["residual"].float().cpu().numpy(), h)
     assert n[0, 0] == np.float32(big) * np.float32(v[0])
     assert np.array_equal(x_out.cpu().numpy(), n)
+
+
+@pytest.mark.parametrize("cols", [544, 2080, 16416])
+@pytest.mark.parametrize("post_norm", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_an_overflow_beside_a_value_that_is_not_finite_is_not_reported(dq, cols, post_norm, dtype):
+    """Status bit 2 is for rows whose inputs are finite: elsewhere in the row of a NaN or an infinity
+    h overflows, and the other rows are clean."""
+    import torch
+
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    X, R = (torch.ones(5, cols, device="cuda", dtype=dt) for _ in range(2))
+    gate = torch.ones(cols, device="cuda")
+    for where, bad, at, over in (("X", float("nan"), 3, cols - 2), ("X", float("inf"), cols - 1, 40),
+                                 ("R", float("nan"), 3, cols - 2), ("R", -float("inf"), cols - 1, 40)):
+        Y, S = X.clone(), R.clone()
+        S[2, over] = 3e38
+        large = S.clone()
+        g = gate.clone()
+        g[over] = 3e38
+        (Y if where == "X" else S)[2, at] = bad
+        for values, want in (((Y, S), 1), ((X, large), 2), ((X, R), 0)):
+            x, r = values
+            codes, scales = dq.act_outputs(x, "mxfp8", 32)
+            st, h = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty_like(x)
+            dq.block_norm_quantize_act_async(x, "mxfp8", 32, codes, scales, st, residual=r,
+                                             residual_out=h, post_norm=post_norm,
+                                             gate=None if want == 0 else g)
+            # without a post norm (or with one whose output is about 1) the gate's 3e38 takes h past the
+            # largest value where residual is 3e38 too
+            assert int(st.item()) == want, (where, bad, at, want)
