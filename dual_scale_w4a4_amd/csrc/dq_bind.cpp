@@ -1,7 +1,8 @@
 // dq_bind.cpp -- the Python binding's calls of the MLP operators (include/dq_mlp.h) and of those
-// of other decoder layers (include/dq_layer.h): argument checks, output tensors, the stream, and the call of the C entry point. A single token's
-// operator is a few microseconds on the GPU, less than the same checks took in Python: on one
-// box gemm_mx_epilogue cost the host 10 us a call there and 5 here.
+// of other decoder layers (include/dq_layer.h): argument checks, output tensors, the stream, and the
+// call of the C entry point. A single token's operator is a few microseconds on the GPU, less than
+// the same checks took in Python: on one box gemm_mx_epilogue cost the host 10 us a call there and 5
+// here.
 //
 // Every tensor lies on one device, the first argument's, which is made current for the call. The
 // work goes to `stream` (a torch stream or None for the device's current one), on which the
@@ -62,6 +63,21 @@ struct Arr {
   }
   const float* floats(PyObject* o, const char* name, int64_t n) const {
     return static_cast<const float*>(option(o, name, at::kFloat, {n}));
+  }
+};
+
+// The bytes of a workspace that the caller gives, all of them the tensor's own
+struct Given {
+  void* ptr = nullptr;
+  size_t bytes = 0;
+
+  Given(PyObject* o, const Arr& arr) {
+    if (o == Py_None) return;
+    const at::Tensor& t = tensor(o, "workspace");
+    if (t.device() != arr.dev || !t.is_contiguous())
+      refuse("workspace must be a contiguous tensor on the arguments' device");
+    ptr = t.data_ptr();
+    bytes = t.nbytes();
   }
 };
 
@@ -200,20 +216,13 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t) {
                                      static_cast<int*>(st.data_ptr()), place.stream),
           "dq_norm_quantize_act_async");
   } else {
-    void* ws = nullptr;
-    size_t bytes = 0;
-    if (a[12] != Py_None) {
-      const at::Tensor& w = tensor(a[12], "workspace");
-      if (w.device() != arr.dev) refuse("workspace must lie on X's device");
-      ws = w.data_ptr();
-      bytes = w.nbytes();
-    }
+    const Given ws(a[12], arr);
     const Place place(arr.dev, a[13]);
     dq_status st;
     Py_BEGIN_ALLOW_THREADS  // it waits for the stream
     st = dq_norm_quantize_act(X.data_ptr(), dt, residual, residual_out, q.tokens, q.cols, weight,
                               wt, eps, b, (dq_format)q.fmt, (int)q.group, g,
-                              static_cast<uint8_t*>(codes), scales, ws, bytes, place.stream);
+                              static_cast<uint8_t*>(codes), scales, ws.ptr, ws.bytes, place.stream);
     Py_END_ALLOW_THREADS
     check(st, "dq_norm_quantize_act");
   }
@@ -277,21 +286,14 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t) {
               static_cast<int*>(st.data_ptr()), place.stream),
           "dq_block_norm_quantize_act_async");
   } else {
-    void* ws = nullptr;
-    size_t bytes = 0;
-    if (a[19] != Py_None) {
-      const at::Tensor& t = tensor(a[19], "workspace");
-      if (t.device() != arr.dev) refuse("workspace must lie on X's device");
-      ws = t.data_ptr();
-      bytes = t.nbytes();
-    }
+    const Given ws(a[19], arr);
     const Place place(arr.dev, a[20]);
     dq_status st;
     Py_BEGIN_ALLOW_THREADS  // it waits for the stream
     st = dq_block_norm_quantize_act(
         X.data_ptr(), type(xt), post_norm, post, post_eps, gate, token_gate, residual, rs,
         residual_out, q.tokens, q.cols, w, type(wt), eps, x_out, type(xot), b, (dq_format)q.fmt,
-        (int)q.group, g, static_cast<uint8_t*>(codes), scales, ws, bytes, place.stream);
+        (int)q.group, g, static_cast<uint8_t*>(codes), scales, ws.ptr, ws.bytes, place.stream);
     Py_END_ALLOW_THREADS
     check(st, "dq_block_norm_quantize_act");
   }
@@ -464,24 +466,15 @@ PyObject* gated_quantized(PyObject*, PyObject* const* a, Py_ssize_t) {
   END_HANDLE_TH_ERRORS
 }
 
-// A call's workspace: the caller's (uint8, on the device), or one that belongs to its stream
-struct Space {
+// A call's workspace: the caller's, or one that belongs to its stream
+struct Space : Given {
   at::Tensor made;
-  void* ptr;
-  size_t bytes;
 
-  Space(PyObject* o, size_t need, const Arr& arr) {
-    if (o == Py_None) {
-      made = make({(int64_t)need}, at::kByte, arr.dev);
-      ptr = made.data_ptr();
-      bytes = need;
-      return;
-    }
-    const at::Tensor& t = tensor(o, "workspace");
-    if (t.device() != arr.dev || !t.is_contiguous())
-      refuse("workspace must be a contiguous tensor on the arguments' device");
-    ptr = t.data_ptr();
-    bytes = t.nbytes();
+  Space(PyObject* o, size_t need, const Arr& arr) : Given(o, arr) {
+    if (o != Py_None) return;
+    made = make({(int64_t)need}, at::kByte, arr.dev);
+    ptr = made.data_ptr();
+    bytes = need;
   }
 };
 

@@ -1,5 +1,5 @@
-"""The block norm where its sums and its status word could go wrong: squares next to fp32's smallest,
-rows that hold both kinds of error."""
+"""The block norm where its sums, its status word and its workspace could go wrong: squares next to
+fp32's smallest, rows that hold both kinds of error, workspaces that are no dense array."""
 from fractions import Fraction
 
 import numpy as np
@@ -79,3 +79,17 @@ def test_an_overflow_beside_a_value_that_is_not_finite_is_not_reported(dq, cols,
             # without a post norm (or with one whose output is about 1) the gate's 3e38 takes h past the
             # largest value where residual is 3e38 too
             assert int(st.item()) == want, (where, bad, at, want)
+
+
+@pytest.mark.parametrize("call", ["norm_quantize_act", "block_norm_quantize_act"])
+def test_a_workspace_that_is_no_dense_array_is_refused(dq, call):
+    import torch
+
+    X = torch.randn(4, 256, device="cuda")
+    run = lambda ws: getattr(dq, call)(X, "mxfp8", 32, workspace=ws)  # noqa: E731
+    for ws in (torch.zeros(1024, dtype=torch.uint8, device="cuda")[::4],
+               torch.zeros(512, 2, dtype=torch.uint8, device="cuda").t(),
+               torch.zeros(512, dtype=torch.uint8, device="cuda")[:1].expand(256)):
+        with pytest.raises(ValueError, match="workspace"):
+            run(ws)
+    run(torch.zeros(256, dtype=torch.uint8, device="cuda"))
