@@ -259,10 +259,12 @@ __global__ __launch_bounds__(kFastWaves * 64) void k_logits_fast(FastArgs p) {
     const int e = (blockIdx.x % ne) * 64 + b * 32 + (l & 31);
     if (t < p.tokens && e < p.experts) {
       // the magnitudes' sum is itself off by up to cols / 2^23 of it, at most 1 / 128; the logit is
-      // rounded here and once more to compare; products below fp32's range may be lost
+      // rounded here and once more to compare; products below fp32's range may be lost. Without any
+      // magnitude it stands as 0: products below 2^-126 add up to 2^-110 at most, and where all of a
+      // token's experts are such their scores are equal in fp64 either way.
       float2 o;
       o.x = (float)s;
-      o.y = m * (1.02f / (1 << 17)) + fabsf(o.x) * 0x1p-22f + 0x1p-100f;
+      o.y = m == 0.0f ? 0.0f : m * (1.02f / (1 << 17)) + fabsf(o.x) * 0x1p-22f + 0x1p-100f;
       *reinterpret_cast<float2*>(p.out + (t * p.experts + e) * 2) = o;
     }
   }
@@ -414,8 +416,8 @@ __device__ __forceinline__ float of_order(uint32_t u) {
   return u2f(u ^ (u >> 31 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// The token's experts that can be among the top_k, in ascending order, the j-th in slot j / 64 of lane
-// j % 64: their exact logits and numbers; returns how many.
+// The token's experts that can be among the top_k (or more), in ascending order, the j-th in slot j / 64
+// of lane j % 64: their exact logits and numbers; returns how many.
 //
 // Keys grow with the logits, so an expert whose key at its upper bound lies below the top_k-th
 // largest of the keys at the lower bounds cannot. The keys of the bounds are fp32, widened by more
@@ -429,7 +431,7 @@ __device__ __forceinline__ int recheck(const SelectArgs& p, int64_t t, double (&
   __shared__ float exact[WPT == 1 ? 1 : 64 * N];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t lo[N], hi[N];
-  bool wild = false;
+  bool wild = false, zeros = true;
   float top = -INFINITY;
 #pragma unroll
   for (int n = 0; n < N; n++) {
@@ -442,6 +444,7 @@ __device__ __forceinline__ int recheck(const SelectArgs& p, int64_t t, double (&
       float from = v.x - v.y, to = v.x + v.y, slack = 1e-7f;
       top = fmaxf(top, to);
       wild |= !(fabsf(v.x) + v.y < 1e38f);
+      zeros &= v.y == 0.0f;
       if (SIGMOID) {
         const float b = p.bias ? p.bias[e] : 0.0f;
         from = __builtin_amdgcn_rcpf(1.0f + expf(-from));
@@ -454,6 +457,18 @@ __device__ __forceinline__ int recheck(const SelectArgs& p, int64_t t, double (&
       lo[n] = from == from ? ordered(from) : 0u;
       hi[n] = ordered(to + slack);
     }
+  }
+  // A token of zeros (a batch's padding): without a bias every expert is in question, and every logit is
+  // known. 4096 tokens, 128 experts, K 4096: 26 us where all are such, 35 with half of them, 46 with none
+  // (summing their experts again 297 and 189, more than the 85 of the fp64 instruction).
+  if (__all(zeros)) {
+#pragma unroll
+    for (int n = 0; n < N; n++)
+      if (n * 64 + lane < p.experts) {
+        id[n] = n * 64 + lane;
+        l[n] = 0.0;
+      }
+    return p.experts;
   }
   // the top_k-th largest of lo, bit by bit until the top_k are apart, then the least of them
   uint32_t kth = 0u;
