@@ -2,8 +2,8 @@
 
 Argument marshalling only: every step runs in the HIP kernels behind the C ABI declared in
 include/dq.h (through ctypes), include/dq_mlp.h and include/dq_layer.h (through the compiled
-_bind.so). PyTorch provides device memory and the current stream. There is no CPU fallback: if libdq.so is missing
-or no GPU is present, calls raise.
+_bind.so). PyTorch provides device memory and the current stream. There is no CPU fallback: if
+libdq.so is missing or no GPU is present, calls raise.
 
     import dual_scale_w4a4_amd as dq
     out = dq.solve(W_cuda_bf16, "mxfp4", group=32, T=20)
@@ -644,7 +644,8 @@ def moe_mx(act_codes, act_scales, ids, weights, gate, up, down, experts: int, a_
     """dq_moe_mx: Y = residual + sum_s weights[t, s] * the gated MLP of expert ids[t, s] (int32 and
     float32, tokens x top_k, as moe_route returns them). ``gate``, ``up`` and ``down`` come from
     gemm_pack_weights on the experts' rows one expert after the other, (experts inner) x K and
-    (experts out) x inner; ``a_*`` and ``b_inner`` are laid out likewise. Between the products the
+    (experts out) x inner; ``a_*`` and ``b_inner`` are laid out likewise. Gate's, up and all experts'
+    weights multiply the same activations and share their column scales. Between the products the
     values are quantized to ``inner_fmt`` ("mxfp4" or "mxfp8"). Returns Y (tokens x out, bfloat16, or
     float32 where both formats are "mxfp4"), into ``y`` when given. ``workspace``: a uint8 tensor
     of moe_workspace_bytes bytes, else it is allocated."""

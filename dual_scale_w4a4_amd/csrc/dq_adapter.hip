@@ -5,14 +5,17 @@
 //   u[t][j] = sum_k X[t][k] A_r[j][k],  r = adapter[t]
 //
 // Two launches: u (here), then the products of dq_mlp.hip, whose kernels add the adapters' part to
-// their sums (adapter_blocks and adapter_tile in dq_mlp_kernels.h). Measured, us, u + product (the
-// product without adapters):
-//   32 sequences, 28 of 40 adapters, rank 16, 14336 -> 4096, bf16       8.3 + 14.5   (9.3)
-//   4096 tokens in runs, 6 adapters, rank 64, 4096 -> 14336, bf16      18.5 + 143-150  (114-124)
-//   515 tokens in runs, 5 adapters, rank 24, 2560 -> 1733, fp32         8.5 + 11.8   (7.8)
-// The first reads 13 MB of A next to 31 MB of weights. In the second u is 2 10^9 multiply-adds on
-// 33 MB of X (1.8 TB/s: 256 workgroups, one a CU, each waiting for its own loads), and B's products
-// are 1/64 of the main ones but at a quarter of their rate and with a third more operands.
+// their sums (adapter_blocks and adapter_tile in dq_mlp_kernels.h). Measured by kernel, us, u + product
+// (the product without adapters):
+//   32 sequences, 28 of 40 adapters, rank 16, 14336 -> 4096, bf16       8 - 9 + 15   (9)
+//   the same from MXFP8 activations                                     8 - 9 + 21   (14)
+//   4096 tokens in runs, 6 adapters, rank 64, 4096 -> 14336, bf16       16 - 19 + 141 - 150   (114 - 147)
+//   515 tokens in runs, 5 adapters, rank 24, 2560 -> 1733, fp32         8 - 9 + 12   (8 - 9)
+// The first reads 13 MB of A next to 31 MB of weights. In the second u is 2 10^9 multiply-adds on 33 MB
+// of X: 256 workgroups, of which those of the first slot, every other one and so on four of the eight
+// XCDs, have work where a block of tokens has one adapter; each waits for its own loads (1.8 - 2.1
+// TB/s). B's products are 1/64 of the main ones but at a quarter of their rate and with a third more
+// operands.
 #include "../../include/dq_layer.h"
 #include "dq_mlp_kernels.h"
 
@@ -175,8 +178,10 @@ constexpr int kMaxRank = 256;
 
 // How the rank values' kernel fills the chip: 32 rank values and eight waves a workgroup with few
 // blocks of tokens, 64 and four with many (4096 tokens, K 4096: rank 64 17.7 against 20.0 us, rank 128
-// 25.1 against 32.4); slots up to the distinct adapters that a block can have; and with one block of
-// tokens k in slices (at least 512 each).
+// 25.1 against 32.4); slots up to the distinct adapters that a block can have (a slot that finds none
+// leaves); and with one block of tokens k in slices (at least 512 each). More blocks have fewer, longer
+// workgroups: rank 16, 40 adapters, K 14336, 32 tokens 8.6 us (256 workgroups), 33 and 64 tokens 18.6
+// (64), 128 tokens 19.0 (128).
 struct RankShape {
   int mr, slots, slices;
   size_t bytes;

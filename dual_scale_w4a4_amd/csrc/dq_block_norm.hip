@@ -10,9 +10,13 @@
 //
 // Memory bounds it: every array moves once, and the rest is kept below that (exact bf16 squares in
 // fp32, roots by Newton steps, packed stores: with fp64 conversions, square roots and quotients
-// 8192 x 4096 took 66 us). 8192 x 4096 bf16 with post norm, gate and x_out to MXFP8: 54 - 55 us for
-// 303 MB, 5.5 TB/s. 1003 x 8160 fp32 with a token gate to MXFP8: 22 us for 107 MB, 4.8 TB/s. One
-// token of 4096: 4.2 us.
+// 8192 x 4096 took 66 us). 8192 x 4096 bf16 with post norm, gate and x_out to MXFP8: 54 - 56 us for
+// 303 MB, 5.4 - 5.5 TB/s. 1003 x 8160 fp32 with a token gate to MXFP8: 22 us for 107 MB, 4.8 TB/s. One
+// token of 4096: 4.2 us. The other formats at 8192 x 4096 in bf16: MXFP4 52 us, MXINT4 53, INT4 56, NVFP4
+// 81, whose quantizer does not fit the registers (13 spilled; in fp32 71, and 155 us against 117).
+// 8192 rows of other widths, as the first, TB/s in bf16 and fp32: 1024 channels 2.8 and 4.2, 2048 4.3 and
+// 5.4, 2880 5.0 and 4.3, 5120 4.5 and 4.6, 8192 5.3 and 5.1, 12288 5.3 and 5.3: where a workgroup has fewer
+// waves than its LDS is laid out for, fewer loads are in flight (below).
 #include <limits.h>
 
 #include "../../include/dq_layer.h"
@@ -131,7 +135,10 @@ __device__ __forceinline__ bool norm16(float (&h)[kNormEpl], float r2, const flo
 // read and written once: X of the next row is loaded before the first of the row's two sums, its
 // residual before the second. post and w stay in registers. gate and b lie in LDS, 16 values that
 // each thread writes and reads alone: with all four in registers 128 of them do not suffice (100
-// spilled), and sixteen waves a CU are needed to cover the loads.
+// spilled), and sixteen waves a CU, which 128 registers allow, cover the loads best. That LDS is laid
+// out for NW waves whatever the workgroup has, and there without gate and b too: four workgroups of up to
+// 4 waves fit a CU, two of up to 8 and one of up to 16, so that rows up to 1024 channels have 4 waves a CU,
+// up to 2048 8 and those of 5 waves (up to 5120) 10.
 template <int FMT, int G, bool BF, int NW>
 __global__ __launch_bounds__(NW * kWave, 4) void k_block_norm(BlockNormArgs p) {
   __shared__ double red[2][NW];
@@ -286,7 +293,9 @@ static hipError_t block_norm_launch(const BlockNormArgs& p, hipStream_t s) {
     return hipGetLastError();
   }
   const int waves = (int)((p.n + kWave * kNormEpl - 1) / (kWave * kNormEpl));
-  const int64_t most = 256 * (16 / waves);  // sixteen waves per CU
+  // sixteen waves a CU; what does not fit beside each other by its LDS follows (workgroups of 1, 2, 3 and 5
+  // waves)
+  const int64_t most = 256 * (16 / waves);
   const dim3 grid((unsigned)(p.m < most ? p.m : most)), block(waves * kWave);
   if (waves <= 4)
     hipLaunchKernelGGL((k_block_norm<FMT, G, BF, 4>), grid, block, 0, s, p);

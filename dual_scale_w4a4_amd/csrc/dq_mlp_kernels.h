@@ -453,7 +453,11 @@ constexpr bool kAdapters = std::is_same<X, Adapters>::value;
 
 // Where a sum's truncation would be seen: a value near a border of the quantizer changes its code, so
 // that an error of 10^-4 of a sum becomes one of 6 10^-3 of what the codes are multiplied into (K 4096,
-// outlier channels). The dense gated product (dq_mlp.h) documents that instead.
+// outlier channels). The dense gated product (dq_mlp.h) documents that instead. No code follows the down
+// product: its truncated sums are off by 4.4 - 5.0 10^-5 (root mean square, relative) where whole ones are by
+// 10^-7, next to 1.6 10^-3 by the rounding to bf16, the one type of Y here; whole they took, us in all
+// against truncated: 24 tokens, 8 of 64 experts 4096 -> 1536 123 / 117; 700 tokens, 4 of 32 131 / 120; 3000
+// tokens, 8 of 64, 2048 -> 1024 273 / 244; 600 tokens, 2 of 8, 4096 -> 14336 356 / 271.
 template <bool ACT8, int OUT, class X>
 constexpr bool kWhole = ACT8 && OUT >= kOutFp4 && kExperts<X>;
 

@@ -168,7 +168,6 @@ bool moe_sizes(int64_t tokens, int64_t K, int64_t inner, int64_t out, int64_t ex
 //   experts, top k, K -> inner, tokens (mean rows)   split, 32 rows   tiles of 64             of 128
 //   64, 8, 2048 -> 1024, 32 (4)                      63 in all        51 in all
 //   64, 8, 4096 -> 1536, 24 (3)                      119 in all       114 in all
-//   8, 2, 4096 -> 14336, 16 (4)                      126 in all       136 in all
 //   64, 8, 4096 -> 1536, 40 (5)                      79 + 58          72 (828) + 46 (1104)
 //   64, 8, 2048 -> 1024, 60 (7)                      40 + 31          31 (568) + 21 (568)
 //   8, 2, 4096 -> 4096, 32 (8)                       29 + 17          30 (288) + 30 (144)
@@ -189,6 +188,20 @@ bool moe_sizes(int64_t tokens, int64_t K, int64_t inner, int64_t out, int64_t ex
 //   4, 2, 4096 -> 4096, 300 (150)                    73               58 (416)                70
 //   8, 2, 4096 -> 14336, 600 (150)                   457              295 (2912)              352
 //   64, 8, 2048 -> 1024, 3000 (375)                  342              210 (3512)              201
+// Both products, by the kernel of each (* the rule's):
+//   gated, down:                                     split, split  tiles, split  split, tiles  tiles, tiles
+//   8, 2, 4096 -> 14336, 12 (3)                      121           131 *         170           180
+//   8, 2, 4096 -> 14336, 32 (8)                      139           143 *         183           187
+//   16, 2, 4096 -> 6144, 32 (4)                      109           113 *         116           119
+//   32, 4, 4096 -> 1536, 64 (8)                      80            84            72            76 *
+//   64, 8, 4096 -> 1536, 40 (5)                      144           140           131           126 *
+//   64, 8, 2048 -> 1024, 60 (7)                      74            66            65            57 *
+//   MXFP8: 8, 2, 4096 -> 14336, 12 (3)               125           147 *         173           195
+//   64, 8, 4096 -> 1536, 24 (3)                      128           150           120           141 *
+//   64, 8, 2048 -> 1024, 60 (7)                      76            69            66            59 *
+// The rule goes by the mean of even routing and by the tiles. It does not know K: at K 4096 few rows of
+// few or of MXFP8 activations' experts would be up to 18% faster with split gated products, which lose
+// about as much at K 2048.
 template <bool ACT8, bool GATED, int OUT>
 hipError_t launch_experts(const MlpArgs& p, Experts x, hipStream_t s) {
   constexpr int kRows = GATED ? 128 : 256;

@@ -121,8 +121,11 @@ dq_status dq_moe_route(const void* X, dq_dtype xt, int64_t tokens, int64_t cols,
  * products as dq_gated_mx_quantized and dq_gemm_mx_epilogue compute them, except that MXFP8
  * activations are multiplied in two parts (codes of at least 4, and the others), which leaves the
  * gate's and up products whole: truncated sums would change codes near a border (up to 6 10^-3 of Y).
+ * The down product of MXFP8 codes q is truncated as dq_gemm_mx_epilogue's (about 5 10^-5 of Y).
  * The sum over s in fp32 in ascending order, residual last, one rounding to Y's type.
- *  act_codes, act_scales, act_fmt, K: the activations, as for dq_gated_mx.
+ *  act_codes, act_scales, act_fmt, K: the activations, as for dq_gated_mx. Gate's, up and all experts'
+ *                weights multiply the same x^, so they share one set of column scales b; only the
+ *                down products' are each expert's own (b_inner).
  *  ids:          tokens x top_k experts (4-byte aligned), in any order; a value outside
  *                0 .. experts - 1 contributes nothing; an expert named twice counts twice.
  *  weights:      tokens x top_k floats (4-byte aligned).   1 <= top_k <= 32.
